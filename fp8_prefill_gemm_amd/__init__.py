@@ -61,6 +61,20 @@ _SIGS = {
     "rz_route_kquant_gemv": (_i32, [_u32]),
     "rz_kquant_weight_scale": (_i32, [_i32, _vp, _u32, _u32, _vp, _vp, _vp, _vp, _vp]),
     "rz_kquant_fp8_gemm": (_i32, [_vp, _u32, _vp, _i32, _vp, _u32, _u32, _f32, _f32, _vp, _vp]),
+    "rz_mxfp4_pad_rows": (_u32, [_u32]),
+    "rz_mxfp4_code_bytes": (ctypes.c_size_t, [_u32, _u32]),
+    "rz_mxfp4_scale_bytes": (ctypes.c_size_t, [_u32, _u32]),
+    "rz_mxfp4_quant": (_i32, [_vp, _u32, _u32, _vp, _vp, _vp]),
+    "rz_mxfp4_pack_weight": (_i32, [_i32, _vp, _u32, _u32, _vp, _vp, _vp]),
+    "rz_mxfp4_dequant": (_i32, [_vp, _vp, _u32, _u32, _i32, _vp, _vp]),
+    "rz_mxfp4_gemm": (_i32, [_vp, _vp, _u32, _vp, _vp, _u32, _u32, _vp, _vp]),
+    "rz_mxfp4_gated": (_i32, [_vp, _vp, _u32, _vp, _vp, _vp, _vp, _u32, _u32, _vp, _vp]),
+    "rz_mxfp4_gated_quant": (_i32, [_vp, _vp, _u32, _vp, _vp, _vp, _vp, _u32, _u32, _vp, _vp, _vp]),
+    "rz_mxfp4_gemv": (_i32, [_vp, _vp, _u32, _u32, _vp, _u32, _vp, _vp]),
+    "rz_mxfp4_gated_gemv": (_i32, [_vp, _vp, _vp, _vp, _u32, _u32, _vp, _u32, _vp, _vp]),
+    "rz_kv_cache_write": (_i32, [_i32, _vp, _vp, _u32, _u32, _u32, _u64, _u64, _vp, _u64, _vp, _vp, _vp, _vp, _vp]),
+    "rz_kv_cache_read": (_i32, [_i32, _vp, _vp, _vp, _vp, _u64, _u32, _u32, _u32, _vp, _u32, _u32, _vp, _u32, _i32,
+                                _vp, _vp, _vp]),
     "rz_status_string": (ctypes.c_char_p, [_i32]),
     "rz_last_error_string": (ctypes.c_char_p, []),
     "rz_version": (ctypes.c_char_p, []),
@@ -429,6 +443,282 @@ def rz_fp16_gemm(a_f16, w_f16, m: int, y=None, stream=None):
         y = _empty((m, n), torch.float32, w_f16.device, stream)
     _check(lib().rz_fp16_gemm(_ptr(a_f16), _ptr(w_f16), m, n, k, _ptr(y), _stream(stream, w_f16.device)))
     return y
+
+
+# MXFP4 tensors are pairs (codes, scales) of uint8 tensors in the tiled layout
+# of include/rz_fp8.h: codes [rows/32][k/64][1024], scales [rows/32][k/256][256].
+
+def rz_mxfp4_pad_rows(rows: int) -> int:
+    return (rows + 31) // 32 * 32
+
+
+def _need(t, what, dtype, shape=None):
+    """Raise unless t is a contiguous tensor of this dtype (and shape)."""
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor" + (f" of shape {tuple(shape)}" if shape is not None else "")
+                         + f", got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"rz_fp8: tensors on {t.device} and {dev}: one device expected")
+
+
+def _out(shape, dtype, dev, stream):
+    """A new output on the call's stream (see _empty)."""
+    return _torch().empty(shape, dtype=dtype, device=dev) if stream is None else _empty(shape, dtype, dev, stream)
+
+
+def _run_on(dev, stream, fn, *args):
+    """Call entry point `fn` with `args` and the stream, on device `dev`."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, _stream(stream, dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream, dev)))
+
+
+def _mx(codes, scales, rows, what):
+    """k of the MXFP4 tensor (codes, scales) of `rows` rows, its shapes checked."""
+    torch = _torch()
+    g = (rows + 31) // 32
+    if codes.dim() != 3:
+        raise ValueError(f"{what} codes: expected shape [rows/32][k/64][1024], got {tuple(codes.shape)}")
+    k = codes.shape[1] * 64
+    _need(codes, f"{what} codes", torch.uint8, (g, k // 64, 1024))
+    _need(scales, f"{what} scales", torch.uint8, (g, k // 256, 256))
+    return k
+
+
+def _mx_out(rows, k, codes, scales, dev, stream, what="output"):
+    torch = _torch()
+    g = (rows + 31) // 32
+    if codes is None:
+        codes = _out((g, k // 64, 1024), torch.uint8, dev, stream)
+    else:
+        _need(codes, f"{what} codes", torch.uint8, (g, k // 64, 1024))
+    if scales is None:
+        scales = _out((g, k // 256, 256), torch.uint8, dev, stream)
+    else:
+        _need(scales, f"{what} scales", torch.uint8, (g, k // 256, 256))
+    return codes, scales
+
+
+def _f32_out(t, what, shape, dev, stream):
+    torch = _torch()
+    if t is None:
+        return _out(shape, torch.float32, dev, stream)
+    _need(t, what, torch.float32, shape)
+    return t
+
+
+def rz_mxfp4_quant(x, codes=None, scales=None, stream=None):
+    """x fp32 [m][k] -> MXFP4 (codes, scales), pad rows included."""
+    _require_cuda(x, codes, scales)
+    _need(x, "x", _torch().float32)
+    m, k = x.shape
+    dev = x.device
+    codes, scales = _mx_out(m, k, codes, scales, dev, stream)
+    _same_device(dev, codes, scales)
+    _run_on(dev, stream, lib().rz_mxfp4_quant, _ptr(x), m, k, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def rz_mxfp4_pack_weight(qtype: int, blocks, n: int, k: int, codes=None, scales=None, stream=None):
+    """A K-quant weight -> MXFP4 (codes, scales)."""
+    _require_cuda(blocks, codes, scales)
+    _need(blocks, "blocks", _torch().uint8)
+    if blocks.numel() < rz_weight_bytes(qtype, n, k):
+        raise ValueError(f"blocks: {blocks.numel()} bytes, {rz_weight_bytes(qtype, n, k)} needed")
+    dev = blocks.device
+    codes, scales = _mx_out(n, k, codes, scales, dev, stream)
+    _same_device(dev, codes, scales)
+    _run_on(dev, stream, lib().rz_mxfp4_pack_weight, qtype, _ptr(blocks), n, k, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def _dtype_id(dtype):
+    torch = _torch()
+    ids = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    if dtype not in ids:
+        raise ValueError(f"dtype: expected float32, float16 or bfloat16, got {dtype}")
+    return ids[dtype]
+
+
+def rz_mxfp4_dequant(codes, scales, rows: int, out=None, dtype=None, stream=None):
+    """MXFP4 -> out [rows][k] of dtype (default: out's, or float32)."""
+    _require_cuda(codes, scales, out)
+    k = _mx(codes, scales, rows, "input")
+    dev = codes.device
+    if dtype is None:
+        dtype = _torch().float32 if out is None else out.dtype
+    did = _dtype_id(dtype)
+    if out is None:
+        out = _out((rows, k), dtype, dev, stream)
+    else:
+        _need(out, "out", dtype, (rows, k))
+    _same_device(dev, scales, out)
+    _run_on(dev, stream, lib().rz_mxfp4_dequant, _ptr(codes), _ptr(scales), rows, k, did, _ptr(out))
+    return out
+
+
+def rz_mxfp4_gemm(a_codes, a_scales, m: int, w_codes, w_scales, n: int, y=None, stream=None):
+    """-> y fp32 [m][n] = a @ w^T of MXFP4 a [m][k] and w [n][k]."""
+    _require_cuda(a_codes, a_scales, w_codes, w_scales, y)
+    k = _mx(a_codes, a_scales, m, "a")
+    if _mx(w_codes, w_scales, n, "w") != k:
+        raise ValueError(f"a has k={k}, w has k={w_codes.shape[1] * 64}")
+    dev = a_codes.device
+    y = _f32_out(y, "y", (m, n), dev, stream)
+    _same_device(dev, a_scales, w_codes, w_scales, y)
+    _run_on(dev, stream, lib().rz_mxfp4_gemm, _ptr(a_codes), _ptr(a_scales), m, _ptr(w_codes), _ptr(w_scales), n, k, _ptr(y))
+    return y
+
+
+def _gated_args(a_codes, a_scales, m, gate, up, n):
+    (gc, gs), (uc, us) = gate, up
+    _require_cuda(a_codes, a_scales, gc, gs, uc, us)
+    k = _mx(a_codes, a_scales, m, "a")
+    if _mx(gc, gs, n, "gate") != k or _mx(uc, us, n, "up") != k:
+        raise ValueError(f"a has k={k}, gate has k={gc.shape[1] * 64}, up has k={uc.shape[1] * 64}")
+    _same_device(a_codes.device, a_scales, gc, gs, uc, us)
+    return k, (_ptr(a_codes), _ptr(a_scales), m, _ptr(gc), _ptr(gs), _ptr(uc), _ptr(us), n, k)
+
+
+def rz_mxfp4_gated(a_codes, a_scales, m: int, gate, up, n: int, h=None, stream=None):
+    """-> h fp32 [m][n] = silu(a @ gate^T) * (a @ up^T); gate and up are
+    MXFP4 (codes, scales) pairs of [n][k]."""
+    k, args = _gated_args(a_codes, a_scales, m, gate, up, n)
+    dev = a_codes.device
+    _require_cuda(h)
+    h = _f32_out(h, "h", (m, n), dev, stream)
+    _same_device(dev, h)
+    _run_on(dev, stream, lib().rz_mxfp4_gated, *args, _ptr(h))
+    return h
+
+
+def rz_mxfp4_gated_quant(a_codes, a_scales, m: int, gate, up, n: int, h_codes=None, h_scales=None, stream=None):
+    """rz_mxfp4_gated with its result as MXFP4 -> (h_codes, h_scales), the
+    down projection's operand (n a multiple of 256)."""
+    k, args = _gated_args(a_codes, a_scales, m, gate, up, n)
+    dev = a_codes.device
+    _require_cuda(h_codes, h_scales)
+    h_codes, h_scales = _mx_out(m, n, h_codes, h_scales, dev, stream, "h")
+    _same_device(dev, h_codes, h_scales)
+    _run_on(dev, stream, lib().rz_mxfp4_gated_quant, *args, _ptr(h_codes), _ptr(h_scales))
+    return h_codes, h_scales
+
+
+MXFP4_GEMV_MAX_M = 8
+
+
+def rz_mxfp4_gemv(w_codes, w_scales, n: int, x, y=None, stream=None):
+    """-> y fp32 [m][n] = x @ w^T, x fp32 [m][k] with m <= MXFP4_GEMV_MAX_M."""
+    _require_cuda(w_codes, w_scales, x, y)
+    k = _mx(w_codes, w_scales, n, "w")
+    m = x.shape[0]
+    _need(x, "x", _torch().float32, (m, k))
+    dev = x.device
+    y = _f32_out(y, "y", (m, n), dev, stream)
+    _same_device(dev, w_codes, w_scales, y)
+    _run_on(dev, stream, lib().rz_mxfp4_gemv, _ptr(w_codes), _ptr(w_scales), n, k, _ptr(x), m, _ptr(y))
+    return y
+
+
+def rz_mxfp4_gated_gemv(gate, up, n: int, x, h=None, stream=None):
+    """-> h fp32 [m][n] = silu(x @ gate^T) * (x @ up^T), x fp32 [m][k] with
+    m <= MXFP4_GEMV_MAX_M."""
+    (gc, gs), (uc, us) = gate, up
+    _require_cuda(gc, gs, uc, us, x, h)
+    k = _mx(gc, gs, n, "gate")
+    if _mx(uc, us, n, "up") != k:
+        raise ValueError(f"gate has k={k}, up has k={uc.shape[1] * 64}")
+    m = x.shape[0]
+    _need(x, "x", _torch().float32, (m, k))
+    dev = x.device
+    h = _f32_out(h, "h", (m, n), dev, stream)
+    _same_device(dev, gc, gs, uc, us, h)
+    _run_on(dev, stream, lib().rz_mxfp4_gated_gemv, _ptr(gc), _ptr(gs), _ptr(uc), _ptr(us), n, k, _ptr(x), m, _ptr(h))
+    return h
+
+
+KV_E4M3, KV_MXFP4 = 0, 1
+
+
+def _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales):
+    """(num_slots, heads, dim) of a cache, its tensors checked."""
+    torch = _torch()
+    if fmt not in (KV_E4M3, KV_MXFP4):
+        raise ValueError(f"fmt: expected KV_E4M3 or KV_MXFP4, got {fmt}")
+    if k_codes.dim() != 3:
+        raise ValueError(f"k_codes: expected 3 dimensions, got {tuple(k_codes.shape)}")
+    slots, heads, width = k_codes.shape
+    dim = width if fmt == KV_E4M3 else 2 * width
+    sdtype, sshape = (torch.float32, (slots, heads)) if fmt == KV_E4M3 else (torch.uint8, (slots, heads, dim // 32))
+    for c, s, what in ((k_codes, k_scales, "k"), (v_codes, v_scales, "v")):
+        _need(c, f"{what}_codes", torch.uint8, (slots, heads, width))
+        _need(s, f"{what}_scales", sdtype, sshape)
+    _same_device(k_codes.device, k_scales, v_codes, v_scales)
+    return slots, heads, dim
+
+
+def rz_kv_cache_write(fmt: int, k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
+    """Quantise k and v, fp32 [tokens][heads][dim] (tokens may be strided),
+    into the cache rows `slots` (int64 [tokens]; out of range: dropped)."""
+    torch = _torch()
+    _require_cuda(k, v, slots, k_codes, k_scales, v_codes, v_scales)
+    num_slots, heads, dim = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
+    tokens = k.shape[0]
+    for t, what in ((k, "k"), (v, "v")):
+        if t.dtype is not torch.float32 or t.shape != (tokens, heads, dim) or (
+                tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
+            raise ValueError(f"{what}: expected float32 [{tokens}][{heads}][{dim}] with contiguous tokens, got {t.dtype} "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+    _need(slots, "slots", torch.int64, (tokens,))
+    dev = k.device
+    _same_device(dev, v, slots, k_codes)
+    # the token stride is free where there is one token
+    ks, vs = (k.stride(0), v.stride(0)) if tokens > 1 else (heads * dim, heads * dim)
+    _run_on(dev, stream, lib().rz_kv_cache_write, fmt, _ptr(k), _ptr(v), tokens, heads, dim, ks, vs, _ptr(slots), num_slots,
+            _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales))
+
+
+def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: int, page_table, offsets, rows: int,
+                     k_out=None, v_out=None, dtype=None, stream=None):
+    """Read sequences back from the paged cache -> (k_out, v_out), each
+    [rows][heads][dim] of dtype (default: the outputs', or float32).
+    page_table int32 [seqs][max_pages]; offsets int32 [seqs + 1]: sequence b
+    is rows offsets[b] .. offsets[b+1] - 1.  Rows of no sequence are left as
+    they are (undefined in a new output)."""
+    torch = _torch()
+    _require_cuda(k_codes, k_scales, v_codes, v_scales, page_table, offsets, k_out, v_out)
+    num_slots, heads, dim = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected 2 dimensions, got {tuple(page_table.shape)}")
+    seqs, max_pages = page_table.shape
+    _need(page_table, "page_table", torch.int32)
+    _need(offsets, "offsets", torch.int32, (seqs + 1,))
+    if page_len < 1 or rows < 0:
+        raise ValueError(f"page_len={page_len} must be positive and rows={rows} not negative")
+    dev = k_codes.device
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.float32
+    did = _dtype_id(dtype)
+    shape = (rows, heads, dim)
+    if k_out is None:
+        k_out = _out(shape, dtype, dev, stream)
+    else:
+        _need(k_out, "k_out", dtype, shape)
+    if v_out is None:
+        v_out = _out(shape, dtype, dev, stream)
+    else:
+        _need(v_out, "v_out", dtype, shape)
+    _same_device(dev, page_table, offsets, k_out, v_out)
+    _run_on(dev, stream, lib().rz_kv_cache_read, fmt, _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), num_slots,
+            heads, dim, page_len, _ptr(page_table), seqs, max_pages, _ptr(offsets), rows, did, _ptr(k_out), _ptr(v_out))
+    return k_out, v_out
 
 
 def rz_dequant_f32(qtype: int, blocks, n: int, k: int, out=None, stream=None):

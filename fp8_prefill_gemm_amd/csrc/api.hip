@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <chrono>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -84,6 +85,38 @@ int device_cus() {
 int check_k(const char* fn, uint32_t k) {
     if (k == 0 || (k % 256u) != 0)
         return fail(RZ_ERR_SHAPE, "%s: k=%u must be a positive multiple of 256", fn, k);
+    return RZ_OK;
+}
+
+// The MXFP4 products' shared checks: dimensions (m is 0 for a weight alone)
+// and the alignment of every tensor pointer.
+int check_mx(const char* fn, uint32_t m, uint32_t n, uint32_t k, std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (!p) return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if (m > 0x7FFFFFE0u || n > RZ_MAX_GEMM_K) return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    if ((uint64_t)rz::mx_pad_rows(n) * k > RZ_MAX_ELEMS || (uint64_t)rz::mx_pad_rows(m) * k > RZ_MAX_ELEMS ||
+        (uint64_t)rz::mx_pad_rows(m) * n > RZ_MAX_ELEMS)
+        return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(RZ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned", fn);
+    return RZ_OK;
+}
+
+// k as every product's K: a positive multiple of 256, at most RZ_MAX_GEMM_K.
+int check_mx_k(const char* fn, uint32_t k) {
+    if (int r = check_k(fn, k)) return r;
+    if (k > RZ_MAX_GEMM_K) return fail(RZ_ERR_SHAPE, "%s: k=%u exceeds %u", fn, k, (unsigned)RZ_MAX_GEMM_K);
+    return RZ_OK;
+}
+
+int check_kv(const char* fn, int format, uint32_t heads, uint32_t dim, uint64_t num_slots) {
+    if (format != RZ_KV_E4M3 && format != RZ_KV_MXFP4) return fail(RZ_ERR_VALUE, "%s: unknown cache format %d", fn, format);
+    if (heads == 0 || dim == 0 || dim % 32u != 0 || dim > RZ_KV_MAX_DIM)
+        return fail(RZ_ERR_SHAPE, "%s: heads=%u must be positive and dim=%u a positive multiple of 32, at most %u", fn,
+                    heads, dim, (unsigned)RZ_KV_MAX_DIM);
+    // a token's offsets, and the heads of a workgroup's tokens, count in 32 bits
+    if ((uint64_t)heads * dim > (1u << 26) || num_slots > RZ_MAX_ELEMS / ((uint64_t)heads * dim))
+        return fail(RZ_ERR_SHAPE, "%s: cache too large", fn);
     return RZ_OK;
 }
 
@@ -594,6 +627,165 @@ int rz_kquant_gemv(int qtype, const void* blocks, uint32_t n, uint32_t k, const 
     if (int r = check_device(fn)) return r;
     hipError_t e = rz::launch_kquant_gemv(qtype, static_cast<const uint8_t*>(blocks), n, k, x, m, y,
                                           as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+uint32_t rz_mxfp4_pad_rows(uint32_t rows) { return rz::mx_pad_rows(rows); }
+
+size_t rz_mxfp4_code_bytes(uint32_t rows, uint32_t k) {
+    return k % 256u != 0 ? 0 : (size_t)rz::mx_pad_rows(rows) * (k / 2u);
+}
+
+size_t rz_mxfp4_scale_bytes(uint32_t rows, uint32_t k) {
+    return k % 256u != 0 ? 0 : (size_t)rz::mx_pad_rows(rows) * (k / 32u);
+}
+
+int rz_mxfp4_quant(const float* x, uint32_t m, uint32_t k, uint8_t* codes, uint8_t* scales, void* stream) {
+    static const char* fn = "rz_mxfp4_quant";
+    if (int r = check_mx_k(fn, k)) return r;
+    if (m == 0) return RZ_OK;  // nothing to read or write
+    if (int r = check_mx(fn, m, 0, k, {x, codes, scales})) return r;
+    if (int r = check_device(fn)) return r;
+    hipError_t e = rz::launch_mx_quant(x, m, k, codes, scales, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_mxfp4_pack_weight(int qtype, const void* blocks, uint32_t n, uint32_t k, uint8_t* codes, uint8_t* scales,
+                         void* stream) {
+    static const char* fn = "rz_mxfp4_pack_weight";
+    if (!blocks || !codes || !scales) return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if (!qtype_ok(qtype)) return fail(RZ_ERR_QTYPE, "%s: unsupported qtype %d", fn, qtype);
+    if (int r = check_mx_k(fn, k)) return r;
+    if (n == 0) return fail(RZ_ERR_SHAPE, "%s: n must be positive", fn);
+    if (int r = check_mx(fn, 0, n, k, {blocks, codes, scales})) return r;
+    if (int r = check_device(fn)) return r;
+    hipError_t e = rz::launch_mx_pack(qtype, static_cast<const uint8_t*>(blocks), n, k, codes, scales, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, uint32_t rows, uint32_t k, int dtype, void* out,
+                     void* stream) {
+    static const char* fn = "rz_mxfp4_dequant";
+    if (int r = check_mx_k(fn, k)) return r;
+    if (dtype != RZ_F32 && dtype != RZ_F16 && dtype != RZ_BF16) return fail(RZ_ERR_VALUE, "%s: unknown dtype %d", fn, dtype);
+    if (rows == 0) return RZ_OK;  // nothing to read or write
+    if (int r = check_mx(fn, rows, 0, k, {codes, scales, out})) return r;
+    if (int r = check_device(fn)) return r;
+    hipError_t e = rz::launch_mx_dequant(codes, scales, rows, k, dtype, out, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* w_codes,
+                  const uint8_t* w_scales, uint32_t n, uint32_t k, float* y, void* stream) {
+    static const char* fn = "rz_mxfp4_gemm";
+    if (int r = check_mx_k(fn, k)) return r;
+    if (m == 0 || n == 0) return RZ_OK;  // empty product: nothing to read or write
+    if (int r = check_mx(fn, m, n, k, {a_codes, a_scales, w_codes, w_scales, y})) return r;
+    if (int r = check_device(fn)) return r;
+    const rz::MxWeights W = {{w_codes, nullptr}, {w_scales, nullptr}};
+    hipError_t e = rz::launch_mx_gemm(a_codes, a_scales, m, W, false, n, k, y, nullptr, nullptr, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_mxfp4_gated(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* gate_codes,
+                   const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales, uint32_t n, uint32_t k,
+                   float* h, void* stream) {
+    static const char* fn = "rz_mxfp4_gated";
+    if (int r = check_mx_k(fn, k)) return r;
+    if (m == 0 || n == 0) return RZ_OK;  // empty product: nothing to read or write
+    if (int r = check_mx(fn, m, n, k, {a_codes, a_scales, gate_codes, gate_scales, up_codes, up_scales, h})) return r;
+    if (int r = check_device(fn)) return r;
+    const rz::MxWeights W = {{gate_codes, up_codes}, {gate_scales, up_scales}};
+    hipError_t e = rz::launch_mx_gemm(a_codes, a_scales, m, W, true, n, k, h, nullptr, nullptr, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_mxfp4_gated_quant(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* gate_codes,
+                         const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales, uint32_t n,
+                         uint32_t k, uint8_t* h_codes, uint8_t* h_scales, void* stream) {
+    static const char* fn = "rz_mxfp4_gated_quant";
+    if (int r = check_mx_k(fn, k)) return r;
+    if (n % 256u != 0) return fail(RZ_ERR_SHAPE, "%s: n=%u must be a multiple of 256", fn, n);
+    if (m == 0 || n == 0) return RZ_OK;  // empty product: nothing to read or write
+    if (int r = check_mx(fn, m, n, k,
+                         {a_codes, a_scales, gate_codes, gate_scales, up_codes, up_scales, h_codes, h_scales}))
+        return r;
+    if (int r = check_device(fn)) return r;
+    const rz::MxWeights W = {{gate_codes, up_codes}, {gate_scales, up_scales}};
+    hipError_t e = rz::launch_mx_gemm(a_codes, a_scales, m, W, true, n, k, nullptr, h_codes, h_scales, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_mxfp4_gemv(const uint8_t* w_codes, const uint8_t* w_scales, uint32_t n, uint32_t k, const float* x, uint32_t m,
+                  float* y, void* stream) {
+    static const char* fn = "rz_mxfp4_gemv";
+    if (int r = check_mx_k(fn, k)) return r;
+    if (m > RZ_MXFP4_GEMV_MAX_M) return fail(RZ_ERR_SHAPE, "%s: m=%u exceeds %u", fn, m, (unsigned)RZ_MXFP4_GEMV_MAX_M);
+    if (m == 0 || n == 0) return RZ_OK;  // empty product: nothing to read or write
+    if (int r = check_mx(fn, m, n, k, {w_codes, w_scales, x, y})) return r;
+    if (int r = check_device(fn)) return r;
+    const rz::MxWeights W = {{w_codes, nullptr}, {w_scales, nullptr}};
+    hipError_t e = rz::launch_mx_gemv(W, false, n, k, x, m, y, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_mxfp4_gated_gemv(const uint8_t* gate_codes, const uint8_t* gate_scales, const uint8_t* up_codes,
+                        const uint8_t* up_scales, uint32_t n, uint32_t k, const float* x, uint32_t m, float* h,
+                        void* stream) {
+    static const char* fn = "rz_mxfp4_gated_gemv";
+    if (int r = check_mx_k(fn, k)) return r;
+    if (m > RZ_MXFP4_GEMV_MAX_M) return fail(RZ_ERR_SHAPE, "%s: m=%u exceeds %u", fn, m, (unsigned)RZ_MXFP4_GEMV_MAX_M);
+    if (m == 0 || n == 0) return RZ_OK;  // empty product: nothing to read or write
+    if (int r = check_mx(fn, m, n, k, {gate_codes, gate_scales, up_codes, up_scales, x, h})) return r;
+    if (int r = check_device(fn)) return r;
+    const rz::MxWeights W = {{gate_codes, up_codes}, {gate_scales, up_scales}};
+    hipError_t e = rz::launch_mx_gemv(W, true, n, k, x, m, h, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_kv_cache_write(int format, const float* k, const float* v, uint32_t tokens, uint32_t heads, uint32_t dim,
+                      uint64_t k_stride, uint64_t v_stride, const int64_t* slots, uint64_t num_slots, uint8_t* k_codes,
+                      void* k_scales, uint8_t* v_codes, void* v_scales, void* stream) {
+    static const char* fn = "rz_kv_cache_write";
+    if (int r = check_kv(fn, format, heads, dim, num_slots)) return r;
+    if (tokens == 0) return RZ_OK;  // nothing to read or write
+    if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales)
+        return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    const uint64_t row = (uint64_t)heads * dim;
+    if (tokens > 1 && (k_stride < row || v_stride < row || k_stride % 4u != 0 || v_stride % 4u != 0))
+        return fail(RZ_ERR_SHAPE, "%s: token strides must be multiples of 4, at least heads*dim", fn);
+    if ((uint64_t)tokens * row > RZ_MAX_ELEMS || k_stride > RZ_MAX_ELEMS || v_stride > RZ_MAX_ELEMS)
+        return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) ||
+        !aligned16(v_scales) || ((uintptr_t)slots & 7u))
+        return fail(RZ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned (slots: 8)", fn);
+    if (int r = check_device(fn)) return r;
+    const rz::KvWrite A = {{k, v},    {k_stride, v_stride}, {k_codes, v_codes}, {k_scales, v_scales}, slots,
+                           num_slots, tokens,               heads,              dim};
+    hipError_t e = rz::launch_kv_write(format, A, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_kv_cache_read(int format, const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes,
+                     const void* v_scales, uint64_t num_slots, uint32_t heads, uint32_t dim, uint32_t page_len,
+                     const int32_t* page_table, uint32_t seqs, uint32_t max_pages, const int32_t* offsets, uint32_t rows,
+                     int dtype, void* k_out, void* v_out, void* stream) {
+    static const char* fn = "rz_kv_cache_read";
+    if (int r = check_kv(fn, format, heads, dim, num_slots)) return r;
+    if (dtype != RZ_F32 && dtype != RZ_F16 && dtype != RZ_BF16) return fail(RZ_ERR_VALUE, "%s: unknown dtype %d", fn, dtype);
+    if (page_len == 0) return fail(RZ_ERR_SHAPE, "%s: page_len must be positive", fn);
+    if (rows == 0 || seqs == 0) return RZ_OK;  // nothing to read or write
+    if (!k_codes || !k_scales || !v_codes || !v_scales || (max_pages != 0 && !page_table) || !offsets || !k_out || !v_out)
+        return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if ((uint64_t)rows * heads * dim > RZ_MAX_ELEMS || rows > 0x7FFFFFFFu)
+        return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) || !aligned16(v_scales) || !aligned16(k_out) ||
+        !aligned16(v_out) || (((uintptr_t)page_table | (uintptr_t)offsets) & 3u))
+        return fail(RZ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned (tables: 4)", fn);
+    if (int r = check_device(fn)) return r;
+    const rz::KvRead A = {{k_codes, v_codes}, {k_scales, v_scales}, {k_out, v_out}, page_table, offsets, num_slots,
+                          heads,              dim,                  page_len,       seqs,       max_pages, rows};
+    hipError_t e = rz::launch_kv_read(format, A, dtype, as_stream(stream));
     return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
 }
 

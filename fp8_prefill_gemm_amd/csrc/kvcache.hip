@@ -1,0 +1,197 @@
+// Quantised key/value cache: written from the K and V projections' fp32
+// outputs, read back for attention.
+//
+// A cache row is one head of one token: `dim` values, in one of two formats:
+//   E4M3   the FP8 path's conversion with a row's own absmax a (NaN ignored):
+//          a' = a or 1 when a == 0, codes E4M3(RN(x * RN(448/a'))), scale
+//          RN(a'/448) in fp32; a value reads back as RN(code * scale);
+//   MXFP4  blocks of 32 as in mx_device.h, rows in plain order: codes
+//          [slot][head][dim/2], scale bytes [slot][head][dim/32].
+// Both directions are bound by memory (a decoding step by its launch).  A
+// lane holds eight values, 8..64 lanes a row; keys and values share a launch
+// (grid y).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_device.h"
+#include "rz_device.h"
+#include "rz_internal.h"
+
+namespace rz {
+namespace {
+using namespace mx;
+
+constexpr int kThreads = 256;
+
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)v, off, kWave);
+        v = v > o ? v : o;
+    }
+    return v;
+}
+
+// L lanes a row (a power of two, 8 L >= dim; lanes past dim are idle).
+template <int FMT, int L>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWrite A) {
+    const uint32_t part = threadIdx.x % L;
+    const uint64_t row = (uint64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    if (row >= (uint64_t)A.tokens * A.heads) return;  // whole rows: the shuffles below stay inside a row
+    const uint32_t token = (uint32_t)(row / A.heads), head = (uint32_t)(row % A.heads);
+    const int64_t slot = A.slots[token];
+    if (slot < 0 || (uint64_t)slot >= A.num_slots) return;  // not a slot: this token is not kept
+    const int c = blockIdx.y;
+    const bool live = part * 8u < A.dim;
+    float x[8] = {};
+    if (live) {
+        const float* p = A.x[c] + (uint64_t)token * A.stride[c] + head * A.dim + part * 8u;
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = a[i];
+            x[4 + i] = b[i];
+        }
+    }
+    const uint64_t dst = (uint64_t)slot * A.heads + head;
+    if constexpr (FMT == kKvE4M3) {
+        uint32_t key = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = abs_key(x[i]);
+            key = key > a ? key : a;
+        }
+        const Scales s = scales_from_key(row_max<L>(key));
+        if (live) {
+            u32x2 w;
+            w.x = e4m3_pack4(x[0] * s.q, x[1] * s.q, x[2] * s.q, x[3] * s.q);
+            w.y = e4m3_pack4(x[4] * s.q, x[5] * s.q, x[6] * s.q, x[7] * s.q);
+            *reinterpret_cast<u32x2*>(A.codes[c] + dst * A.dim + part * 8u) = w;
+        }
+        if (part == 0) static_cast<float*>(A.scales[c])[dst] = s.dq;
+    } else {
+        uint32_t byte;
+        const uint32_t w = quantise8(x, byte);
+        if (live) {
+            *reinterpret_cast<uint32_t*>(A.codes[c] + dst * (A.dim / 2u) + part * 4u) = w;
+            if ((part & 3u) == 0) static_cast<uint8_t*>(A.scales[c])[dst * (A.dim / 32u) + part / 4u] = (uint8_t)byte;
+        }
+    }
+}
+
+// A workgroup reads kRows consecutive output rows (tokens): one lane a token
+// finds its sequence (binary search in the offsets) and slot, then the
+// workgroup copies the tokens' heads.
+constexpr int kRows = 32;
+
+template <int FMT, int DT, int L>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead A) {
+    __shared__ int64_t slot_of[kRows];  // -1: zeros, -2: not a row of any sequence
+    const uint32_t row0 = blockIdx.x * kRows;
+    if (threadIdx.x < kRows) {
+        const uint32_t row = row0 + threadIdx.x;
+        int64_t slot = -2;
+        if (row < A.rows && (int64_t)row >= A.offsets[0] && (int64_t)row < A.offsets[A.seqs]) {
+            uint32_t lo = 0, hi = A.seqs;  // offsets[lo] <= row < offsets[hi]
+            while (hi - lo > 1) {
+                const uint32_t mid = (lo + hi) >> 1;
+                if ((int64_t)row >= A.offsets[mid]) lo = mid; else hi = mid;
+            }
+            const uint32_t pos = row - (uint32_t)A.offsets[lo];
+            const uint32_t page = pos / A.page_len;
+            slot = -1;
+            if (page < A.max_pages) {
+                const int32_t id = A.page_table[(uint64_t)lo * A.max_pages + page];
+                const uint64_t s = (uint64_t)(uint32_t)id * A.page_len + pos % A.page_len;
+                if (id >= 0 && s < A.num_slots) slot = (int64_t)s;
+            }
+        }
+        slot_of[threadIdx.x] = slot;
+    }
+    __syncthreads();
+    const int c = blockIdx.y;
+    const uint32_t part = threadIdx.x % L;
+    if (part * 8u >= A.dim) return;
+    for (uint32_t i = threadIdx.x / L; i < kRows * A.heads; i += kThreads / L) {
+        const uint32_t t = i / A.heads, head = i % A.heads;
+        const int64_t slot = slot_of[t];
+        if (slot == -2) continue;
+        float v[8] = {};
+        if (slot >= 0) {
+            const uint64_t src = (uint64_t)slot * A.heads + head;
+            if constexpr (FMT == kKvE4M3) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(A.codes[c] + src * A.dim + part * 8u);
+                const float s = static_cast<const float*>(A.scales[c])[src];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
+                    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+                    v[4 * j] = a.x * s;
+                    v[4 * j + 1] = a.y * s;
+                    v[4 * j + 2] = b.x * s;
+                    v[4 * j + 3] = b.y * s;
+                }
+            } else {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(A.codes[c] + src * (A.dim / 2u) + part * 4u);
+                const uint32_t byte = static_cast<const uint8_t*>(A.scales[c])[src * (A.dim / 32u) + part / 4u];
+                decode8(w, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = times_scale(v[j], byte);
+            }
+        }
+        store8<DT>(A.out[c], ((uint64_t)(row0 + t) * A.heads + head) * A.dim + part * 8u, v);
+    }
+}
+
+template <int FMT, int L>
+void read_as(const KvRead& A, int dtype, dim3 grid, hipStream_t st) {
+    if (dtype == kF32)
+        kv_read_kernel<FMT, kF32, L><<<grid, kThreads, 0, st>>>(A);
+    else if (dtype == kF16)
+        kv_read_kernel<FMT, kF16, L><<<grid, kThreads, 0, st>>>(A);
+    else
+        kv_read_kernel<FMT, kBF16, L><<<grid, kThreads, 0, st>>>(A);
+}
+
+// Calls f(integral_constant<L>) with the fewest lanes that hold dim values.
+template <typename F>
+void with_lanes(uint32_t dim, F&& f) {
+    if (dim <= 64)
+        f(std::integral_constant<int, 8>{});
+    else if (dim <= 128)
+        f(std::integral_constant<int, 16>{});
+    else if (dim <= 256)
+        f(std::integral_constant<int, 32>{});
+    else
+        f(std::integral_constant<int, 64>{});
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(int format, const KvWrite& A, hipStream_t st) {
+    with_lanes(A.dim, [&](auto l) {
+        constexpr int L = decltype(l)::value;
+        const uint64_t rows = (uint64_t)A.tokens * A.heads;
+        const dim3 grid((uint32_t)((rows + kThreads / L - 1) / (kThreads / L)), 2);
+        if (format == kKvE4M3)
+            kv_write_kernel<kKvE4M3, L><<<grid, kThreads, 0, st>>>(A);
+        else
+            kv_write_kernel<kKvMXFP4, L><<<grid, kThreads, 0, st>>>(A);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_read(int format, const KvRead& A, int dtype, hipStream_t st) {
+    with_lanes(A.dim, [&](auto l) {
+        constexpr int L = decltype(l)::value;
+        const dim3 grid((A.rows + kRows - 1) / kRows, 2);
+        if (format == kKvE4M3)
+            read_as<kKvE4M3, L>(A, dtype, grid, st);
+        else
+            read_as<kKvMXFP4, L>(A, dtype, grid, st);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace rz

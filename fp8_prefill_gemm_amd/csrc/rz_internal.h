@@ -106,4 +106,56 @@ hipError_t launch_q8_q4k_gemm(const uint8_t* q8, uint32_t m, const uint8_t* bloc
 hipError_t launch_kquant_gemv(int qtype, const uint8_t* blocks, uint32_t n, uint32_t k, const float* x,
                               uint32_t m, float* y, hipStream_t st);
 
+// Rows of a tiled MXFP4 tensor's buffers.
+inline uint32_t mx_pad_rows(uint32_t rows) { return (rows + 31u) & ~31u; }
+
+// ---- mxquant.hip (tiled MXFP4, see mx_device.h; k a multiple of 256)
+hipError_t launch_mx_quant(const float* x, uint32_t m, uint32_t k, uint8_t* codes, uint8_t* scales, hipStream_t st);
+hipError_t launch_mx_pack(int qtype, const uint8_t* blocks, uint32_t n, uint32_t k, uint8_t* codes, uint8_t* scales,
+                          hipStream_t st);
+// out [m][k] row-major; dtype: rz_dtype.
+hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, uint32_t m, uint32_t k, int dtype, void* out,
+                             hipStream_t st);
+
+// The weights of a product: one, or the gate and the up weight of a gated one.
+struct MxWeights {
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
+};
+
+// ---- mxgemm.hip
+// y fp32 [m][n] = a w^T, or silu(a wg^T) * (a wu^T) when gated; a tiled MXFP4.
+// With h_codes (gated, n a multiple of 256) the result goes to h_codes and
+// h_scales as tiled MXFP4 instead of y.
+hipError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const MxWeights& W, bool gated,
+                          uint32_t n, uint32_t k, float* y, uint8_t* h_codes, uint8_t* h_scales, hipStream_t st);
+
+// ---- mxgemv.hip
+// The same products from an fp32 x [m][k], 1 <= m <= RZ_MXFP4_GEMV_MAX_M.
+hipError_t launch_mx_gemv(const MxWeights& W, bool gated, uint32_t n, uint32_t k, const float* x, uint32_t m, float* y,
+                          hipStream_t st);
+
+// ---- kvcache.hip (index 0: keys, 1: values)
+enum KvFormat { kKvE4M3 = 0, kKvMXFP4 = 1 };
+struct KvWrite {
+    const float* x[2];
+    uint64_t stride[2];  // elements between a tensor's tokens
+    uint8_t* codes[2];
+    void* scales[2];
+    const int64_t* slots;
+    uint64_t num_slots;
+    uint32_t tokens, heads, dim;
+};
+struct KvRead {
+    const uint8_t* codes[2];
+    const void* scales[2];
+    void* out[2];
+    const int32_t* page_table;
+    const int32_t* offsets;
+    uint64_t num_slots;
+    uint32_t heads, dim, page_len, seqs, max_pages, rows;
+};
+hipError_t launch_kv_write(int format, const KvWrite& A, hipStream_t st);
+hipError_t launch_kv_read(int format, const KvRead& A, int dtype, hipStream_t st);
+
 }  // namespace rz

@@ -52,7 +52,8 @@ typedef enum {
     RZ_ERR_SHAPE = -3,  /* k not a positive multiple of 256, n == 0, size limits */
     RZ_ERR_ALIGN = -4,  /* a device pointer is not 16-byte aligned */
     RZ_ERR_HIP = -5,    /* a HIP runtime call failed, or the device is not gfx950 */
-    RZ_ERR_VALUE = -6   /* a scalar argument is not finite where it must be */
+    RZ_ERR_VALUE = -6   /* a scalar argument is not finite where it must be, or an
+                           rz_dtype / rz_kv_format argument is not one */
 } rz_status;
 
 /* Largest accepted n*k (weights) and m*k (activations): 2^36 elements. */
@@ -397,6 +398,166 @@ int rz_fp16_convert_act(const float* x, uint32_t m, uint32_t k, uint16_t* a_f16,
  */
 int rz_fp16_gemm(const uint16_t* a_f16, const uint16_t* w_f16, uint32_t m, uint32_t n, uint32_t k,
                  float* y, void* stream);
+
+/* ---------------------------------------------------------------------
+ * MXFP4 path: weights and activations in the OCP microscaling format with
+ * 4-bit elements, multiplied on the block-scaled matrix cores at twice the
+ * E4M3 rate.  Blocks of 32 consecutive values of a row share a power of two
+ * X = 2^(byte - 127) (E8M0); a value is an E2M1 code of x / X:
+ *   a = max |x| of the block, byte = max(floor(log2 a) - 2 + 127, 0) (0 for
+ *   a == 0), code = x / X to the nearest of +-{0, .5, 1, 1.5, 2, 3, 4, 6}
+ *   (codes 0..7, sign in bit 3), ties to the even code, saturating at 6.
+ * A block that holds a NaN or an infinity gets byte 255 and zero codes; byte
+ * 255 is the format's NaN, so every value of the block reads as NaN, and so
+ * does every sum it enters.
+ *
+ * Layout of a tensor [rows][k], k a multiple of 256, rows padded to
+ * rz_mxfp4_pad_rows(rows) with zero codes and zero scale bytes:
+ *   codes  uint8 [rows/32][k/64][2][32][16]: value (r, c) is in byte
+ *          (((r/32)*(k/64) + c/64)*2 + c/32%2)*512 + r%32*16 + c%32/2, the low
+ *          nibble for even c
+ *   scales uint8 [rows/32][k/256][2][32][4]: the byte of the block of (r, c)
+ *          is (((r/32)*(k/256) + c/256)*2 + c/32%2)*128 + r%32*4 + c/64%4
+ * k, n <= RZ_MAX_GEMM_K.  No entry point here uses a workspace or waits on
+ * the host, and every sum has a fixed order.
+ * --------------------------------------------------------------------- */
+
+/* Element types of the outputs that are read back. */
+typedef enum { RZ_F32 = 0, RZ_F16 = 1, RZ_BF16 = 2 } rz_dtype;
+
+/* rows rounded up to a multiple of 32. */
+uint32_t rz_mxfp4_pad_rows(uint32_t rows);
+
+/* Bytes of the codes (pad_rows * k/2) and of the scales (pad_rows * k/32) of
+ * a [rows][k] tensor; 0 if k is not a positive multiple of 256. */
+size_t rz_mxfp4_code_bytes(uint32_t rows, uint32_t k);
+size_t rz_mxfp4_scale_bytes(uint32_t rows, uint32_t k);
+
+/*
+ * x fp32 [m][k] row-major (device) -> codes, scales (device out), pad rows
+ * included, in one pass.  m == 0 is a no-op.
+ */
+int rz_mxfp4_quant(const float* x, uint32_t m, uint32_t k, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * A K-quant weight -> codes, scales: rz_mxfp4_quant of the values that
+ * rz_dequant_f32 gives, which are not written.
+ *   qtype, blocks, n, k   the weight, as for rz_fp8_pack_weight
+ */
+int rz_mxfp4_pack_weight(int qtype, const void* blocks, uint32_t n, uint32_t k, uint8_t* codes, uint8_t* scales,
+                         void* stream);
+
+/*
+ * codes, scales of [rows][k] -> out [rows][k] row-major of type `dtype`
+ * (rz_dtype).  Exact in fp32 and bf16, one rounding to nearest even in fp16.
+ * rows == 0 is a no-op.
+ */
+int rz_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, uint32_t rows, uint32_t k, int dtype, void* out,
+                     void* stream);
+
+/*
+ * y[i][j] = sum_kk a[i][kk] * w[j][kk]   for i < m, j < n
+ *   a_codes, a_scales   MXFP4 [m][k]
+ *   w_codes, w_scales   MXFP4 [n][k]
+ *   y                   device out, fp32 [m][n] row-major
+ * Products are exact; sums are accumulated in fp32.  m == 0 or n == 0 is a
+ * no-op (any pointer may then be NULL).
+ */
+int rz_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* w_codes,
+                  const uint8_t* w_scales, uint32_t n, uint32_t k, float* y, void* stream);
+
+/*
+ * The gated product of a feed-forward block: gate and up projections, the
+ * activation and the product in one kernel,
+ *   h[i][j] = g / (1 + e^-g) * u,  g = a gate^T, u = a up^T   for i < m, j < n
+ *   gate_*, up_*   MXFP4 [n][k] each
+ *   h              device out, fp32 [m][n] row-major
+ * m == 0 or n == 0 is a no-op.  (Forward only: weights here are frozen codes.)
+ */
+int rz_mxfp4_gated(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* gate_codes,
+                   const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales, uint32_t n,
+                   uint32_t k, float* h, void* stream);
+
+/*
+ * rz_mxfp4_gated with its result as rz_mxfp4_quant(h) would give it: the
+ * down projection's operand, without h in memory.
+ *   h_codes, h_scales   device out, MXFP4 [m][n], pad rows included
+ * n must be a multiple of 256 (it is the next product's k).
+ */
+int rz_mxfp4_gated_quant(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* gate_codes,
+                         const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales, uint32_t n,
+                         uint32_t k, uint8_t* h_codes, uint8_t* h_scales, void* stream);
+
+/* Largest batch rz_mxfp4_gemv and rz_mxfp4_gated_gemv accept. */
+#define RZ_MXFP4_GEMV_MAX_M 8u
+
+/*
+ * The same two products for small batches, the input in fp32 and not
+ * quantised:  y = x w^T  and  h = silu(x gate^T) * (x up^T)
+ *   x   device, fp32 [m][k] row-major, m <= RZ_MXFP4_GEMV_MAX_M
+ *   y, h   device out, fp32 [m][n] row-major
+ * fp32 multiply-adds: |y - exact| <= gamma_{k + k/32} sum |x w|, gamma_t =
+ * t u / (1 - t u), u = 2^-24.  m == 0 or n == 0 is a no-op.
+ */
+int rz_mxfp4_gemv(const uint8_t* w_codes, const uint8_t* w_scales, uint32_t n, uint32_t k, const float* x, uint32_t m,
+                  float* y, void* stream);
+int rz_mxfp4_gated_gemv(const uint8_t* gate_codes, const uint8_t* gate_scales, const uint8_t* up_codes,
+                        const uint8_t* up_scales, uint32_t n, uint32_t k, const float* x, uint32_t m, float* h,
+                        void* stream);
+
+/* ---------------------------------------------------------------------
+ * Quantised key/value cache: rows of `dim` values, one a token and head,
+ * written from the K and V projections' fp32 outputs and read back.
+ * --------------------------------------------------------------------- */
+
+/*
+ * RZ_KV_E4M3: codes uint8 [num_slots][heads][dim], E4M3(RN(x * RN(448/a')))
+ *   as rz_fp8_quant_act encodes, with the row's own a = max |x| (NaN
+ *   ignored), a' = a or 1; scales fp32 [num_slots][heads], RN(a'/448).  A
+ *   value reads back as RN(code * scale), then rounded to the output's type.
+ * RZ_KV_MXFP4: codes uint8 [num_slots][heads][dim/2] (even element in the
+ *   low nibble), scales uint8 [num_slots][heads][dim/32], each row in blocks
+ *   of 32 as above.
+ */
+typedef enum { RZ_KV_E4M3 = 0, RZ_KV_MXFP4 = 1 } rz_kv_format;
+
+/* Largest dim (a multiple of 32); heads*dim is at most 2^26. */
+#define RZ_KV_MAX_DIM 512u
+
+/*
+ * Quantise tokens' keys and values into slots of the cache.
+ *   k, v          device, fp32 [tokens][heads][dim]; consecutive tokens are
+ *                 k_stride / v_stride elements apart (a multiple of 4, at
+ *                 least heads*dim), so column ranges of one fused projection
+ *                 can be passed as they are
+ *   slots         device, int64 [tokens]: token t goes to slot slots[t]; a
+ *                 slot that is negative or >= num_slots drops the token
+ *   k_codes ...   device, the cache; other slots are left as they are
+ * Slots of one call must differ: where two tokens name the same slot, what it
+ * holds afterwards may mix their rows (no other slot is affected).
+ * tokens == 0 is a no-op.
+ */
+int rz_kv_cache_write(int format, const float* k, const float* v, uint32_t tokens, uint32_t heads, uint32_t dim,
+                      uint64_t k_stride, uint64_t v_stride, const int64_t* slots, uint64_t num_slots,
+                      uint8_t* k_codes, void* k_scales, uint8_t* v_codes, void* v_scales, void* stream);
+
+/*
+ * Read sequences back from a paged cache, one after another.
+ *   page_len      slots in a page: position p of sequence b is slot
+ *                 page_table[b][p / page_len] * page_len + p % page_len
+ *   page_table    device, int32 [seqs][max_pages]
+ *   offsets       device, int32 [seqs + 1], not decreasing: sequence b is
+ *                 output rows offsets[b] .. offsets[b+1] - 1
+ *   k_out, v_out  device out, [rows][heads][dim] of type `dtype` (rz_dtype)
+ * A position whose page index is >= max_pages, or whose slot lies outside
+ * the cache, reads as zeros.  Rows before offsets[0] and from offsets[seqs]
+ * on are left as they are; rows past `rows` are not written.  rows == 0 or
+ * seqs == 0 is a no-op.
+ */
+int rz_kv_cache_read(int format, const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes,
+                     const void* v_scales, uint64_t num_slots, uint32_t heads, uint32_t dim, uint32_t page_len,
+                     const int32_t* page_table, uint32_t seqs, uint32_t max_pages, const int32_t* offsets,
+                     uint32_t rows, int dtype, void* k_out, void* v_out, void* stream);
 
 /* ---------------------------------------------------------------------
  * Diagnostics: the individual steps, exposed so that each can be checked

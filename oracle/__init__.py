@@ -19,6 +19,9 @@ Modules:
              exact FP8 GEMM, fused epilogue and the parity error bound
   kquant_gemv — the small-M GEMV straight from K-quant blocks (fp32 input
              and output) and its fp32-accumulation error bound
+  mxfp4    — MXFP4 quantisation, the tiled layout, the products and the
+             gated product on it, and their error bounds
+  kv_cache — the quantised key/value cache, written and read back
 
 Parity status: every function is pinned by tests under ``tests/`` that do
 not re-derive it (fixed points, closed forms, exhaustive sweeps, a library
