@@ -54,7 +54,7 @@ def read(fmt: int, codes, scales, page_len: int, table, offsets, out: np.ndarray
     """Sequences into out fp32 [rows][heads][dim], in place."""
     for b in range(len(offsets) - 1):
         for row in range(offsets[b], min(offsets[b + 1], out.shape[0])):
-            page, at = divmod(row - offsets[b], page_len)
+            page, at = divmod(int(row) - int(offsets[b]), page_len)
             s = int(table[b, page]) * page_len + at if page < table.shape[1] and table[b, page] >= 0 else -1
             for h in range(out.shape[1]):
                 out[row, h] = read_row(fmt, codes[s, h], scales[s, h]) if 0 <= s < codes.shape[0] else 0.0
