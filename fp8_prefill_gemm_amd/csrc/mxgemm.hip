@@ -53,9 +53,43 @@ enum Out { kOutF32 = 0, kOutMX = 1 };
 
 __host__ __device__ __forceinline__ uint32_t min_u32(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
+// Workgroup -> tile: the dispatcher sends workgroup w to XCD w % 8; each XCD
+// takes a contiguous run of tiles, m fastest in groups of group_m, so the
+// workgroups that run together on one share rows through its L2.
+__device__ __forceinline__ void tile_of(const Args& P, uint32_t& tm, uint32_t& tn) {
+    const uint32_t T = P.tiles_m * P.tiles_n, x = blockIdx.x % kXcds;
+    const uint32_t t = x * (T / kXcds) + min_u32(x, T % kXcds) + blockIdx.x / kXcds;
+    const uint32_t per = P.group_m * P.tiles_n, first = t / per * P.group_m;
+    const uint32_t gm = min_u32(P.group_m, P.tiles_m - first), in = t % per;
+    tn = in / gm;
+    tm = first + in % gm;
+}
+
+// f(integral_constant<0>) ... f(integral_constant<N - 1>).
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_each_index(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        for_each_index<N, I + 1>(f);
+    }
+}
+
 // A row group's codes or scales as a buffer: `per` bytes for each 256-column slab.
 __device__ __forceinline__ const uint8_t* group_base(const uint8_t* base, uint32_t grp, uint32_t slabs, uint32_t per) {
     return base + (uint64_t)grp * slabs * per;
+}
+
+// `count` row groups from `grp` on as a buffer (k <= RZ_MAX_GEMM_K keeps it
+// under 2^31 bytes), and loads at a lane's offset plus a uniform one.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rsrc(const uint8_t* base, uint32_t grp, uint32_t slabs, uint32_t per,
+                                                             uint32_t count) {
+    return gemm::tile_rsrc(group_base(base, grp, slabs, per), count * slabs * per);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t vo, uint32_t so) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, vo, so, 0));
+}
+__device__ __forceinline__ uint32_t load4(__amdgpu_buffer_rsrc_t rs, uint32_t vo, uint32_t so) {
+    return __builtin_amdgcn_raw_buffer_load_b32(rs, vo, so, 0);
 }
 
 // The 32 x 32 block v (v[e]: row 8 (e/4) + 4 (lane/32) + e%4, column lane%32)
@@ -76,16 +110,11 @@ __device__ __forceinline__ void store_f32(const Args& P, const float (&v)[16], u
     }
 }
 
-// The same block as tiled MXFP4: through this wave's 4 KB of LDS, so that a
-// quad of lanes gets a row's 32 values.  Pad rows are products of zero rows
-// and quantise to zero.
-__device__ __forceinline__ void store_mx(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane,
-                                         float* lds) {
+// A 32 x 32 block in LDS (row-major) to row group grp, columns col0 .. + 31 of
+// the tiled MXFP4 output, by one wave: a quad of lanes holds a row's block.
+// Pad rows are products of zero rows and quantise to zero.
+__device__ __forceinline__ void quantise_block(const Args& P, uint32_t grp, uint32_t col0, uint32_t lane, const float* lds) {
     if (grp * 32u >= P.m) return;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) lds[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * 32 + (lane & 31)] = v[e];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
     const uint32_t blk = col0 / 32u, part = lane & 3u;
     uint8_t* codes = P.h_codes + ((uint64_t)grp * (P.n / 64u) + blk / 2u) * 1024u + (blk & 1u) * 512u;
     uint8_t* scales = P.h_scales + ((uint64_t)grp * (P.n / 256u) + blk / 8u) * 256u + (blk & 1u) * 128u + (blk / 2u) % 4u;
@@ -100,262 +129,330 @@ __device__ __forceinline__ void store_mx(const Args& P, const float (&v)[16], ui
         *reinterpret_cast<uint32_t*>(codes + row * 16u + part * 4u) = c;
         if (part == 0) scales[row * 4u] = (uint8_t)byte;
     }
+}
+
+// The block v (as store_f32 takes it) quantised by its wave, through 4 KB of
+// LDS that no other wave uses.
+__device__ __forceinline__ void store_mx(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane,
+                                         float* lds) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) lds[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * 32 + (lane & 31)] = v[e];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    quantise_block(P, grp, col0, lane, lds);
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
 
 // ---------------------------------------------------------------------------
 // Tile kernel: 128 tokens x 256 weight rows a workgroup (gated: 128 gate and
-// 128 up rows), four waves along the weight rows, each 128 x 64.
+// 128 up rows of the same columns), four waves along the weight rows, each
+// 128 x 64: kTM activation blocks x kWN weight blocks.
 //
 // The four waves read the same activation blocks, so those go through LDS
 // (two 16 KB stages of 256 columns, one barrier each); a weight block is
 // used by one wave only and goes from the L2 straight to registers, a step
-// ahead.  Two workgroups share a CU: while one stores its tile or waits, the
-// other computes.
+// ahead.  With 244 registers and 32 KB of LDS two workgroups share a CU:
+// while one stores its tile or waits, the other computes.
+//
+// Measured (random codes, M = 2048): gated N=18944 K=3584 133 us, 4.2
+// PFLOP/s, of it 11 us that a copy without the store does not take; down
+// N=3584 K=18944 65 us, 4.3 PFLOP/s.  What bounds it is the power limit: with
+// every code 1.0 the same launches run at 5.5 and 5.7 PFLOP/s (2.4 GHz instead
+// of 1.7 to 2.0), and the MFMA alone, on random register operands, reaches
+// 6.6 (9.4 on constant ones).  Left to the compiler's own order, which moves
+// the loads next to their use, 156 and 82 us.  A 256 x 256 tile of eight
+// waves reads a third less through the L2 but has one workgroup a CU: 138
+// and 85 us.
 // ---------------------------------------------------------------------------
-constexpr int kTM = 4;             // activation blocks of 32 rows
-constexpr int kWN = 2;             // weight blocks a wave
-constexpr int kStage = kTM * 4096; // one 256-column step of the activation rows
+constexpr int kTM = 4, kWN = 2, kNW = 4;
 
 template <bool GATED, int OUT>
-__global__ __launch_bounds__(256, 2) void mx_gemm_tile_kernel(Args P) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2][kStage];
+__global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
+    constexpr int kCols = GATED ? kWN / 2 : kWN;  // output blocks of a wave
+    constexpr int kSides = GATED ? 2 : 1;
+    static_assert(64 * kNW == 256, "a thread stages 16 of a row group's 4096 bytes");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2][kTM * 4096];
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t slabs = P.k / 256u;
+    uint32_t tn, tm;
+    tile_of(P, tm, tn);
 
-    // workgroup -> tile: the dispatcher sends workgroup w to XCD w % 8; each
-    // XCD takes a contiguous run of tiles, m fastest in groups of group_m
-    const uint32_t T = P.tiles_m * P.tiles_n, x = blockIdx.x % kXcds, j0 = blockIdx.x / kXcds;
-    const uint32_t t = x * (T / kXcds) + min_u32(x, T % kXcds) + j0;
-    const uint32_t per = P.group_m * P.tiles_n, gi = t / per, first = gi * P.group_m;
-    const uint32_t gm = min_u32(P.group_m, P.tiles_m - first), tin = t - gi * per;
-    const uint32_t tn = tin / gm, tm = first + tin % gm;
-
+    // Offsets (in slabs) of the row groups from the tile's or the wave's first
+    // one, all uniform.  A group past the tensor's last is replaced by the
+    // last: what it gives is not stored.
     const uint32_t a_groups = pad32(P.m) / 32u, w_groups = pad32(P.n) / 32u;
-    uint32_t wg[kWN], wcol[kWN];  // each weight block's row group, first output column
-    const uint8_t *wc[kWN], *ws[kWN];
+    const uint32_t g0 = tm * kTM, w0 = (tn * kNW + wave) * kCols, wb = min_u32(w0, w_groups - 1u);
+    const __amdgpu_buffer_rsrc_t arc = group_rsrc(P.a_codes, g0, slabs, 4096u, kTM);
+    const __amdgpu_buffer_rsrc_t ars = group_rsrc(P.a_scales, g0, slabs, 256u, kTM);
+    __amdgpu_buffer_rsrc_t wrc[kSides], wrs[kSides];
 #pragma unroll
-    for (int i = 0; i < kWN; ++i) {
-        wg[i] = GATED ? tn * 4u + wave : tn * 8u + wave * 2u + i;
-        wcol[i] = wg[i] * 32u;
-        const uint32_t g = min_u32(wg[i], w_groups - 1u);  // past the last group: any rows, not stored
-        wc[i] = group_base(P.w.codes[GATED ? i : 0], g, slabs, 4096u) + lane * 16u;
-        ws[i] = group_base(P.w.scales[GATED ? i : 0], g, slabs, 256u) + lane * 4u;
+    for (int g = 0; g < kSides; ++g) {
+        wrc[g] = group_rsrc(P.w.codes[g], wb, slabs, 4096u, kCols);
+        wrs[g] = group_rsrc(P.w.scales[g], wb, slabs, 256u, kCols);
     }
-    const uint8_t *ac[kTM], *as[kTM];
+    uint32_t ag[kTM], wg[kCols];
 #pragma unroll
-    for (int j = 0; j < kTM; ++j) {
-        const uint32_t g = min_u32(tm * kTM + j, a_groups - 1u);
-        ac[j] = group_base(P.a_codes, g, slabs, 4096u) + tid * 16u;
-        as[j] = group_base(P.a_scales, g, slabs, 256u) + lane * 4u;
-    }
+    for (int j = 0; j < kTM; ++j) ag[j] = (min_u32(g0 + j, a_groups - 1u) - g0) * slabs;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) wg[i] = (min_u32(wb + i, w_groups - 1u) - wb) * slabs;
+    const uint32_t avo = tid * 16u, wvo = lane * 16u, svo = lane * 4u;
 
     v16f acc[kWN][kTM] = {};
-    u32x4 st[kTM];             // activation rows on their way to LDS
-    u32x4 w[2][kWN][4];        // weight blocks of this step and the next
+    u32x4 st[kTM];       // activation rows on their way to LDS
+    u32x4 w[2][kWN][4];  // weight blocks of this step and the next
     uint32_t sa[2][kTM], sw[2][kWN];
 
-    auto load_a = [&](uint32_t s) {
-#pragma unroll
-        for (int j = 0; j < kTM; ++j) st[j] = *reinterpret_cast<const u32x4*>(ac[j] + (uint64_t)s * 4096u);
+    auto load_a = [&](int j, uint32_t s) { st[j] = load16(arc, avo, (ag[j] + s) * 4096u); };
+    auto put_a = [&](uint8_t* dst, int j) { *reinterpret_cast<u32x4*>(dst + j * 4096 + avo) = st[j]; };
+    auto load_w = [&](int b, int i, int q, uint32_t s) {
+        w[b][i][q] = load16(wrc[i / kCols], wvo + q * 1024u, (wg[i % kCols] + s) * 4096u);
     };
-    auto put_a = [&](uint8_t* dst) {
-#pragma unroll
-        for (int j = 0; j < kTM; ++j) *reinterpret_cast<u32x4*>(dst + j * 4096 + tid * 16) = st[j];
-    };
-    auto load_w = [&](int b, uint32_t s) {
-#pragma unroll
-        for (int i = 0; i < kWN; ++i) {
-            sw[b][i] = *reinterpret_cast<const uint32_t*>(ws[i] + (uint64_t)s * 256u);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                w[b][i][q] = *reinterpret_cast<const u32x4*>(wc[i] + (uint64_t)s * 4096u + q * 1024);
-        }
-#pragma unroll
-        for (int j = 0; j < kTM; ++j) sa[b][j] = *reinterpret_cast<const uint32_t*>(as[j] + (uint64_t)s * 256u);
-    };
-    auto step = [&](int b, uint32_t s) {
+    auto load_sw = [&](int b, int i, uint32_t s) { sw[b][i] = load4(wrs[i / kCols], svo, (wg[i % kCols] + s) * 256u); };
+    auto load_sa = [&](int b, int j, uint32_t s) { sa[b][j] = load4(ars, svo, (ag[j] + s) * 256u); };
+
+    // One 256-column step: 16 pieces (64-column slab q, activation block j) of
+    // two MFMAs each, their order kept by the barriers to the scheduler.  In
+    // the shadow of a piece's MFMAs: the read of the activation block two
+    // pieces on; in the first eight the loads of the next step's weights and
+    // scales; in the next four the write of an activation block to the other
+    // stage and the load of the one two steps on.  So every load has a whole
+    // step to land.
+    auto step = [&](auto bc, uint32_t s) {
+        constexpr int b = decltype(bc)::value;
+        constexpr int kPieces = 4 * kTM;
+        static_assert(kPieces == 16 && 4 * kWN == 8 && kTM == 4, "the loads' places below");
+        const uint8_t* cur = smem[b] + wvo;
+        uint8_t* nxt = smem[b ^ 1];
+        const uint32_t s1 = min_u32(s + 1u, slabs - 1u), s2 = min_u32(s + 2u, slabs - 1u);
         __syncthreads();
-        const uint8_t* cur = smem[b];
-        load_w(b ^ 1, min_u32(s + 1u, slabs - 1u));
-        auto part = [&](auto qc) {
-            constexpr int q = decltype(qc)::value;
-#pragma unroll
-            for (int j = 0; j < kTM; ++j) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(cur + j * 4096 + q * 1024 + lane * 16);
-#pragma unroll
-                for (int i = 0; i < kWN; ++i) acc[i][j] = mma<q>(a, w[b][i][q], acc[i][j], sa[b][j], sw[b][i]);
+        u32x4 a[3];
+        a[0] = *reinterpret_cast<const u32x4*>(cur);
+        a[1] = *reinterpret_cast<const u32x4*>(cur + 4096);
+        __builtin_amdgcn_sched_barrier(0);
+        for_each_index<kPieces>([&](auto pc) {
+            constexpr int p = decltype(pc)::value, q = p / kTM, j = p % kTM;
+            if constexpr (p < kPieces - 2) {
+                constexpr int pn = p + 2;
+                a[pn % 3] = *reinterpret_cast<const u32x4*>(cur + (pn % kTM) * 4096 + (pn / kTM) * 1024);
             }
-        };
-        part(std::integral_constant<int, 0>{});
-        part(std::integral_constant<int, 1>{});
-        put_a(smem[b ^ 1]);
-        load_a(min_u32(s + 2u, slabs - 1u));
-        part(std::integral_constant<int, 2>{});
-        part(std::integral_constant<int, 3>{});
+            if constexpr (p < 8) load_w(b ^ 1, p % kWN, p / kWN, s1);
+            if constexpr (p >= 2 && p < 4) load_sw(b ^ 1, p - 2, s1);
+            if constexpr (p >= 4 && p < 8) load_sa(b ^ 1, p - 4, s1);
+            if constexpr (p >= 8 && p < 12) {
+                put_a(nxt, p - 8);
+                load_a(p - 8, s2);
+            }
+#pragma unroll
+            for (int i = 0; i < kWN; ++i) acc[i][j] = mma<q>(a[p % 3], w[b][i][q], acc[i][j], sa[b][j], sw[b][i]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
     };
-    load_a(0);
-    load_w(0, 0);
-    put_a(smem[0]);
-    load_a(min_u32(1u, slabs - 1u));
+#pragma unroll
+    for (int j = 0; j < kTM; ++j) load_a(j, 0);
+#pragma unroll
+    for (int j = 0; j < kTM; ++j) load_sa(0, j, 0);
+#pragma unroll
+    for (int i = 0; i < kWN; ++i) {
+        load_sw(0, i, 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_w(0, i, q, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kTM; ++j) {
+        put_a(smem[0], j);
+        load_a(j, min_u32(1u, slabs - 1u));
+    }
     for (uint32_t s = 0; s < slabs; s += 2) {
-        step(0, s);
-        if (s + 1 < slabs) step(1, s + 1);
+        step(std::integral_constant<int, 0>{}, s);
+        if (s + 1 < slabs) step(std::integral_constant<int, 1>{}, s + 1);
     }
 
     if constexpr (OUT == kOutMX) __syncthreads();  // the stages become the waves' exchange space
 #pragma unroll
-    for (int j = 0; j < kTM; ++j) {
-        float v[16];
-        if constexpr (GATED) {
+    for (int j = 0; j < kTM; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = silu(acc[0][j][e]) * acc[kWN - 1][j][e];
+        for (int i = 0; i < kCols; ++i) {
+            float v[16];
+            const uint32_t col = (w0 + i) * 32u;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = GATED ? silu(acc[i][j][e]) * acc[kWN - kCols + i][j][e] : acc[i][j][e];
             if constexpr (OUT == kOutMX) {
-                if (wcol[0] < P.n)
-                    store_mx(P, v, tm * kTM + j, wcol[0], lane, reinterpret_cast<float*>(smem[0]) + wave * 1024);
+                if (col < P.n) store_mx(P, v, g0 + j, col, lane, reinterpret_cast<float*>(smem) + wave * 1024);
             } else {
-                store_f32(P, v, tm * kTM + j, wcol[0], lane);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWN; ++i) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
-                store_f32(P, v, tm * kTM + j, wcol[i], lane);
+                store_f32(P, v, g0 + j, col, lane);
             }
         }
-    }
 }
 
 // ---------------------------------------------------------------------------
-// Split kernel, for few tiles: 32 TM tokens x 32 weight rows (gated: 32 gate
-// and 32 up rows) a workgroup, whose eight waves share the K range (256
+// Split kernel, for few tiles: 32 TM tokens x 32 WN weight rows (gated: WN/2
+// gate and WN/2 up blocks) a workgroup, whose KS waves share the K range (256
 // columns a turn) and add their sums through LDS in a fixed order.  Every
-// operand goes straight to registers; the activation rows come from the L2.
+// operand goes straight from the L2 to registers; a 64-column slab's next
+// turn is loaded as soon as its MFMAs are issued.
 // ---------------------------------------------------------------------------
-constexpr int kSplit = 8;
-
-template <int TM, int G, int OUT>
-__global__ __launch_bounds__(64 * kSplit) void mx_gemm_split_kernel(Args P) {
-    __shared__ __attribute__((aligned(16))) float sums[kSplit][G * TM][16][64];
+template <int TM, int WN, int KS, bool GATED, int OUT>
+__global__ __launch_bounds__(64 * KS, 2) void mx_gemm_split_kernel(Args P) {
+    constexpr int kCols = GATED ? WN / 2 : WN;
+    constexpr int kPair = GATED ? 2 : 1;
+    constexpr int kRound = 16 / KS < kPair ? kPair : (16 / KS > TM * WN ? TM * WN : 16 / KS);  // blocks added at a time
+    constexpr int kOutBlocks = kRound / kPair;
+    constexpr int kPer = kOutBlocks * 16 / KS;         // register rows a wave adds
+    static_assert(TM * WN % kRound == 0 && kPer >= 1 && kPer * KS == kOutBlocks * 16, "rounds");
+    __shared__ __attribute__((aligned(16))) float sums[KS][kRound][16][64];
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t slabs = P.k / 256u;
-    const uint32_t tn = blockIdx.x % P.tiles_n, tm = blockIdx.x / P.tiles_n;
-    const uint32_t a_groups = pad32(P.m) / 32u;
-    const uint8_t *wc[G], *ws[G], *ac[TM], *as[TM];
+    uint32_t tn, tm;
+    tile_of(P, tm, tn);
+    const uint32_t a_groups = pad32(P.m) / 32u, w_groups = pad32(P.n) / 32u;
+    const uint32_t g0 = tm * TM, w0 = tn * kCols;
+    const __amdgpu_buffer_rsrc_t arc = group_rsrc(P.a_codes, g0, slabs, 4096u, TM), ars = group_rsrc(P.a_scales, g0, slabs, 256u, TM);
+    __amdgpu_buffer_rsrc_t wrc[kPair], wrs[kPair];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        wc[g] = group_base(P.w.codes[g], tn, slabs, 4096u) + lane * 16u;
-        ws[g] = group_base(P.w.scales[g], tn, slabs, 256u) + lane * 4u;
+    for (int g = 0; g < kPair; ++g) {
+        wrc[g] = group_rsrc(P.w.codes[g], w0, slabs, 4096u, kCols);
+        wrs[g] = group_rsrc(P.w.scales[g], w0, slabs, 256u, kCols);
     }
+    uint32_t ag[TM], wg[kCols];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-        const uint32_t g = min_u32(tm * TM + j, a_groups - 1u);
-        ac[j] = group_base(P.a_codes, g, slabs, 4096u) + lane * 16u;
-        as[j] = group_base(P.a_scales, g, slabs, 256u) + lane * 4u;
+    for (int j = 0; j < TM; ++j) ag[j] = (min_u32(g0 + j, a_groups - 1u) - g0) * slabs;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) wg[i] = (min_u32(w0 + i, w_groups - 1u) - w0) * slabs;
+    const uint32_t cvo = lane * 16u, svo = lane * 4u;
+    v16f acc[WN][TM] = {};
+    u32x4 a[TM][4], w[WN][4];
+    uint32_t sa[2][TM], sw[2][WN];
+    auto load_q = [&](int q, uint32_t s) {
+#pragma unroll
+        for (int i = 0; i < WN; ++i) w[i][q] = load16(wrc[i / kCols], cvo + q * 1024u, (wg[i % kCols] + s) * 4096u);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) a[j][q] = load16(arc, cvo + q * 1024u, (ag[j] + s) * 4096u);
+    };
+    auto load_s = [&](int b, uint32_t s) {
+#pragma unroll
+        for (int i = 0; i < WN; ++i) sw[b][i] = load4(wrs[i / kCols], svo, (wg[i % kCols] + s) * 256u);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) sa[b][j] = load4(ars, svo, (ag[j] + s) * 256u);
+    };
+    auto turn = [&](auto bc, uint32_t s) {
+        constexpr int b = decltype(bc)::value;
+        const uint32_t next = min_u32(s + KS, slabs - 1u);
+        load_s(b ^ 1, next);
+        for_each_index<4>([&](auto qc) {
+            constexpr int q = decltype(qc)::value;
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+#pragma unroll
+                for (int i = 0; i < WN; ++i) acc[i][j] = mma<q>(a[j][q], w[i][q], acc[i][j], sa[b][j], sw[b][i]);
+            load_q(q, next);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    if (wave < slabs) {
+        load_s(0, wave);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_q(q, wave);
+        for (uint32_t s = wave; s < slabs; s += 2 * KS) {
+            turn(std::integral_constant<int, 0>{}, s);
+            if (s + KS < slabs) turn(std::integral_constant<int, 1>{}, s + KS);
+        }
     }
-    v16f acc[G][TM] = {};
-    for (uint32_t s = wave; s < slabs; s += kSplit) {
-        u32x4 a[TM][4], w[G][4];
-        uint32_t sa[TM], sw[G];
+    // rounds of kRound blocks; block b of a round is output block b / kPair
+    // (gate before up)
+    for_each_index<TM * WN / kRound>([&](auto rc) {
+        constexpr int r = decltype(rc)::value;
+        auto block = [&](int b) { return r * kOutBlocks + b / kPair; };  // output block i + kCols j
+        if constexpr (r > 0) __syncthreads();
+        for_each_index<kRound>([&](auto bc) {
+            constexpr int b = decltype(bc)::value, o = r * kOutBlocks + b / kPair, i = o % kCols + (b % kPair) * kCols, j = o / kCols;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+            for (int e = 0; e < 16; ++e) sums[wave][b][e][lane] = acc[i][j][e];
+        });
+        __syncthreads();
+        float v[kPer];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                w[g][q] = *reinterpret_cast<const u32x4*>(wc[g] + (uint64_t)s * 4096u + q * 1024);
-            sw[g] = *reinterpret_cast<const uint32_t*>(ws[g] + (uint64_t)s * 256u);
-        }
+        for (int u = 0; u < kPer; ++u) {
+            const int e = (int)wave * kPer + u, b = (e / 16) * kPair;
+            float s[kPair];
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
+            for (int g = 0; g < kPair; ++g) {
+                s[g] = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                a[j][q] = *reinterpret_cast<const u32x4*>(ac[j] + (uint64_t)s * 4096u + q * 1024);
-            sa[j] = *reinterpret_cast<const uint32_t*>(as[j] + (uint64_t)s * 256u);
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                acc[g][j] = mma<0>(a[j][0], w[g][0], acc[g][j], sa[j], sw[g]);
-                acc[g][j] = mma<1>(a[j][1], w[g][1], acc[g][j], sa[j], sw[g]);
-                acc[g][j] = mma<2>(a[j][2], w[g][2], acc[g][j], sa[j], sw[g]);
-                acc[g][j] = mma<3>(a[j][3], w[g][3], acc[g][j], sa[j], sw[g]);
+                for (int z = 0; z < KS; ++z) s[g] += sums[z][b + g][e % 16][lane];
             }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sums[wave][g * TM + j][e][lane] = acc[g][j][e];
-    __syncthreads();
-    // the block's 16 x TM register rows, two a wave (TM = 1) or more
-    constexpr int kPer = 16 * TM / kSplit;
-    float v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = (int)wave * kPer + i;
-        float s[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            s[g] = 0.0f;
-#pragma unroll
-            for (int u = 0; u < kSplit; ++u) s[g] += sums[u][g * TM + e / 16][e % 16][lane];
+            v[u] = GATED ? silu(s[0]) * s[kPair - 1] : s[0];
         }
-        if constexpr (G == 2)
-            v[i] = silu(s[0]) * s[G - 1];
-        else
-            v[i] = s[0];
-    }
-    const uint32_t col = tn * 32u + (lane & 31u);
-    if constexpr (OUT == kOutF32) {
+        if constexpr (OUT == kOutF32) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const uint32_t e = wave * kPer + i;
-            const uint32_t row = (tm * TM + e / 16u) * 32u + 8u * ((e & 15u) >> 2) + 4u * (lane >> 5) + (e & 3u);
-            if (row < P.m && col < P.n) P.y[(uint64_t)row * P.n + col] = v[i];
-        }
-    } else {
-        __syncthreads();
-        float* blk = &sums[0][0][0][0];  // TM row groups of 32 x 32, as store_mx reads them
+            for (int u = 0; u < kPer; ++u) {
+                const uint32_t e = wave * kPer + u, o = block((e / 16u) * kPair);
+                const uint32_t row = (g0 + o / kCols) * 32u + 8u * ((e & 15u) >> 2) + 4u * (lane >> 5) + (e & 3u);
+                const uint32_t col = (w0 + o % kCols) * 32u + (lane & 31u);
+                if (row < P.m && col < P.n) P.y[(uint64_t)row * P.n + col] = v[u];
+            }
+        } else {
+            __syncthreads();
+            float* blk = &sums[0][0][0][0];  // the output blocks as 32 x 32 rows, for store_mx
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const uint32_t e = wave * kPer + i;
-            blk[(e / 16u) * 1024u + (8u * ((e & 15u) >> 2) + 4u * (lane >> 5) + (e & 3u)) * 32u + (lane & 31u)] = v[i];
+            for (int u = 0; u < kPer; ++u) {
+                const uint32_t e = wave * kPer + u;
+                blk[(e / 16u) * 1024u + (8u * ((e & 15u) >> 2) + 4u * (lane >> 5) + (e & 3u)) * 32u + (lane & 31u)] = v[u];
+            }
+            __syncthreads();
+            if (wave < kOutBlocks) {  // one block a wave
+                const uint32_t o = block((int)wave * kPair);
+                if ((w0 + o % kCols) * 32u < P.n) quantise_block(P, g0 + o / kCols, (w0 + o % kCols) * 32u, lane, blk + wave * 1024);
+            }
         }
-        __syncthreads();
-        if (wave < TM) {  // one row group a wave
-            float b[16];
-            const float* src = blk + wave * 1024;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) b[e] = src[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * 32 + (lane & 31)];
-            store_mx(P, b, tm * TM + wave, tn * 32u, lane, blk + wave * 1024);
-        }
-    }
+    });
 }
 
+template <int TM, int WN, int KS, bool GATED, int OUT>
+void launch_split(Args& P, uint32_t a_groups, uint32_t w_groups, hipStream_t st) {
+    constexpr uint32_t cols = GATED ? WN / 2 : WN;
+    P.tiles_m = P.group_m = (a_groups + TM - 1) / TM;
+    P.tiles_n = (w_groups + cols - 1) / cols;
+    mx_gemm_split_kernel<TM, WN, KS, GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * KS, 0, st>>>(P);
+}
+
+// The kernel goes by the number of 32 x 32 block products of a K step, the
+// gate's and the up's counted: few blocks take small workgroups with K split
+// eight ways, then larger ones split four ways, many the tile kernel.  K
+// itself does not matter: every candidate's time is nearly linear in it.
+// Measured around the bounds, K = 3584 (us: 1x1 / 2x1 / 2x2 blocks / tile):
+//   256 blocks (512 x 512)     3.9 /  4.7 /  5.5 / 11.7
+//   288        (37 x 4608)     5.1 /  4.7 /  5.6 / 11.3
+//   448        (128 x 3584)    5.4 /  5.0 /  5.8 / 11.8
+//   896        (256 x 3584)    8.5 /  7.3 /  6.4 / 11.9   (K = 18944: 28 / 22 / 17 / 46)
+//   1024       (2048 x 512)   10.2 /  9.7 /  8.3 / 12.0
+//   1792       (512 x 3584)   13.2 / 12.3 /  9.5 / 12.1
+//   2048       (4096 x 512)   20.1 / 20.6 / 12.9 / 12.3
+//   2368       (128 x 18944)  18.0 / 15.4 / 13.7 / 12.6
+// gated (us: 1x2 / 2x2 / tile): 1152 blocks (128 x 4608) 10.0 / 9.5 / 12.4,
+// 2368 (37 x 18944) 16.5 / 16.3 / 14.4.  A single row group keeps the 1-high
+// workgroups (16 x 18944 gated, 1184 blocks: 13.9 / 15.3 / 13.8).
 template <bool GATED, int OUT>
 void launch_as(Args P, hipStream_t st) {
     const uint32_t a_groups = pad32(P.m) / 32u, w_groups = pad32(P.n) / 32u;
-    const uint32_t wn = GATED ? 4u : 8u;  // output blocks of 32 columns a tile
-    P.tiles_m = (a_groups + kTM - 1) / kTM;
-    P.tiles_n = (w_groups + wn - 1) / wn;
-    if ((uint64_t)P.tiles_m * P.tiles_n >= 192u) {
+    const uint64_t blocks = (uint64_t)a_groups * w_groups * (GATED ? 2 : 1);
+    if (blocks > (a_groups == 1 ? 1200u : 2000u)) {
+        constexpr uint32_t cols = (GATED ? kWN / 2 : kWN) * kNW;
+        P.tiles_m = (a_groups + kTM - 1) / kTM;
+        P.tiles_n = (w_groups + cols - 1) / cols;
         P.group_m = min_u32(P.tiles_m, 8u);
-        mx_gemm_tile_kernel<GATED, OUT><<<P.tiles_m * P.tiles_n, 256, 0, st>>>(P);
-        return;
+        mx_gemm_tile_kernel<GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * kNW, 0, st>>>(P);
+    } else if (a_groups > 1 && blocks > (GATED ? 600u : 800u)) {
+        launch_split<2, 2, 4, GATED, OUT>(P, a_groups, w_groups, st);
+    } else if constexpr (GATED) {
+        launch_split<1, 2, 8, GATED, OUT>(P, a_groups, w_groups, st);
+    } else if (a_groups > 1 && blocks > 272u) {
+        launch_split<2, 1, 8, GATED, OUT>(P, a_groups, w_groups, st);
+    } else {
+        launch_split<1, 1, 8, GATED, OUT>(P, a_groups, w_groups, st);
     }
-    constexpr int G = GATED ? 2 : 1;
-    const uint32_t tm = a_groups > 1 ? 2u : 1u;
-    P.tiles_n = w_groups;
-    P.tiles_m = (a_groups + tm - 1) / tm;
-    if (tm == 1)
-        mx_gemm_split_kernel<1, G, OUT><<<P.tiles_m * P.tiles_n, 64 * kSplit, 0, st>>>(P);
-    else
-        mx_gemm_split_kernel<2, G, OUT><<<P.tiles_m * P.tiles_n, 64 * kSplit, 0, st>>>(P);
 }
 
 }  // namespace
