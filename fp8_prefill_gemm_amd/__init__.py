@@ -447,95 +447,101 @@ def rz_fp16_gemm(a_f16, w_f16, m: int, y=None, stream=None):
 
 # MXFP4 tensors are pairs (codes, scales) of uint8 tensors in the tiled layout
 # of include/rz_fp8.h: codes [rows/32][k/64][1024], scales [rows/32][k/256][256].
+# The kernels below take a few microseconds, so their wrappers check in few
+# steps and read the current stream without building a torch object for it.
 
 def rz_mxfp4_pad_rows(rows: int) -> int:
     return (rows + 31) // 32 * 32
 
 
-def _need(t, what, dtype, shape=None):
-    """Raise unless t is a contiguous tensor of this dtype (and shape)."""
-    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor" + (f" of shape {tuple(shape)}" if shape is not None else "")
-                         + f", got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+def _refuse(t, what, dtype, shape, index):
+    want = f"a contiguous {dtype} tensor of shape {tuple(shape)} on device {index}"
+    raise ValueError(f"{what}: expected {want}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"rz_fp8: tensors on {t.device} and {dev}: one device expected")
+def _need(t, what, dtype, shape, index):
+    """Raise unless t is a contiguous tensor of this dtype and shape on GPU `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, what, dtype, shape, index)
 
 
-def _out(shape, dtype, dev, stream):
-    """A new output on the call's stream (see _empty)."""
-    return _torch().empty(shape, dtype=dtype, device=dev) if stream is None else _empty(shape, dtype, dev, stream)
+def _gpu(t, what):
+    """The GPU index of t."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{what}: rz_fp8 works on device (cuda/hip) tensors only")
+    return index
 
 
-def _run_on(dev, stream, fn, *args):
-    """Call entry point `fn` with `args` and the stream, on device `dev`."""
+def _out(t, what, shape, dtype, like, index, stream):
+    """t, checked, or a new output on the call's stream (see _empty)."""
+    if t is not None:
+        _need(t, what, dtype, shape, index)
+        return t
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _empty(shape, dtype, like.device, stream)
+
+
+_raw_stream = None
+
+
+def _run_on(index, stream, fn, *args):
+    """Call entry point `fn` with `args` and the stream on GPU `index`."""
+    global _raw_stream
     torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, _stream(stream, dev)))
+    if stream is not None:
+        handle = stream.cuda_stream
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream, dev)))
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda i: torch.cuda.current_stream(i).cuda_stream)
+        handle = _raw_stream(index)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status:
+        _check(status)
 
 
-def _mx(codes, scales, rows, what):
-    """k of the MXFP4 tensor (codes, scales) of `rows` rows, its shapes checked."""
-    torch = _torch()
+def _mx(codes, scales, rows, what, index):
+    """k of the MXFP4 tensor (codes, scales) of `rows` rows, checked."""
+    u8 = _torch().uint8
+    shape = codes.shape
+    slabs = shape[1] if len(shape) == 3 else 0
     g = (rows + 31) // 32
-    if codes.dim() != 3:
-        raise ValueError(f"{what} codes: expected shape [rows/32][k/64][1024], got {tuple(codes.shape)}")
-    k = codes.shape[1] * 64
-    _need(codes, f"{what} codes", torch.uint8, (g, k // 64, 1024))
-    _need(scales, f"{what} scales", torch.uint8, (g, k // 256, 256))
-    return k
+    _need(codes, what + " codes", u8, (g, slabs, 1024), index)
+    _need(scales, what + " scales", u8, (g, slabs // 4, 256), index)
+    return slabs * 64
 
 
-def _mx_out(rows, k, codes, scales, dev, stream, what="output"):
-    torch = _torch()
+def _mx_out(rows, k, codes, scales, what, like, index, stream):
+    u8 = _torch().uint8
     g = (rows + 31) // 32
-    if codes is None:
-        codes = _out((g, k // 64, 1024), torch.uint8, dev, stream)
-    else:
-        _need(codes, f"{what} codes", torch.uint8, (g, k // 64, 1024))
-    if scales is None:
-        scales = _out((g, k // 256, 256), torch.uint8, dev, stream)
-    else:
-        _need(scales, f"{what} scales", torch.uint8, (g, k // 256, 256))
-    return codes, scales
-
-
-def _f32_out(t, what, shape, dev, stream):
-    torch = _torch()
-    if t is None:
-        return _out(shape, torch.float32, dev, stream)
-    _need(t, what, torch.float32, shape)
-    return t
+    return (_out(codes, what + " codes", (g, k // 64, 1024), u8, like, index, stream),
+            _out(scales, what + " scales", (g, k // 256, 256), u8, like, index, stream))
 
 
 def rz_mxfp4_quant(x, codes=None, scales=None, stream=None):
     """x fp32 [m][k] -> MXFP4 (codes, scales), pad rows included."""
-    _require_cuda(x, codes, scales)
-    _need(x, "x", _torch().float32)
+    index = _gpu(x, "x")
     m, k = x.shape
-    dev = x.device
-    codes, scales = _mx_out(m, k, codes, scales, dev, stream)
-    _same_device(dev, codes, scales)
-    _run_on(dev, stream, lib().rz_mxfp4_quant, _ptr(x), m, k, _ptr(codes), _ptr(scales))
+    _need(x, "x", _torch().float32, (m, k), index)
+    codes, scales = _mx_out(m, k, codes, scales, "output", x, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_quant, x.data_ptr(), m, k, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def rz_mxfp4_pack_weight(qtype: int, blocks, n: int, k: int, codes=None, scales=None, stream=None):
     """A K-quant weight -> MXFP4 (codes, scales)."""
-    _require_cuda(blocks, codes, scales)
-    _need(blocks, "blocks", _torch().uint8)
+    index = _gpu(blocks, "blocks")
+    _need(blocks, "blocks", _torch().uint8, blocks.shape, index)
     if blocks.numel() < rz_weight_bytes(qtype, n, k):
         raise ValueError(f"blocks: {blocks.numel()} bytes, {rz_weight_bytes(qtype, n, k)} needed")
-    dev = blocks.device
-    codes, scales = _mx_out(n, k, codes, scales, dev, stream)
-    _same_device(dev, codes, scales)
-    _run_on(dev, stream, lib().rz_mxfp4_pack_weight, qtype, _ptr(blocks), n, k, _ptr(codes), _ptr(scales))
+    codes, scales = _mx_out(n, k, codes, scales, "output", blocks, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_pack_weight, qtype, blocks.data_ptr(), n, k, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -549,65 +555,60 @@ def _dtype_id(dtype):
 
 def rz_mxfp4_dequant(codes, scales, rows: int, out=None, dtype=None, stream=None):
     """MXFP4 -> out [rows][k] of dtype (default: out's, or float32)."""
-    _require_cuda(codes, scales, out)
-    k = _mx(codes, scales, rows, "input")
-    dev = codes.device
+    index = _gpu(codes, "codes")
+    k = _mx(codes, scales, rows, "input", index)
     if dtype is None:
         dtype = _torch().float32 if out is None else out.dtype
     did = _dtype_id(dtype)
-    if out is None:
-        out = _out((rows, k), dtype, dev, stream)
-    else:
-        _need(out, "out", dtype, (rows, k))
-    _same_device(dev, scales, out)
-    _run_on(dev, stream, lib().rz_mxfp4_dequant, _ptr(codes), _ptr(scales), rows, k, did, _ptr(out))
+    out = _out(out, "out", (rows, k), dtype, codes, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_dequant, codes.data_ptr(), scales.data_ptr(), rows, k, did, out.data_ptr())
     return out
 
 
 def rz_mxfp4_gemm(a_codes, a_scales, m: int, w_codes, w_scales, n: int, y=None, stream=None):
     """-> y fp32 [m][n] = a @ w^T of MXFP4 a [m][k] and w [n][k]."""
-    _require_cuda(a_codes, a_scales, w_codes, w_scales, y)
-    k = _mx(a_codes, a_scales, m, "a")
-    if _mx(w_codes, w_scales, n, "w") != k:
+    index = _gpu(a_codes, "a codes")
+    k = _mx(a_codes, a_scales, m, "a", index)
+    if _mx(w_codes, w_scales, n, "w", index) != k:
         raise ValueError(f"a has k={k}, w has k={w_codes.shape[1] * 64}")
-    dev = a_codes.device
-    y = _f32_out(y, "y", (m, n), dev, stream)
-    _same_device(dev, a_scales, w_codes, w_scales, y)
-    _run_on(dev, stream, lib().rz_mxfp4_gemm, _ptr(a_codes), _ptr(a_scales), m, _ptr(w_codes), _ptr(w_scales), n, k, _ptr(y))
+    y = _out(y, "y", (m, n), _torch().float32, a_codes, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_gemm, a_codes.data_ptr(), a_scales.data_ptr(), m, w_codes.data_ptr(),
+            w_scales.data_ptr(), n, k, y.data_ptr())
     return y
 
 
-def _gated_args(a_codes, a_scales, m, gate, up, n):
+def _gate_up(gate, up, n, index):
+    """(k, pointers) of the gate and up weights, checked."""
     (gc, gs), (uc, us) = gate, up
-    _require_cuda(a_codes, a_scales, gc, gs, uc, us)
-    k = _mx(a_codes, a_scales, m, "a")
-    if _mx(gc, gs, n, "gate") != k or _mx(uc, us, n, "up") != k:
-        raise ValueError(f"a has k={k}, gate has k={gc.shape[1] * 64}, up has k={uc.shape[1] * 64}")
-    _same_device(a_codes.device, a_scales, gc, gs, uc, us)
-    return k, (_ptr(a_codes), _ptr(a_scales), m, _ptr(gc), _ptr(gs), _ptr(uc), _ptr(us), n, k)
+    k = _mx(gc, gs, n, "gate", index)
+    if _mx(uc, us, n, "up", index) != k:
+        raise ValueError(f"gate has k={k}, up has k={uc.shape[1] * 64}")
+    return k, (gc.data_ptr(), gs.data_ptr(), uc.data_ptr(), us.data_ptr())
+
+
+def _gated_args(a_codes, a_scales, m, gate, up, n):
+    index = _gpu(a_codes, "a codes")
+    k, weights = _gate_up(gate, up, n, index)
+    if _mx(a_codes, a_scales, m, "a", index) != k:
+        raise ValueError(f"a has k={a_codes.shape[1] * 64}, gate and up have k={k}")
+    return index, (a_codes.data_ptr(), a_scales.data_ptr(), m, *weights, n, k)
 
 
 def rz_mxfp4_gated(a_codes, a_scales, m: int, gate, up, n: int, h=None, stream=None):
     """-> h fp32 [m][n] = silu(a @ gate^T) * (a @ up^T); gate and up are
     MXFP4 (codes, scales) pairs of [n][k]."""
-    k, args = _gated_args(a_codes, a_scales, m, gate, up, n)
-    dev = a_codes.device
-    _require_cuda(h)
-    h = _f32_out(h, "h", (m, n), dev, stream)
-    _same_device(dev, h)
-    _run_on(dev, stream, lib().rz_mxfp4_gated, *args, _ptr(h))
+    index, args = _gated_args(a_codes, a_scales, m, gate, up, n)
+    h = _out(h, "h", (m, n), _torch().float32, a_codes, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_gated, *args, h.data_ptr())
     return h
 
 
 def rz_mxfp4_gated_quant(a_codes, a_scales, m: int, gate, up, n: int, h_codes=None, h_scales=None, stream=None):
     """rz_mxfp4_gated with its result as MXFP4 -> (h_codes, h_scales), the
     down projection's operand (n a multiple of 256)."""
-    k, args = _gated_args(a_codes, a_scales, m, gate, up, n)
-    dev = a_codes.device
-    _require_cuda(h_codes, h_scales)
-    h_codes, h_scales = _mx_out(m, n, h_codes, h_scales, dev, stream, "h")
-    _same_device(dev, h_codes, h_scales)
-    _run_on(dev, stream, lib().rz_mxfp4_gated_quant, *args, _ptr(h_codes), _ptr(h_scales))
+    index, args = _gated_args(a_codes, a_scales, m, gate, up, n)
+    h_codes, h_scales = _mx_out(m, n, h_codes, h_scales, "h", a_codes, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_gated_quant, *args, h_codes.data_ptr(), h_scales.data_ptr())
     return h_codes, h_scales
 
 
@@ -616,31 +617,26 @@ MXFP4_GEMV_MAX_M = 8
 
 def rz_mxfp4_gemv(w_codes, w_scales, n: int, x, y=None, stream=None):
     """-> y fp32 [m][n] = x @ w^T, x fp32 [m][k] with m <= MXFP4_GEMV_MAX_M."""
-    _require_cuda(w_codes, w_scales, x, y)
-    k = _mx(w_codes, w_scales, n, "w")
+    index = _gpu(x, "x")
+    k = _mx(w_codes, w_scales, n, "w", index)
     m = x.shape[0]
-    _need(x, "x", _torch().float32, (m, k))
-    dev = x.device
-    y = _f32_out(y, "y", (m, n), dev, stream)
-    _same_device(dev, w_codes, w_scales, y)
-    _run_on(dev, stream, lib().rz_mxfp4_gemv, _ptr(w_codes), _ptr(w_scales), n, k, _ptr(x), m, _ptr(y))
+    f32 = _torch().float32
+    _need(x, "x", f32, (m, k), index)
+    y = _out(y, "y", (m, n), f32, x, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_gemv, w_codes.data_ptr(), w_scales.data_ptr(), n, k, x.data_ptr(), m, y.data_ptr())
     return y
 
 
 def rz_mxfp4_gated_gemv(gate, up, n: int, x, h=None, stream=None):
     """-> h fp32 [m][n] = silu(x @ gate^T) * (x @ up^T), x fp32 [m][k] with
     m <= MXFP4_GEMV_MAX_M."""
-    (gc, gs), (uc, us) = gate, up
-    _require_cuda(gc, gs, uc, us, x, h)
-    k = _mx(gc, gs, n, "gate")
-    if _mx(uc, us, n, "up") != k:
-        raise ValueError(f"gate has k={k}, up has k={uc.shape[1] * 64}")
+    index = _gpu(x, "x")
+    k, weights = _gate_up(gate, up, n, index)
     m = x.shape[0]
-    _need(x, "x", _torch().float32, (m, k))
-    dev = x.device
-    h = _f32_out(h, "h", (m, n), dev, stream)
-    _same_device(dev, gc, gs, uc, us, h)
-    _run_on(dev, stream, lib().rz_mxfp4_gated_gemv, _ptr(gc), _ptr(gs), _ptr(uc), _ptr(us), n, k, _ptr(x), m, _ptr(h))
+    f32 = _torch().float32
+    _need(x, "x", f32, (m, k), index)
+    h = _out(h, "h", (m, n), f32, x, index, stream)
+    _run_on(index, stream, lib().rz_mxfp4_gated_gemv, *weights, n, k, x.data_ptr(), m, h.data_ptr())
     return h
 
 
@@ -648,41 +644,48 @@ KV_E4M3, KV_MXFP4 = 0, 1
 
 
 def _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales):
-    """(num_slots, heads, dim) of a cache, its tensors checked."""
+    """(num_slots, heads, dim, GPU index) of a cache, its tensors checked."""
     torch = _torch()
     if fmt not in (KV_E4M3, KV_MXFP4):
         raise ValueError(f"fmt: expected KV_E4M3 or KV_MXFP4, got {fmt}")
     if k_codes.dim() != 3:
         raise ValueError(f"k_codes: expected 3 dimensions, got {tuple(k_codes.shape)}")
-    slots, heads, width = k_codes.shape
-    dim = width if fmt == KV_E4M3 else 2 * width
-    sdtype, sshape = (torch.float32, (slots, heads)) if fmt == KV_E4M3 else (torch.uint8, (slots, heads, dim // 32))
-    for c, s, what in ((k_codes, k_scales, "k"), (v_codes, v_scales, "v")):
-        _need(c, f"{what}_codes", torch.uint8, (slots, heads, width))
-        _need(s, f"{what}_scales", sdtype, sshape)
-    _same_device(k_codes.device, k_scales, v_codes, v_scales)
-    return slots, heads, dim
+    index = _gpu(k_codes, "k_codes")
+    shape = slots, heads, width = k_codes.shape
+    if fmt == KV_E4M3:
+        dim, sdtype, sshape = width, torch.float32, (slots, heads)
+    else:
+        dim, sdtype, sshape = 2 * width, torch.uint8, (slots, heads, width // 16)
+    _need(k_codes, "k_codes", torch.uint8, shape, index)
+    _need(v_codes, "v_codes", torch.uint8, shape, index)
+    _need(k_scales, "k_scales", sdtype, sshape, index)
+    _need(v_scales, "v_scales", sdtype, sshape, index)
+    return slots, heads, dim, index
+
+
+def _kv_rows(t, what, shape, index):
+    """The token stride of t, fp32 [tokens][heads][dim] with contiguous tokens."""
+    stride = t.stride()
+    tokens, heads, dim = shape
+    if t.dtype is not _torch().float32 or t.shape != shape or t.get_device() != index or (
+            tokens and (stride[2] != 1 or (heads > 1 and stride[1] != dim))):
+        raise ValueError(f"{what}: expected float32 {tuple(shape)} with contiguous tokens on device {index}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {stride} on {t.device}")
+    return stride[0] if tokens > 1 else heads * dim  # free where there is one token
 
 
 def rz_kv_cache_write(fmt: int, k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
     """Quantise k and v, fp32 [tokens][heads][dim] (tokens may be strided),
     into the cache rows `slots` (int64 [tokens]; out of range: dropped)."""
-    torch = _torch()
-    _require_cuda(k, v, slots, k_codes, k_scales, v_codes, v_scales)
-    num_slots, heads, dim = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
+    num_slots, heads, dim, index = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
     tokens = k.shape[0]
-    for t, what in ((k, "k"), (v, "v")):
-        if t.dtype is not torch.float32 or t.shape != (tokens, heads, dim) or (
-                tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
-            raise ValueError(f"{what}: expected float32 [{tokens}][{heads}][{dim}] with contiguous tokens, got {t.dtype} "
-                             f"{tuple(t.shape)} with strides {t.stride()}")
-    _need(slots, "slots", torch.int64, (tokens,))
-    dev = k.device
-    _same_device(dev, v, slots, k_codes)
-    # the token stride is free where there is one token
-    ks, vs = (k.stride(0), v.stride(0)) if tokens > 1 else (heads * dim, heads * dim)
-    _run_on(dev, stream, lib().rz_kv_cache_write, fmt, _ptr(k), _ptr(v), tokens, heads, dim, ks, vs, _ptr(slots), num_slots,
-            _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales))
+    k_stride = _kv_rows(k, "k", (tokens, heads, dim), index)
+    v_stride = _kv_rows(v, "v", (tokens, heads, dim), index)
+    if min(k_stride, v_stride) < heads * dim:
+        raise ValueError(f"token strides {k_stride} and {v_stride}: at least heads*dim={heads * dim} expected")
+    _need(slots, "slots", _torch().int64, (tokens,), index)
+    _run_on(index, stream, lib().rz_kv_cache_write, fmt, k.data_ptr(), v.data_ptr(), tokens, heads, dim, k_stride, v_stride,
+            slots.data_ptr(), num_slots, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr())
 
 
 def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: int, page_table, offsets, rows: int,
@@ -693,31 +696,23 @@ def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: i
     is rows offsets[b] .. offsets[b+1] - 1.  Rows of no sequence are left as
     they are (undefined in a new output)."""
     torch = _torch()
-    _require_cuda(k_codes, k_scales, v_codes, v_scales, page_table, offsets, k_out, v_out)
-    num_slots, heads, dim = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
+    num_slots, heads, dim, index = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
     if page_table.dim() != 2:
         raise ValueError(f"page_table: expected 2 dimensions, got {tuple(page_table.shape)}")
     seqs, max_pages = page_table.shape
-    _need(page_table, "page_table", torch.int32)
-    _need(offsets, "offsets", torch.int32, (seqs + 1,))
+    _need(page_table, "page_table", torch.int32, page_table.shape, index)
+    _need(offsets, "offsets", torch.int32, (seqs + 1,), index)
     if page_len < 1 or rows < 0:
         raise ValueError(f"page_len={page_len} must be positive and rows={rows} not negative")
-    dev = k_codes.device
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.float32
     did = _dtype_id(dtype)
     shape = (rows, heads, dim)
-    if k_out is None:
-        k_out = _out(shape, dtype, dev, stream)
-    else:
-        _need(k_out, "k_out", dtype, shape)
-    if v_out is None:
-        v_out = _out(shape, dtype, dev, stream)
-    else:
-        _need(v_out, "v_out", dtype, shape)
-    _same_device(dev, page_table, offsets, k_out, v_out)
-    _run_on(dev, stream, lib().rz_kv_cache_read, fmt, _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), num_slots,
-            heads, dim, page_len, _ptr(page_table), seqs, max_pages, _ptr(offsets), rows, did, _ptr(k_out), _ptr(v_out))
+    k_out = _out(k_out, "k_out", shape, dtype, k_codes, index, stream)
+    v_out = _out(v_out, "v_out", shape, dtype, k_codes, index, stream)
+    _run_on(index, stream, lib().rz_kv_cache_read, fmt, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+            v_scales.data_ptr(), num_slots, heads, dim, page_len, page_table.data_ptr(), seqs, max_pages, offsets.data_ptr(), rows,
+            did, k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
 
 

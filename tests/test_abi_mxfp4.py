@@ -137,6 +137,9 @@ class Fake:
     def stride(self, i=None):
         return tuple(self._strides) if i is None else self._strides[i]
 
+    def get_device(self):
+        return self.device.index
+
     def is_contiguous(self):
         return tuple(self._strides) == torch.empty(self.shape, device="meta").stride()
 
