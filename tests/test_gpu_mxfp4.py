@@ -246,8 +246,8 @@ def test_gated_quant_is_quant_of_gated(rz, m, n, k):
     same(hc, tc)
 
 
-@pytest.mark.parametrize("n,k", [(1, 256), (37, 512), (100, 3584), (64, 18944)])
-@pytest.mark.parametrize("m", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("n,k", [(1, 256), (37, 512), (100, 3584), (64, 18944), (48, 4096), (5000, 2304)])
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 6, 7, 8])
 def test_gemv(rz, m, n, k):
     w, u = random_tensor(50, n, k, 3), small_scale(random_tensor(51, n, k, 2), 6)
     x = W.act_normal(52 + m, m, k)
