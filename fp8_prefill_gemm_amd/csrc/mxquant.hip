@@ -98,8 +98,9 @@ __global__ __launch_bounds__(kThreads) void mx_pack_kernel(const uint8_t* __rest
                                                            uint32_t slabs, uint8_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales) {
     const TileLane t;
-    const uint64_t tile = blockIdx.x;
-    const uint32_t grp = blockIdx.x / slabs, slab = blockIdx.x % slabs;
+    const uint32_t T = gridDim.x, xcd = blockIdx.x % 8u;
+    const uint64_t tile = xcd * (T / 8u) + (xcd < T % 8u ? xcd : T % 8u) + blockIdx.x / 8u;
+    const uint32_t grp = (uint32_t)tile / slabs, slab = (uint32_t)tile % slabs;
     const uint32_t row = grp * 32u + t.row;
     float v[4][8];
     if (row < n) {
