@@ -80,16 +80,18 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWrite A) {
     }
 }
 
-// A workgroup reads kRows consecutive output rows (tokens): one lane a token
+// A workgroup reads `per` consecutive output rows (tokens): one lane a token
 // finds its sequence (binary search in the offsets) and slot, then the
-// workgroup copies the tokens' heads.
-constexpr int kRows = 32;
+// workgroup copies the tokens' heads, kTurn of them a lane at a time so that
+// their loads are in flight together.
+constexpr int kMaxRows = 64;
+constexpr int kTurn = 4;
 
 template <int FMT, int DT, int L>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead A) {
-    __shared__ int64_t slot_of[kRows];  // -1: zeros, -2: not a row of any sequence
-    const uint32_t row0 = blockIdx.x * kRows;
-    if (threadIdx.x < kRows) {
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead A, uint32_t per) {
+    __shared__ int64_t slot_of[kMaxRows];  // -1: zeros, -2: not a row of any sequence
+    const uint32_t row0 = blockIdx.x * per;
+    if (threadIdx.x < per) {
         const uint32_t row = row0 + threadIdx.x;
         int64_t slot = -2;
         if (row < A.rows && (int64_t)row >= A.offsets[0] && (int64_t)row < A.offsets[A.seqs]) {
@@ -111,47 +113,76 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead A) {
     }
     __syncthreads();
     const int c = blockIdx.y;
-    const uint32_t part = threadIdx.x % L;
+    const uint32_t part = threadIdx.x % L, end = per * A.heads;
     if (part * 8u >= A.dim) return;
-    for (uint32_t i = threadIdx.x / L; i < kRows * A.heads; i += kThreads / L) {
-        const uint32_t t = i / A.heads, head = i % A.heads;
-        const int64_t slot = slot_of[t];
-        if (slot == -2) continue;
-        float v[8] = {};
-        if (slot >= 0) {
-            const uint64_t src = (uint64_t)slot * A.heads + head;
+    for (uint32_t i0 = threadIdx.x / L; i0 < end; i0 += kTurn * (kThreads / L)) {
+        int64_t slot[kTurn];
+        u32x2 w[kTurn];
+        uint32_t sc[kTurn];  // the row's fp32 scale, or the block's byte
+#pragma unroll
+        for (int u = 0; u < kTurn; ++u) {
+            const uint32_t i = i0 + u * (kThreads / L), t = i / A.heads;
+            slot[u] = i < end ? slot_of[t] : -2;
+            w[u] = (u32x2){0u, 0u};
+            sc[u] = 0;  // zeros, where nothing is read
+            if (slot[u] >= 0) {
+                const uint64_t src = (uint64_t)slot[u] * A.heads + (i - t * A.heads);
+                if constexpr (FMT == kKvE4M3) {
+                    w[u] = *reinterpret_cast<const u32x2*>(A.codes[c] + src * A.dim + part * 8u);
+                    sc[u] = static_cast<const uint32_t*>(A.scales[c])[src];
+                } else {
+                    w[u].x = *reinterpret_cast<const uint32_t*>(A.codes[c] + src * (A.dim / 2u) + part * 4u);
+                    sc[u] = static_cast<const uint8_t*>(A.scales[c])[src * (A.dim / 32u) + part / 4u];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kTurn; ++u) {
+            if (slot[u] == -2) continue;
+            float v[8];
             if constexpr (FMT == kKvE4M3) {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(A.codes[c] + src * A.dim + part * 8u);
-                const float s = static_cast<const float*>(A.scales[c])[src];
+                const float s = __uint_as_float(sc[u]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
-                    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+                    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][j], false);
+                    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][j], true);
                     v[4 * j] = a.x * s;
                     v[4 * j + 1] = a.y * s;
                     v[4 * j + 2] = b.x * s;
                     v[4 * j + 3] = b.y * s;
                 }
             } else {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(A.codes[c] + src * (A.dim / 2u) + part * 4u);
-                const uint32_t byte = static_cast<const uint8_t*>(A.scales[c])[src * (A.dim / 32u) + part / 4u];
-                decode8(w, v);
+                decode8(w[u].x, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = times_scale(v[j], byte);
+                for (int j = 0; j < 8; ++j) v[j] = times_scale(v[j], sc[u]);
             }
+            const uint64_t i = i0 + u * (kThreads / L);  // (row - row0) * heads + head
+            store8<DT>(A.out[c], ((uint64_t)row0 * A.heads + i) * A.dim + part * 8u, v);
         }
-        store8<DT>(A.out[c], ((uint64_t)(row0 + t) * A.heads + head) * A.dim + part * 8u, v);
     }
 }
 
+// Tokens a reading workgroup takes: one turn of its lanes (1024 items of
+// eight values), halved while that leaves fewer than 512 workgroups a tensor
+// (E4M3, heads 4 x dim 128, us at 8 / 16 / 32 tokens: 4096 rows 4.7 / 4.9 /
+// 6.2; 16384 rows 10.8 / 9.7 / 10.9; 131072 rows 100 / 81 / 84, of which 81
+// is 5.0 TB/s).
+uint32_t rows_per_group(const KvRead& A, uint32_t lanes) {
+    uint32_t per = kMaxRows;
+    while (per > 4u && (uint64_t)per * A.heads * lanes > 1024u) per >>= 1;
+    while (per > 8u && A.rows / per < 512u) per >>= 1;
+    return per;
+}
+
 template <int FMT, int L>
-void read_as(const KvRead& A, int dtype, dim3 grid, hipStream_t st) {
+void read_as(const KvRead& A, int dtype, uint32_t per, hipStream_t st) {
+    const dim3 grid((A.rows + per - 1) / per, 2);
     if (dtype == kF32)
-        kv_read_kernel<FMT, kF32, L><<<grid, kThreads, 0, st>>>(A);
+        kv_read_kernel<FMT, kF32, L><<<grid, kThreads, 0, st>>>(A, per);
     else if (dtype == kF16)
-        kv_read_kernel<FMT, kF16, L><<<grid, kThreads, 0, st>>>(A);
+        kv_read_kernel<FMT, kF16, L><<<grid, kThreads, 0, st>>>(A, per);
     else
-        kv_read_kernel<FMT, kBF16, L><<<grid, kThreads, 0, st>>>(A);
+        kv_read_kernel<FMT, kBF16, L><<<grid, kThreads, 0, st>>>(A, per);
 }
 
 // Calls f(integral_constant<L>) with the fewest lanes that hold dim values.
@@ -185,11 +216,11 @@ hipError_t launch_kv_write(int format, const KvWrite& A, hipStream_t st) {
 hipError_t launch_kv_read(int format, const KvRead& A, int dtype, hipStream_t st) {
     with_lanes(A.dim, [&](auto l) {
         constexpr int L = decltype(l)::value;
-        const dim3 grid((A.rows + kRows - 1) / kRows, 2);
+        const uint32_t per = rows_per_group(A, L);
         if (format == kKvE4M3)
-            read_as<kKvE4M3, L>(A, dtype, grid, st);
+            read_as<kKvE4M3, L>(A, dtype, per, st);
         else
-            read_as<kKvMXFP4, L>(A, dtype, grid, st);
+            read_as<kKvMXFP4, L>(A, dtype, per, st);
     });
     return hipGetLastError();
 }

@@ -95,7 +95,8 @@ def filled(fmt, slots, heads, dim, seed):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("page,lens,heads,dim", [(1, [3], 1, 32), (16, [1, 0, 33, 16], 4, 128), (7, [20, 5, 7], 3, 96), (64, [100], 2, 256), (5, [9, 40], 1, 512)])
+@pytest.mark.parametrize("page,lens,heads,dim", [(1, [3], 1, 32), (16, [1, 0, 33, 16], 4, 128), (7, [20, 5, 7], 3, 96), (64, [100], 2, 256), (5, [9, 40], 1, 512),
+                                                  (16, [700, 1, 5000, 3000], 1, 64), (3, [9], 70, 32)])
 def test_read(rz, fmt, page, lens, heads, dim):
     """Pages that end inside the batch, empty sequences, a row before and rows behind the sequences left as they were."""
     need = [max(1, -(-n // page)) for n in lens]
