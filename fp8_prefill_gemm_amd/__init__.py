@@ -447,169 +447,107 @@ def rz_fp16_gemm(a_f16, w_f16, m: int, y=None, stream=None):
 
 # MXFP4 tensors are pairs (codes, scales) of uint8 tensors in the tiled layout
 # of include/rz_fp8.h: codes [rows/32][k/64][1024], scales [rows/32][k/256][256].
-# The kernels below take a few microseconds, so their wrappers check in few
-# steps and read the current stream without building a torch object for it.
+# The kernels of the functions below take a few microseconds on small batches,
+# so their arguments are checked and marshalled in C++ (csrc/native.cpp):
+# wrong types, shapes, strides or devices raise ValueError (TypeError for what
+# is no tensor), a refusal of the library RzError.  Outputs that are not passed
+# in are allocated on the call's stream.
+
+_native_mod = None
+
+
+def _native():
+    """The native half of the binding (loaded once; raises if it has not been built)."""
+    global _native_mod
+    if _native_mod is None:
+        import importlib.machinery
+        import importlib.util
+        lib()
+        _torch()
+        path = _build.NATIVE_PATH
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing: build it with `python -m fp8_prefill_gemm_amd.build`; there is no fallback implementation")
+        loader = importlib.machinery.ExtensionFileLoader("_rz_native", path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_rz_native", path, loader=loader))
+        loader.exec_module(mod)
+        mod.set_error(RzError)
+        _native_mod = mod
+    return _native_mod
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
+
 
 def rz_mxfp4_pad_rows(rows: int) -> int:
     return (rows + 31) // 32 * 32
 
 
-def _refuse(t, what, dtype, shape, index):
-    want = f"a contiguous {dtype} tensor of shape {tuple(shape)} on device {index}"
-    raise ValueError(f"{what}: expected {want}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
-def _need(t, what, dtype, shape, index):
-    """Raise unless t is a contiguous tensor of this dtype and shape on GPU `index`."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-        _refuse(t, what, dtype, shape, index)
-
-
-def _gpu(t, what):
-    """The GPU index of t."""
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{what}: rz_fp8 works on device (cuda/hip) tensors only")
-    return index
-
-
-def _out(t, what, shape, dtype, like, index, stream):
-    """t, checked, or a new output on the call's stream (see _empty)."""
-    if t is not None:
-        _need(t, what, dtype, shape, index)
-        return t
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    return _empty(shape, dtype, like.device, stream)
-
-
-_raw_stream = None
-
-
-def _run_on(index, stream, fn, *args):
-    """Call entry point `fn` with `args` and the stream on GPU `index`."""
-    global _raw_stream
-    torch = _torch()
-    if stream is not None:
-        handle = stream.cuda_stream
-    else:
-        if _raw_stream is None:
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-                lambda i: torch.cuda.current_stream(i).cuda_stream)
-        handle = _raw_stream(index)
-    if torch.cuda.current_device() == index:
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, handle)
-    if status:
-        _check(status)
-
-
-def _mx(codes, scales, rows, what, index):
-    """k of the MXFP4 tensor (codes, scales) of `rows` rows, checked."""
-    u8 = _torch().uint8
-    shape = codes.shape
-    slabs = shape[1] if len(shape) == 3 else 0
-    g = (rows + 31) // 32
-    _need(codes, what + " codes", u8, (g, slabs, 1024), index)
-    _need(scales, what + " scales", u8, (g, slabs // 4, 256), index)
-    return slabs * 64
-
-
-def _mx_out(rows, k, codes, scales, what, like, index, stream):
+def _mx_empty(rows, k, codes, scales, device, stream):
+    """The outputs of a call on another stream than the current one."""
     u8 = _torch().uint8
     g = (rows + 31) // 32
-    return (_out(codes, what + " codes", (g, k // 64, 1024), u8, like, index, stream),
-            _out(scales, what + " scales", (g, k // 256, 256), u8, like, index, stream))
+    return (_empty((g, k // 64, 1024), u8, device, stream) if codes is None else codes,
+            _empty((g, k // 256, 256), u8, device, stream) if scales is None else scales)
 
 
 def rz_mxfp4_quant(x, codes=None, scales=None, stream=None):
     """x fp32 [m][k] -> MXFP4 (codes, scales), pad rows included."""
-    index = _gpu(x, "x")
-    m, k = x.shape
-    _need(x, "x", _torch().float32, (m, k), index)
-    codes, scales = _mx_out(m, k, codes, scales, "output", x, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_quant, x.data_ptr(), m, k, codes.data_ptr(), scales.data_ptr())
-    return codes, scales
+    if stream is not None:
+        codes, scales = _mx_empty(*x.shape, codes, scales, x.device, stream)
+    return _native().mxfp4_quant(x, codes, scales, _handle(stream))
 
 
 def rz_mxfp4_pack_weight(qtype: int, blocks, n: int, k: int, codes=None, scales=None, stream=None):
     """A K-quant weight -> MXFP4 (codes, scales)."""
-    index = _gpu(blocks, "blocks")
-    _need(blocks, "blocks", _torch().uint8, blocks.shape, index)
-    if blocks.numel() < rz_weight_bytes(qtype, n, k):
-        raise ValueError(f"blocks: {blocks.numel()} bytes, {rz_weight_bytes(qtype, n, k)} needed")
-    codes, scales = _mx_out(n, k, codes, scales, "output", blocks, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_pack_weight, qtype, blocks.data_ptr(), n, k, codes.data_ptr(), scales.data_ptr())
-    return codes, scales
+    if stream is not None:
+        codes, scales = _mx_empty(n, k, codes, scales, blocks.device, stream)
+    return _native().mxfp4_pack_weight(qtype, blocks, n, k, codes, scales, _handle(stream))
+
+
+_DTYPES = {}
 
 
 def _dtype_id(dtype):
-    torch = _torch()
-    ids = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    if dtype not in ids:
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    if dtype not in _DTYPES:
         raise ValueError(f"dtype: expected float32, float16 or bfloat16, got {dtype}")
-    return ids[dtype]
+    return _DTYPES[dtype]
 
 
 def rz_mxfp4_dequant(codes, scales, rows: int, out=None, dtype=None, stream=None):
     """MXFP4 -> out [rows][k] of dtype (default: out's, or float32)."""
-    index = _gpu(codes, "codes")
-    k = _mx(codes, scales, rows, "input", index)
     if dtype is None:
         dtype = _torch().float32 if out is None else out.dtype
-    did = _dtype_id(dtype)
-    out = _out(out, "out", (rows, k), dtype, codes, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_dequant, codes.data_ptr(), scales.data_ptr(), rows, k, did, out.data_ptr())
-    return out
+    if stream is not None and out is None:
+        out = _empty((rows, codes.shape[1] * 64), dtype, codes.device, stream)
+    return _native().mxfp4_dequant(codes, scales, rows, out, _dtype_id(dtype), _handle(stream))
 
 
 def rz_mxfp4_gemm(a_codes, a_scales, m: int, w_codes, w_scales, n: int, y=None, stream=None):
     """-> y fp32 [m][n] = a @ w^T of MXFP4 a [m][k] and w [n][k]."""
-    index = _gpu(a_codes, "a codes")
-    k = _mx(a_codes, a_scales, m, "a", index)
-    if _mx(w_codes, w_scales, n, "w", index) != k:
-        raise ValueError(f"a has k={k}, w has k={w_codes.shape[1] * 64}")
-    y = _out(y, "y", (m, n), _torch().float32, a_codes, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_gemm, a_codes.data_ptr(), a_scales.data_ptr(), m, w_codes.data_ptr(),
-            w_scales.data_ptr(), n, k, y.data_ptr())
-    return y
-
-
-def _gate_up(gate, up, n, index):
-    """(k, pointers) of the gate and up weights, checked."""
-    (gc, gs), (uc, us) = gate, up
-    k = _mx(gc, gs, n, "gate", index)
-    if _mx(uc, us, n, "up", index) != k:
-        raise ValueError(f"gate has k={k}, up has k={uc.shape[1] * 64}")
-    return k, (gc.data_ptr(), gs.data_ptr(), uc.data_ptr(), us.data_ptr())
-
-
-def _gated_args(a_codes, a_scales, m, gate, up, n):
-    index = _gpu(a_codes, "a codes")
-    k, weights = _gate_up(gate, up, n, index)
-    if _mx(a_codes, a_scales, m, "a", index) != k:
-        raise ValueError(f"a has k={a_codes.shape[1] * 64}, gate and up have k={k}")
-    return index, (a_codes.data_ptr(), a_scales.data_ptr(), m, *weights, n, k)
+    if stream is not None and y is None:
+        y = _empty((m, n), _torch().float32, a_codes.device, stream)
+    return _native().mxfp4_gemm(a_codes, a_scales, m, w_codes, w_scales, n, y, _handle(stream))
 
 
 def rz_mxfp4_gated(a_codes, a_scales, m: int, gate, up, n: int, h=None, stream=None):
     """-> h fp32 [m][n] = silu(a @ gate^T) * (a @ up^T); gate and up are
     MXFP4 (codes, scales) pairs of [n][k]."""
-    index, args = _gated_args(a_codes, a_scales, m, gate, up, n)
-    h = _out(h, "h", (m, n), _torch().float32, a_codes, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_gated, *args, h.data_ptr())
-    return h
+    if stream is not None and h is None:
+        h = _empty((m, n), _torch().float32, a_codes.device, stream)
+    return _native().mxfp4_gated(a_codes, a_scales, m, *gate, *up, n, h, _handle(stream))
 
 
 def rz_mxfp4_gated_quant(a_codes, a_scales, m: int, gate, up, n: int, h_codes=None, h_scales=None, stream=None):
     """rz_mxfp4_gated with its result as MXFP4 -> (h_codes, h_scales), the
     down projection's operand (n a multiple of 256)."""
-    index, args = _gated_args(a_codes, a_scales, m, gate, up, n)
-    h_codes, h_scales = _mx_out(m, n, h_codes, h_scales, "h", a_codes, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_gated_quant, *args, h_codes.data_ptr(), h_scales.data_ptr())
-    return h_codes, h_scales
+    if stream is not None:
+        h_codes, h_scales = _mx_empty(m, n, h_codes, h_scales, a_codes.device, stream)
+    return _native().mxfp4_gated_quant(a_codes, a_scales, m, *gate, *up, n, h_codes, h_scales, _handle(stream))
 
 
 MXFP4_GEMV_MAX_M = 8
@@ -617,75 +555,29 @@ MXFP4_GEMV_MAX_M = 8
 
 def rz_mxfp4_gemv(w_codes, w_scales, n: int, x, y=None, stream=None):
     """-> y fp32 [m][n] = x @ w^T, x fp32 [m][k] with m <= MXFP4_GEMV_MAX_M."""
-    index = _gpu(x, "x")
-    k = _mx(w_codes, w_scales, n, "w", index)
-    m = x.shape[0]
-    f32 = _torch().float32
-    _need(x, "x", f32, (m, k), index)
-    y = _out(y, "y", (m, n), f32, x, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_gemv, w_codes.data_ptr(), w_scales.data_ptr(), n, k, x.data_ptr(), m, y.data_ptr())
-    return y
+    if stream is not None and y is None:
+        y = _empty((x.shape[0], n), _torch().float32, x.device, stream)
+    return _native().mxfp4_gemv(w_codes, w_scales, n, x, y, _handle(stream))
 
 
 def rz_mxfp4_gated_gemv(gate, up, n: int, x, h=None, stream=None):
     """-> h fp32 [m][n] = silu(x @ gate^T) * (x @ up^T), x fp32 [m][k] with
     m <= MXFP4_GEMV_MAX_M."""
-    index = _gpu(x, "x")
-    k, weights = _gate_up(gate, up, n, index)
-    m = x.shape[0]
-    f32 = _torch().float32
-    _need(x, "x", f32, (m, k), index)
-    h = _out(h, "h", (m, n), f32, x, index, stream)
-    _run_on(index, stream, lib().rz_mxfp4_gated_gemv, *weights, n, k, x.data_ptr(), m, h.data_ptr())
-    return h
+    if stream is not None and h is None:
+        h = _empty((x.shape[0], n), _torch().float32, x.device, stream)
+    return _native().mxfp4_gated_gemv(*gate, *up, n, x, h, _handle(stream))
 
 
 KV_E4M3, KV_MXFP4 = 0, 1
 
 
-def _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales):
-    """(num_slots, heads, dim, GPU index) of a cache, its tensors checked."""
-    torch = _torch()
-    if fmt not in (KV_E4M3, KV_MXFP4):
-        raise ValueError(f"fmt: expected KV_E4M3 or KV_MXFP4, got {fmt}")
-    if k_codes.dim() != 3:
-        raise ValueError(f"k_codes: expected 3 dimensions, got {tuple(k_codes.shape)}")
-    index = _gpu(k_codes, "k_codes")
-    shape = slots, heads, width = k_codes.shape
-    if fmt == KV_E4M3:
-        dim, sdtype, sshape = width, torch.float32, (slots, heads)
-    else:
-        dim, sdtype, sshape = 2 * width, torch.uint8, (slots, heads, width // 16)
-    _need(k_codes, "k_codes", torch.uint8, shape, index)
-    _need(v_codes, "v_codes", torch.uint8, shape, index)
-    _need(k_scales, "k_scales", sdtype, sshape, index)
-    _need(v_scales, "v_scales", sdtype, sshape, index)
-    return slots, heads, dim, index
-
-
-def _kv_rows(t, what, shape, index):
-    """The token stride of t, fp32 [tokens][heads][dim] with contiguous tokens."""
-    stride = t.stride()
-    tokens, heads, dim = shape
-    if t.dtype is not _torch().float32 or t.shape != shape or t.get_device() != index or (
-            tokens and (stride[2] != 1 or (heads > 1 and stride[1] != dim))):
-        raise ValueError(f"{what}: expected float32 {tuple(shape)} with contiguous tokens on device {index}, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {stride} on {t.device}")
-    return stride[0] if tokens > 1 else heads * dim  # free where there is one token
-
-
 def rz_kv_cache_write(fmt: int, k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
     """Quantise k and v, fp32 [tokens][heads][dim] (tokens may be strided),
-    into the cache rows `slots` (int64 [tokens]; out of range: dropped)."""
-    num_slots, heads, dim, index = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
-    tokens = k.shape[0]
-    k_stride = _kv_rows(k, "k", (tokens, heads, dim), index)
-    v_stride = _kv_rows(v, "v", (tokens, heads, dim), index)
-    if min(k_stride, v_stride) < heads * dim:
-        raise ValueError(f"token strides {k_stride} and {v_stride}: at least heads*dim={heads * dim} expected")
-    _need(slots, "slots", _torch().int64, (tokens,), index)
-    _run_on(index, stream, lib().rz_kv_cache_write, fmt, k.data_ptr(), v.data_ptr(), tokens, heads, dim, k_stride, v_stride,
-            slots.data_ptr(), num_slots, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr())
+    into the cache rows `slots` (int64 [tokens]; out of range: dropped).
+    Cache: codes uint8 [slots][heads][dim] and scales float32 [slots][heads]
+    (KV_E4M3), or uint8 [slots][heads][dim/2] and [slots][heads][dim/32]
+    (KV_MXFP4)."""
+    _native().kv_cache_write(fmt, k, v, slots, k_codes, k_scales, v_codes, v_scales, _handle(stream))
 
 
 def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: int, page_table, offsets, rows: int,
@@ -695,25 +587,15 @@ def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: i
     page_table int32 [seqs][max_pages]; offsets int32 [seqs + 1]: sequence b
     is rows offsets[b] .. offsets[b+1] - 1.  Rows of no sequence are left as
     they are (undefined in a new output)."""
-    torch = _torch()
-    num_slots, heads, dim, index = _kv_cache(fmt, k_codes, k_scales, v_codes, v_scales)
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table: expected 2 dimensions, got {tuple(page_table.shape)}")
-    seqs, max_pages = page_table.shape
-    _need(page_table, "page_table", torch.int32, page_table.shape, index)
-    _need(offsets, "offsets", torch.int32, (seqs + 1,), index)
-    if page_len < 1 or rows < 0:
-        raise ValueError(f"page_len={page_len} must be positive and rows={rows} not negative")
     if dtype is None:
-        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.float32
+        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else _torch().float32
     did = _dtype_id(dtype)
-    shape = (rows, heads, dim)
-    k_out = _out(k_out, "k_out", shape, dtype, k_codes, index, stream)
-    v_out = _out(v_out, "v_out", shape, dtype, k_codes, index, stream)
-    _run_on(index, stream, lib().rz_kv_cache_read, fmt, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-            v_scales.data_ptr(), num_slots, heads, dim, page_len, page_table.data_ptr(), seqs, max_pages, offsets.data_ptr(), rows,
-            did, k_out.data_ptr(), v_out.data_ptr())
-    return k_out, v_out
+    if stream is not None:
+        shape = (rows, k_codes.shape[1], k_codes.shape[2] * (1 if fmt == KV_E4M3 else 2))
+        k_out = _empty(shape, dtype, k_codes.device, stream) if k_out is None else k_out
+        v_out = _empty(shape, dtype, k_codes.device, stream) if v_out is None else v_out
+    return _native().kv_cache_read(fmt, k_codes, k_scales, v_codes, v_scales, page_len, page_table, offsets, rows, k_out, v_out, did,
+                                   _handle(stream))
 
 
 def rz_dequant_f32(qtype: int, blocks, n: int, k: int, out=None, stream=None):

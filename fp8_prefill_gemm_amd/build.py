@@ -1,4 +1,5 @@
-"""Ahead-of-time build of librz_fp8.so for gfx950 (hipcc, in-tree).
+"""Ahead-of-time build of librz_fp8.so for gfx950 (hipcc, in-tree) and of the
+binding's native half (g++, against torch and that library).
 
 The library is the product: HIP kernels plus the C ABI declared in
 include/rz_fp8.h.  It is compiled for gfx950 only, without fast-math, with
@@ -7,9 +8,11 @@ instructions disabled.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -19,6 +22,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "kquant.hip", "actquant.hip", "gemm.hip", "gemm_edge.hip", "kgemv.hip", "kqgemm.hip",
            "q8gemm.hip", "mxquant.hip", "mxgemm.hip", "mxgemv.hip", "kvcache.hip"]
 ARCH = "gfx950"
+NATIVE_NAME = "_rz_native.so"
+NATIVE_PATH = os.path.join(PKG_DIR, NATIVE_NAME)
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -41,7 +46,8 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into LIB_PATH (always rebuilds)."""
+    """Compile every HIP source into LIB_PATH and the native half of the
+    binding into NATIVE_PATH (always rebuilds)."""
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), *srcs, "-o", tmp]
@@ -56,7 +62,30 @@ def build(verbose: bool = False) -> str:
     if verbose and msgs:
         print("\n".join(msgs), flush=True)
     os.replace(tmp, LIB_PATH)
+    build_native(verbose)
     return LIB_PATH
+
+
+def build_native(verbose: bool = False) -> str:
+    """csrc/native.cpp -> NATIVE_PATH, linked to the library beside it."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = NATIVE_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(rocm, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "native.cpp"), "-o", tmp,
+           "-L", PKG_DIR, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, NATIVE_PATH)
+    return NATIVE_PATH
 
 
 if __name__ == "__main__":

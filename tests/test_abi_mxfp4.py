@@ -121,90 +121,101 @@ def test_kv_read(L):
     assert L.rz_kv_cache_read(*(good[:13] + [0] + good[14:])) == OK
 
 
-class Fake:
-    """Enough of a device tensor for the binding's checks."""
-
-    def __init__(self, dtype, *shape, strides=None, device="cuda:0"):
-        self.dtype, self.shape, self.device, self.is_cuda = dtype, torch.Size(shape), torch.device(device), True
-        self._strides = strides or torch.empty(shape, device="meta").stride()
-
-    def dim(self):
-        return len(self.shape)
-
-    def numel(self):
-        return self.shape.numel()
-
-    def stride(self, i=None):
-        return tuple(self._strides) if i is None else self._strides[i]
-
-    def get_device(self):
-        return self.device.index
-
-    def is_contiguous(self):
-        return tuple(self._strides) == torch.empty(self.shape, device="meta").stride()
-
-    def data_ptr(self):
-        return P
-
-
+# The binding's checks of a CPU tensor end with the one for a device, so what
+# they say before it can be tested here: every call below names its own fault.
 F32, U8, I32, I64 = torch.float32, torch.uint8, torch.int32, torch.int64
 
 
-def mx(rows, k, **kw):
+def mx(rows, k):
     g = (rows + 31) // 32
-    return Fake(U8, g, k // 64, 1024, **kw), Fake(U8, g, k // 256, 256, **kw)
+    return torch.zeros(g, k // 64, 1024, dtype=U8), torch.zeros(g, k // 256, 256, dtype=U8)
 
 
-def test_binding_refuses(L):
-    a, w, o = mx(37, 512), mx(70, 512), Fake(F32, 37, 70)
-    bad = [
-        lambda: rz.rz_mxfp4_quant(torch.zeros(2, 256)),
-        lambda: rz.rz_mxfp4_quant(Fake(torch.bfloat16, 2, 256), *mx(2, 256)),
-        lambda: rz.rz_mxfp4_quant(Fake(F32, 2, 256, strides=(512, 1)), *mx(2, 256)),
-        lambda: rz.rz_mxfp4_quant(Fake(F32, 33, 256), *mx(2, 256)),
-        lambda: rz.rz_mxfp4_pack_weight(12, Fake(U8, 143), 1, 256, *mx(1, 256)),
-        lambda: rz.rz_mxfp4_dequant(*a, 65, out=Fake(F32, 65, 512)),
-        lambda: rz.rz_mxfp4_dequant(*a, 37, dtype=torch.float64),
-        lambda: rz.rz_mxfp4_dequant(*a, 37, out=Fake(F32, 36, 512)),
-        lambda: rz.rz_mxfp4_gemm(*a, 70, *w, 70, y=o),
-        lambda: rz.rz_mxfp4_gemm(*a, 37, *w, 37, y=Fake(F32, 37, 37)),
-        lambda: rz.rz_mxfp4_gemm(*a, 37, *mx(70, 768), 70, y=o),
-        lambda: rz.rz_mxfp4_gemm(a[0], mx(37, 768)[1], 37, *w, 70, y=o),
-        lambda: rz.rz_mxfp4_gemm(*a, 37, *w, 70, y=Fake(F32, 70, 37)),
-        lambda: rz.rz_mxfp4_gemm(*a, 37, *mx(70, 512, device="cuda:1"), 70, y=o),
-        lambda: rz.rz_mxfp4_gated(*a, 37, w, mx(70, 256), 70, h=o),
-        lambda: rz.rz_mxfp4_gated(*a, -1, w, w, 70, h=o),
-        lambda: rz.rz_mxfp4_gated_quant(*a, 37, mx(256, 512), mx(256, 512), 256, *mx(65, 256)),
-        lambda: rz.rz_mxfp4_gemv(*w, 70, Fake(F32, 2, 256), y=Fake(F32, 2, 70)),
-        lambda: rz.rz_mxfp4_gated_gemv(w, mx(70, 768), 70, Fake(F32, 2, 512), h=Fake(F32, 2, 70)),
-    ]
-    for i, f in enumerate(bad):
-        with pytest.raises(ValueError):
-            f()
-            pytest.fail(f"case {i} was not refused")
+def f32(*shape):
+    return torch.zeros(*shape)
 
 
-def test_binding_refuses_cache(L):
-    c = [Fake(U8, 10, 2, 64), Fake(F32, 10, 2)] * 2
-    k, slots = Fake(F32, 3, 2, 64), Fake(I64, 3)
-    t, off = Fake(I32, 2, 4), Fake(I32, 3)
-    bad = [
-        lambda: rz.rz_kv_cache_write(2, k, k, slots, *c),
-        lambda: rz.rz_kv_cache_write(1, k, k, slots, *c),
-        lambda: rz.rz_kv_cache_write(0, k, Fake(F32, 4, 2, 64), slots, *c),
-        lambda: rz.rz_kv_cache_write(0, k, k, Fake(I32, 3), *c),
-        lambda: rz.rz_kv_cache_write(0, k, k, Fake(I64, 2), *c),
-        lambda: rz.rz_kv_cache_write(0, k, Fake(F32, 3, 2, 64, strides=(128, 1, 2)), slots, *c),
-        lambda: rz.rz_kv_cache_write(0, Fake(torch.float16, 3, 2, 64), k, slots, *c),
-        lambda: rz.rz_kv_cache_write(0, k, k, slots, c[0], Fake(F32, 10, 2, 1), c[2], c[3]),
-        lambda: rz.rz_kv_cache_read(0, *c, 16, t, Fake(I32, 2), 5),
-        lambda: rz.rz_kv_cache_read(0, *c, 16, Fake(I64, 2, 4), off, 5),
-        lambda: rz.rz_kv_cache_read(0, *c, 0, t, off, 5),
-        lambda: rz.rz_kv_cache_read(0, *c, 16, t, off, -1),
-        lambda: rz.rz_kv_cache_read(0, *c, 16, t, off, 5, Fake(F32, 5, 2, 32), Fake(F32, 5, 2, 32)),
-        lambda: rz.rz_kv_cache_read(0, *c, 16, t, off, 5, Fake(F32, 5, 2, 64), Fake(torch.float16, 5, 2, 64)),
-    ]
-    for i, f in enumerate(bad):
-        with pytest.raises(ValueError):
-            f()
-            pytest.fail(f"case {i} was not refused")
+A, X = mx(37, 512), f32(37, 512)
+Wt = mx(70, 512)
+
+ACCEPTED = [
+    lambda: rz.rz_mxfp4_quant(X),
+    lambda: rz.rz_mxfp4_quant(X, *A),
+    lambda: rz.rz_mxfp4_pack_weight(12, torch.zeros(2 * 2, 144, dtype=U8), 2, 512),
+    lambda: rz.rz_mxfp4_dequant(*A, 37, dtype=torch.bfloat16),
+    lambda: rz.rz_mxfp4_gemm(*A, 37, *Wt, 70),
+    lambda: rz.rz_mxfp4_gated(*A, 37, Wt, Wt, 70),
+    lambda: rz.rz_mxfp4_gated_quant(*A, 37, mx(256, 512), mx(256, 512), 256),
+    lambda: rz.rz_mxfp4_gemv(*Wt, 70, f32(2, 512)),
+    lambda: rz.rz_mxfp4_gated_gemv(Wt, Wt, 70, f32(2, 512)),
+]
+
+REFUSED = [
+    ("x: expected a contiguous Float", lambda: rz.rz_mxfp4_quant(torch.zeros(2, 256, dtype=torch.bfloat16))),
+    ("x: expected a contiguous Float", lambda: rz.rz_mxfp4_quant(f32(2, 512)[:, :256])),
+    ("x: expected 2 dimensions", lambda: rz.rz_mxfp4_quant(f32(2, 2, 256))),
+    ("blocks: 143 bytes, 144 needed", lambda: rz.rz_mxfp4_pack_weight(12, torch.zeros(143, dtype=U8), 1, 256)),
+    ("n=-1", lambda: rz.rz_mxfp4_pack_weight(12, torch.zeros(144, dtype=U8), -1, 256)),
+    ("blocks: expected a contiguous Byte", lambda: rz.rz_mxfp4_pack_weight(12, torch.zeros(144), 1, 256)),
+    ("input: expected a contiguous Byte", lambda: rz.rz_mxfp4_dequant(*A, 65)),
+    ("dtype: expected float32, float16 or bfloat16", lambda: rz.rz_mxfp4_dequant(*A, 37, dtype=torch.float64)),
+    ("a: expected a contiguous Byte", lambda: rz.rz_mxfp4_gemm(*A, 70, *Wt, 70)),
+    ("w: expected a contiguous Byte", lambda: rz.rz_mxfp4_gemm(*A, 37, *Wt, 37)),
+    ("w: expected a contiguous Byte", lambda: rz.rz_mxfp4_gemm(*A, 37, Wt[0].view(-1), Wt[1], 70)),
+    ("operands have k=512 and k=768", lambda: rz.rz_mxfp4_gemm(*A, 37, *mx(70, 768), 70)),
+    ("a: expected a contiguous Byte", lambda: rz.rz_mxfp4_gemm(A[0], mx(37, 768)[1], 37, *Wt, 70)),
+    ("m=-1", lambda: rz.rz_mxfp4_gemm(*A, -1, *Wt, 70)),
+    ("m=4294967296", lambda: rz.rz_mxfp4_gemm(*A, 1 << 32, *Wt, 70)),
+    ("operands have k=512 and k=256", lambda: rz.rz_mxfp4_gated(*A, 37, Wt, mx(70, 256), 70)),
+    ("a: expected a contiguous Byte", lambda: rz.rz_mxfp4_gated_quant(*mx(65, 512), 37, mx(256, 512), mx(256, 512), 256)),
+    ("x: expected a contiguous Float", lambda: rz.rz_mxfp4_gemv(*Wt, 70, f32(2, 256))),
+    ("x: expected a contiguous Float", lambda: rz.rz_mxfp4_gemv(*Wt, 70, f32(512))),
+    ("operands have k=512 and k=768", lambda: rz.rz_mxfp4_gated_gemv(Wt, mx(70, 768), 70, f32(2, 512))),
+]
+
+C = [torch.zeros(10, 2, 64, dtype=U8), f32(10, 2)] * 2
+K, SL = f32(3, 2, 64), torch.zeros(3, dtype=I64)
+TAB, OFF = torch.zeros(2, 4, dtype=I32), torch.zeros(3, dtype=I32)
+
+ACCEPTED += [
+    lambda: rz.rz_kv_cache_write(0, K, f32(3, 256)[:, 128:].view(3, 2, 64), SL, *C),
+    lambda: rz.rz_kv_cache_read(0, *C, 16, TAB, OFF, 5, dtype=torch.float16),
+]
+REFUSED += [
+    ("fmt=2", lambda: rz.rz_kv_cache_write(2, K, K, SL, *C)),
+    ("k_scales: expected a contiguous Byte", lambda: rz.rz_kv_cache_write(1, K, K, SL, *C)),
+    ("k_scales: expected a contiguous Float", lambda: rz.rz_kv_cache_write(0, K, K, SL, C[0], f32(10, 2, 1), *C[2:])),
+    ("v_codes: expected a contiguous Byte", lambda: rz.rz_kv_cache_write(0, K, K, SL, *C[:2], C[0][:9], C[1])),
+    ("v: expected a contiguous Float", lambda: rz.rz_kv_cache_write(0, K, f32(4, 2, 64), SL, *C)),
+    ("k: expected a contiguous Float", lambda: rz.rz_kv_cache_write(0, f32(3, 64, 2).transpose(1, 2), K, SL, *C)),
+    ("k: expected a contiguous Float", lambda: rz.rz_kv_cache_write(0, f32(1, 2, 64).expand(3, 2, 64), K, SL, *C)),
+    ("k: expected a contiguous Float", lambda: rz.rz_kv_cache_write(0, K.half(), K, SL, *C)),
+    ("slots: expected a contiguous Long", lambda: rz.rz_kv_cache_write(0, K, K, SL.int(), *C)),
+    ("slots: expected a contiguous Long", lambda: rz.rz_kv_cache_write(0, K, K, SL[:2], *C)),
+    ("offsets: expected a contiguous Int", lambda: rz.rz_kv_cache_read(0, *C, 16, TAB, OFF[:2], 5)),
+    ("page_table: expected a contiguous Int", lambda: rz.rz_kv_cache_read(0, *C, 16, TAB.long(), OFF, 5)),
+    ("page_table: expected 2 dimensions", lambda: rz.rz_kv_cache_read(0, *C, 16, TAB[0], OFF, 5)),
+    ("page_len=0", lambda: rz.rz_kv_cache_read(0, *C, 0, TAB, OFF, 5)),
+    ("rows=-1", lambda: rz.rz_kv_cache_read(0, *C, 16, TAB, OFF, -1)),
+    ("dtype: expected", lambda: rz.rz_kv_cache_read(0, *C, 16, TAB, OFF, 5, dtype=torch.float64)),
+]
+
+
+@pytest.mark.parametrize("i", range(len(ACCEPTED)))
+def test_binding_wants_a_device(L, i):
+    with pytest.raises(ValueError, match="works on device"):
+        ACCEPTED[i]()
+
+
+@pytest.mark.parametrize("i", range(len(REFUSED)))
+def test_binding_refuses(L, i):
+    with pytest.raises(ValueError) as e:
+        REFUSED[i][1]()
+    assert str(e.value).startswith(REFUSED[i][0]) or REFUSED[i][0] in str(e.value)
+
+
+def test_binding_wants_tensors(L):
+    with pytest.raises(TypeError, match="x: expected a tensor, got list"):
+        rz.rz_mxfp4_quant([1.0])
+    with pytest.raises(TypeError):
+        rz.rz_mxfp4_gemm(*A, 37.0, *Wt, 70)
