@@ -63,12 +63,13 @@ __device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], 1.0f, 3);
 }
 
-// The eight E2M1 values (not yet times X) of a word of codes.
-__device__ __forceinline__ void decode8(uint32_t w, float (&v)[8]) {
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+// The eight E2M1 values of a word of codes, times `scale` (a power of two or
+// NaN; 1 gives the values not yet times X).
+__device__ __forceinline__ void decode8(uint32_t w, float (&v)[8], float scale = 1.0f) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
     v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
 }

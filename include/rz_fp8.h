@@ -496,8 +496,12 @@ int rz_mxfp4_gated_quant(const uint8_t* a_codes, const uint8_t* a_scales, uint32
  * quantised:  y = x w^T  and  h = silu(x gate^T) * (x up^T)
  *   x   device, fp32 [m][k] row-major, m <= RZ_MXFP4_GEMV_MAX_M
  *   y, h   device out, fp32 [m][n] row-major
- * fp32 multiply-adds: |y - exact| <= gamma_{k + k/32} sum |x w|, gamma_t =
- * t u / (1 - t u), u = 2^-24.  m == 0 or n == 0 is a no-op.
+ * Products are exact, sums fp32: |y - exact| <= gamma_{2 (k + k/32)} sum |x w|,
+ * gamma_t = t u / (1 - t u), u = 2^-24.  For m > 1 this takes |x| >= 2^-110
+ * or 0: x passes as three bf16 parts, and what lies below 2^-133 is lost.
+ * Weights beyond the fp32 range (scale bytes 253 and 254, which
+ * rz_mxfp4_quant never writes) count as infinite here.  m == 0 or n == 0 is
+ * a no-op.
  */
 int rz_mxfp4_gemv(const uint8_t* w_codes, const uint8_t* w_scales, uint32_t n, uint32_t k, const float* x, uint32_t m,
                   float* y, void* stream);

@@ -85,10 +85,15 @@ def gemm(a: np.ndarray, w: np.ndarray):
 
 
 def gemv(x: np.ndarray, w: np.ndarray):
-    """(x w^T, bound) for fp32 x: fp32 multiply-adds in any order, one
-    rounding each, at most k + k/32 on the way of a term."""
+    """(x w^T, bound) for fp32 x.
+
+    One token: fp32 multiply-adds, one rounding (u) each, at most k + k/32 on
+    the way of a term.  More: x is the exact sum of three parts of its sign,
+    the products of the parts are exact, and a product passes fewer than k
+    additions in the matrix core (2u each, truncation) and k/256 + 2 outside
+    it.  Both are within gamma_{2 (k + k/32)} sum |x w|."""
     k = x.shape[1]
-    t = (k + k // 32) * U
+    t = 2 * (k + k // 32) * U
     g = t / (1 - t) + k * 2.0 ** -53
     x = x.astype(np.float64)
     return x @ w.T, g * (np.abs(x) @ np.abs(w).T)

@@ -271,6 +271,42 @@ def test_gemv_nan_and_zero(rz):
     assert np.isnan(y[:, 6]).all() and np.isfinite(np.delete(y, 6, 1)).all() and (np.delete(y, 6, 1)[1] == 0).all()
 
 
+@pytest.mark.parametrize("m", [1, 2, 5, 8])
+def test_gemv_ranges(rz, m):
+    """Every scale a finite fp32 weight has (each row of w one) with inputs from 2^-95 to 2^24, values
+    next to the largest float, and an infinity and a NaN in single tokens."""
+    n, k = 40, 512
+    g = W.rng(55)
+    w = random_tensor(56, n, k)
+    w[1][:] = np.linspace(0, 252, n).astype(np.uint8)[:, None]
+    w[0][w[0] == 8] = 0
+    wv = mxfp4.dequant(*w)
+    x = W.act_normal(57, m, k)
+    x = np.where(np.abs(x) < 2.0 ** -7, np.float32(1), x)
+    for e in (-95, -40, 0, 24):
+        xe = np.ldexp(x, e).astype(np.float32)
+        ref, bound = mxfp4.gemv(xe, wv)
+        y = host(rz.rz_mxfp4_gemv(*tiled(w), n, dev(xe))).astype(np.float64)
+        # no partial sum can overflow (each is at most sum |x w|), and no result is next to the subnormals
+        fine = (np.abs(xe.astype(np.float64)) @ np.abs(wv).T < 2.0 ** 127) & (np.abs(ref) > 1e-30)
+        assert fine.any() and (np.abs(y - ref)[fine] <= bound[fine]).all(), e
+    w[1][:] = 120
+    wv = mxfp4.dequant(*w)
+    x[0, 7] = np.finfo(np.float32).max
+    within(rz.rz_mxfp4_gemv(*tiled(w), n, dev(x)), *mxfp4.gemv(x, wv))
+    x[0, 7] = -np.inf
+    x[m - 1, 9] = np.nan if m > 1 else x[0, 9]
+    y = host(rz.rz_mxfp4_gemv(*tiled(w), n, dev(x)))
+    with np.errstate(invalid="ignore"):
+        lead = x[0, 7] * wv[:, 7].astype(np.float32)  # -inf, inf, or NaN where the weight is 0
+    assert np.array_equal(y[0], lead, equal_nan=True)
+    if m > 1:
+        assert np.isnan(y[m - 1]).all()
+    if m > 2:
+        r, b = mxfp4.gemv(x[1:m - 1], wv)
+        assert (np.abs(y[1:m - 1] - r) <= b).all()
+
+
 # ---------------------------------------------------------------- used together
 
 def test_feed_forward(rz):
