@@ -10,6 +10,11 @@
 // block shared by its quad (two DPP maxima finish the block's absmax), reads
 // are 256-byte runs of eight rows, each wave writes 128-byte runs of codes,
 // and the four 64-column slabs of a lane are in flight together.
+//
+// Measured: quantising 2048 x 18944 31.4 us (5.6 TB/s), reading it back in
+// bf16 16.0 us (6.1 TB/s), packing 18944 x 3584 from Q4_K 22.0 us in a trace,
+// 18.5 back to back (4.0 TB/s; 19.9 with neighbouring tiles on different
+// XCDs, whose caches then fetch the 144-byte blocks' shared lines twice).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
