@@ -47,6 +47,7 @@ struct Args {
     uint8_t* h_scales;
     uint32_t m, n, k;
     uint32_t tiles_m, tiles_n, group_m;
+    bool nt;  // every row of y starts on 64 bytes
 };
 
 enum Out { kOutF32 = 0, kOutMX = 1 };
@@ -94,8 +95,10 @@ __device__ __forceinline__ uint32_t load4(__amdgpu_buffer_rsrc_t rs, uint32_t vo
 
 // The 32 x 32 block v (v[e]: row 8 (e/4) + 4 (lane/32) + e%4, column lane%32)
 // of row group grp and columns col0 .. + 31 to y; rows and columns outside
-// [0, m) x [0, n) are dropped (rows by the buffer's range).
-__device__ __forceinline__ void store_f32(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane) {
+// [0, m) x [0, n) are dropped (rows by the buffer's range).  NT: non-temporal,
+// the output is not kept in the caches.
+template <bool NT>
+__device__ __forceinline__ void store_rows(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane) {
     const uint32_t row0 = grp * 32u;
     if (row0 >= P.m) return;
     const uint32_t rows = min_u32(32u, P.m - row0);
@@ -106,8 +109,19 @@ __device__ __forceinline__ void store_f32(const Args& P, const float (&v)[16], u
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         const uint32_t row = 8u * (e >> 2) + 4u * (lane >> 5) + (e & 3);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), rs, (row * P.n + col) * 4u, 0, kNonTemporal);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), rs, (row * P.n + col) * 4u, 0, NT ? kNonTemporal : 0);
     }
+}
+
+// Non-temporal where every row of y starts on 64 bytes (2048 x 18944 x 3584:
+// 77 us, 99 with ordinary stores); other widths leave parts of lines that the
+// L2 has to put together first (2048 x 9000 x 3584: 47 us, non-temporal 59;
+// 4096 x 9000 x 512: 46 and 81).
+__device__ __forceinline__ void store_f32(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane) {
+    if (P.nt)
+        store_rows<true>(P, v, grp, col0, lane);
+    else
+        store_rows<false>(P, v, grp, col0, lane);
 }
 
 // A 32 x 32 block in LDS (row-major) to row group grp, columns col0 .. + 31 of
@@ -469,6 +483,7 @@ hipError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint3
     P.m = m;
     P.n = n;
     P.k = k;
+    P.nt = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)n * 4u) & 63u) == 0;
     if (!gated)
         launch_as<false, kOutF32>(P, st);
     else if (h_codes)
