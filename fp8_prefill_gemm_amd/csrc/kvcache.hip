@@ -155,9 +155,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead A, uint32_t pe
                     v[4 * j + 3] = b.y * s;
                 }
             } else {
-                decode8(w[u].x, v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = times_scale(v[j], sc[u]);
+                decode8(w[u].x, v, cvt_scale(sc[u]));
             }
             const uint64_t i = i0 + u * (kThreads / L);  // (row - row0) * heads + head
             store8<DT>(A.out[c], ((uint64_t)row0 * A.heads + i) * A.dim + part * 8u, v);

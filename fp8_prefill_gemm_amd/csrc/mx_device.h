@@ -48,36 +48,29 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t key) {
     return e == 255u ? kNanByte : (e > 2u ? e - 2u : 0u);
 }
 
-// 1 / X as a float, exact and normal for every byte of a finite block (at
-// most 252); 0 for the NaN byte, which makes the codes of finite values zero.
-__device__ __forceinline__ float inv_scale(uint32_t byte) {
-    return byte == kNanByte ? 0.0f : __uint_as_float((254u - byte) << 23);
+// The scale operand of the v_cvt_scalef32 conversions, of which they read the
+// exponent field as an E8M0 byte: 2^(byte - 127), 255 NaN.
+__device__ __forceinline__ float cvt_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// E2M1 codes of eight values divided by `scale`, value i in nibble i:
+// nearest, ties to even, saturating.
+__device__ __forceinline__ uint32_t encode8(const float (&v)[8], float scale) {
+    uint32_t w = __builtin_nondeterministic_value(0u);  // every byte is written
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
 }
 
-// E2M1 codes of eight values already divided by X, value i in nibble i.
-// v_cvt_scalef32_pk_fp4_f32 (scale 1) rounds to nearest even and saturates.
-__device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
-    uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], 1.0f, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], 1.0f, 3);
-}
-
-// The eight E2M1 values of a word of codes, times `scale` (a power of two or
-// NaN; 1 gives the values not yet times X).
-__device__ __forceinline__ void decode8(uint32_t w, float (&v)[8], float scale = 1.0f) {
+// The eight E2M1 values of a word of codes, times `scale`: exact in fp32 (its
+// subnormals too), infinite past its range, NaN where scale is NaN.
+__device__ __forceinline__ void decode8(uint32_t w, float (&v)[8], float scale) {
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0);
     const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1);
     const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2);
     const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
     v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
-}
-
-// v * 2^(byte - 127), NaN for the NaN byte.  ldexp is exact but for results
-// below the smallest subnormal, which no E2M1 value times X reaches.
-__device__ __forceinline__ float times_scale(float v, uint32_t byte) {
-    return byte == kNanByte ? __uint_as_float(0x7FC00000u) : __builtin_amdgcn_ldexpf(v, (int)byte - 127);
 }
 
 // Maximum over the four lanes of a quad (lanes 4i .. 4i+3), every lane gets it.
@@ -98,12 +91,8 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& byt
         key = key > a ? key : a;
     }
     byte = scale_byte(quad_max(key));
-    const float inv = inv_scale(byte);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[i] * inv;
-    const uint32_t w = encode8(v);
-    return byte == kNanByte ? 0u : w;  // NaN and Inf products have codes of their own
+    const uint32_t w = encode8(x, cvt_scale(byte));
+    return byte == kNanByte ? 0u : w;
 }
 
 // Element types of the reading-back kernels' outputs (rz_dtype).

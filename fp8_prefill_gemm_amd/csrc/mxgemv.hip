@@ -23,9 +23,6 @@ namespace rz {
 namespace {
 using namespace mx;
 
-// 2^(byte - 127): exact for every byte (byte 0 is a subnormal, 255 NaN).
-__device__ __forceinline__ float scale_value(uint32_t byte) { return times_scale(1.0f, byte); }
-
 constexpr int kRun = 36;          // floats a 32-column run of x takes in LDS: the runs start in different banks
 constexpr int kSlabX = 8 * kRun;  // floats of a slab
 
@@ -69,7 +66,7 @@ __global__ __launch_bounds__(1024) void mx_gemv_token_kernel(MxWeights W, uint32
         for (int t = 0; t < 2; ++t) {
             float f[G];
 #pragma unroll
-            for (int g = 0; g < G; ++g) f[g] = scale_value((sc[g] >> (16 * t)) & 0xFFu);
+            for (int g = 0; g < G; ++g) f[g] = cvt_scale((sc[g] >> (16 * t)) & 0xFFu);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float* xp = xs + (2 * (q0 + 2 * t) + h) * kRun + 8 * c;
@@ -200,7 +197,7 @@ __global__ __launch_bounds__(1024) void mx_gemv_batch_kernel(MxWeights W, uint32
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) f[g][u] = scale_value((sc[g][u] >> (16 * t)) & 0xFFu);
+                for (int u = 0; u < 2; ++u) f[g][u] = cvt_scale((sc[g][u] >> (16 * t)) & 0xFFu);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 bf16x8 b[kTiles];

@@ -178,9 +178,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequant_kernel(const uint8_t* __r
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         float v[8];
-        decode8(w[q], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = times_scale(v[i], (sc >> (8 * q)) & 0xFFu);
+        decode8(w[q], v, cvt_scale((sc >> (8 * q)) & 0xFFu));
         store8<DT>(out, at + 64u * q, v);
     }
 }
