@@ -166,7 +166,7 @@ __device__ __forceinline__ void store_mx(const Args& P, const float (&v)[16], ui
 // The four waves read the same activation blocks, so those go through LDS
 // (two 16 KB stages of 256 columns, one barrier each); a weight block is
 // used by one wave only and goes from the L2 straight to registers, a step
-// ahead.  With 244 registers and 32 KB of LDS two workgroups share a CU:
+// ahead.  With 242 registers and 32 KB of LDS two workgroups share a CU:
 // while one stores its tile or waits, the other computes.
 //
 // Measured (random codes, M = 2048): gated N=18944 K=3584 133 us, 4.2
@@ -177,7 +177,9 @@ __device__ __forceinline__ void store_mx(const Args& P, const float (&v)[16], ui
 // 6.6 (9.4 on constant ones).  Left to the compiler's own order, which moves
 // the loads next to their use, 156 and 82 us.  A 256 x 256 tile of eight
 // waves reads a third less through the L2 but has one workgroup a CU: 138
-// and 85 us.
+// and 85 us; one of four waves of 128 x 128, with half the LDS reads, takes 91
+// us where this takes 73 (2048 x 18944 x 3584, not gated).  Three weight
+// buffers, one workgroup a CU: 68 us for the down product.
 // ---------------------------------------------------------------------------
 constexpr int kTM = 4, kWN = 2, kNW = 4;
 
