@@ -52,6 +52,11 @@ shapes at M=2048, with both paths' accuracy on the gate GEMM.
 weight on the int8 matrix cores) beside the FP8 path, with both paths'
 accuracy on the gate GEMM.
 
+--mxfp4 instead times the MXFP4 path (weights and activations in 4-bit
+microscaled blocks) on the FFN shapes at M=2048 beside the FP8 path: packing,
+quantisation, the gated product with fp32 and with MXFP4 output, the down
+product, with both paths' accuracy on the gate GEMM.
+
 --kquant-gemm instead times the FP8 GEMM that encodes the weight from its
 K-quant blocks inside the kernel (no FP8 weight cache) beside the cached
 path's GEMM, at the model's prefill shapes (warm).
@@ -833,6 +838,74 @@ def q8_gemm(args, dev) -> int:
     return 0
 
 
+def mxfp4(args, dev) -> int:
+    """The MXFP4 path on configuration 3's FFN (M=2048; gate and up 18944 x
+    3584, down 3584 x 18944) beside the FP8 path (one line): warm times, HIP
+    events around 50 launches after 10 warm-up launches, and the accuracy of
+    both paths' gate GEMM on 64 rows against a float64 product of the fp32
+    activation and the fp32 dequantised weight."""
+    import torch
+
+    import fp8_prefill_gemm_amd as rz
+    import workloads as W
+
+    stream = torch.cuda.current_stream(dev)
+
+    def timed(fn, reps=TIMED_LAUNCHES):
+        for _ in range(WARM_LAUNCHES):
+            fn()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for _ in range(reps):
+            fn()
+        e1.record(stream)
+        e1.synchronize()
+        return e0.elapsed_time(e1) * 1e3 / reps  # us
+
+    m, n, k = 2048, 18944, 3584
+    x = torch.from_numpy(W.act_normal(W.seed_for(3, 0, "x_ffn"), m, k)).to(dev)
+    blocks = {s: torch.from_numpy(W.weight_blocks(q, W.seed_for(3, 0, s), *d)).to(dev)
+              for s, q, d in (("gate", W.Q4_K, (n, k)), ("up", W.Q4_K, (n, k)), ("down", W.Q6_K, (k, n)))}
+    gate, up = (rz.rz_mxfp4_pack_weight(W.Q4_K, blocks[s], n, k) for s in ("gate", "up"))
+    down = rz.rz_mxfp4_pack_weight(W.Q6_K, blocks["down"], k, n)
+    a = rz.rz_mxfp4_quant(x)
+    h = torch.empty((m, n), dtype=torch.float32, device=dev)
+    hq = rz.rz_mxfp4_gated_quant(*a, m, gate, up, n)
+    y = torch.empty((m, k), dtype=torch.float32, device=dev)
+    us = {"pack_gate": timed(lambda: rz.rz_mxfp4_pack_weight(W.Q4_K, blocks["gate"], n, k, *gate)),
+          "pack_down": timed(lambda: rz.rz_mxfp4_pack_weight(W.Q6_K, blocks["down"], k, n, *down)),
+          "quant": timed(lambda: rz.rz_mxfp4_quant(x, *a)),
+          "gated": timed(lambda: rz.rz_mxfp4_gated(*a, m, gate, up, n, h)),
+          "gated_quant": timed(lambda: rz.rz_mxfp4_gated_quant(*a, m, gate, up, n, *hq)),
+          "down": timed(lambda: rz.rz_mxfp4_gemm(*hq, m, *down, k, y))}
+    us["ffn"] = timed(lambda: (rz.rz_mxfp4_quant(x, *a), rz.rz_mxfp4_gated_quant(*a, m, gate, up, n, *hq),
+                               rz.rz_mxfp4_gemm(*hq, m, *down, k, y)))
+    # the FP8 path's products of the same shapes (its FFN has the activation
+    # between them done by the caller)
+    a8, sc = rz.rz_fp8_quant_act(x)
+    packed = [rz.rz_fp8_pack_weight(W.Q4_K, blocks[s], n, k) for s in ("gate", "up")]
+    ys = [torch.empty((m, n), dtype=torch.float32, device=dev) for _ in range(2)]
+    us["fp8_gate_up"] = timed(lambda: rz.rz_fp8_gemm_group(a8, m, sc, [(w, s) for w, s, _ in packed], ys))
+    fl = 2.0 * m * n * k
+    rate = {"gated": 2 * fl / us["gated"] / 1e6, "gated_quant": 2 * fl / us["gated_quant"] / 1e6, "down": fl / us["down"] / 1e6,
+            "fp8_gate_up": 2 * fl / us["fp8_gate_up"] / 1e6}
+    wf = rz.rz_dequant_f32(W.Q4_K, blocks["gate"], n, k)
+    sel = torch.linspace(0, m - 1, 64, device=dev).long()
+    ref = x[sel].double() @ wf.double().t()
+    den = ref.abs().mean().item()
+    yg = rz.rz_mxfp4_gemm(*a, m, *gate, n)
+    acc = {nm: {"mean_abs_err_rel": round((v[sel].double() - ref).abs().mean().item() / den, 6),
+                "max_abs_err_rel": round((v[sel].double() - ref).abs().max().item() / den, 6)}
+           for nm, v in (("mxfp4", yg), ("fp8", ys[0]))}
+    out = {"metric": "MXFP4 FFN vs FP8 (M=2048, warm)", "unit": "us", "higher_is_better": False,
+           "rows_us": {s: round(v, 1) for s, v in us.items()}, "tflops": {s: round(v, 1) for s, v in rate.items()},
+           "accuracy_vs_fp64_of_fp32_inputs": acc, "dtype": "mxfp4 (fp32 accumulate)", "data": "synthetic",
+           "config": {"workload": "FFN prefill, M=2048: gate+up K=3584 N=18944 Q4_K, down K=18944 N=3584 Q6_K, packed to MXFP4"}}
+    log(out)
+    print(json.dumps(out), flush=True)
+    return 0
+
+
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
@@ -856,6 +929,8 @@ def main() -> int:
                     help="instead time the FP16 cached-weight comparator beside the FP8 path (warm, M=2048 FFN)")
     ap.add_argument("--q8-gemm", action="store_true",
                     help="instead time the integer path (Q8_1 activation x Q4_K weight) beside the FP8 path (warm)")
+    ap.add_argument("--mxfp4", action="store_true",
+                    help="instead time the MXFP4 path's FFN beside the FP8 path (warm, M=2048)")
     ap.add_argument("--gemm-clock", action="store_true",
                     help="instead run the gate+up GEMM back to back with random and constant codes, sampling the "
                          "GFX clock and board power")
@@ -900,7 +975,7 @@ def main() -> int:
         return hbm_rates(args, dev)
     # board clock and power readings (refreshed once a second): the default
     # step's clock pass and --gemm-clock
-    sampled = not any((args.pack_model, args.gemm_shapes, args.kquant_gemm, args.fp16_gemm, args.q8_gemm,
+    sampled = not any((args.pack_model, args.gemm_shapes, args.kquant_gemm, args.fp16_gemm, args.q8_gemm, args.mxfp4,
                        args.small_m is not None)) and not args.no_clock
     metrics = GpuMetrics() if sampled else None
     try:
@@ -929,6 +1004,8 @@ def measure(args, dev, metrics) -> int:
         return fp16_gemm(args, dev)
     if args.q8_gemm:
         return q8_gemm(args, dev)
+    if args.mxfp4:
+        return mxfp4(args, dev)
     if args.small_m is not None:
         if not args.small_m:
             args.small_m = [1, 2, 3, 4, 8, 37]
