@@ -29,7 +29,7 @@ using gemm::v4i;
 using gemm::v8i;
 
 // acc += a w for one 32 x 32 block and 64 columns; Q: the byte of the scale
-// dwords.
+// dwords.  The rows of the result (registers) are the first operand's.
 template <int Q>
 __device__ __forceinline__ v16f mma(u32x4 a, u32x4 w, v16f acc, uint32_t sa, uint32_t sw) {
     const v4i a4 = __builtin_bit_cast(v4i, a), w4 = __builtin_bit_cast(v4i, w);
@@ -124,14 +124,24 @@ __device__ __forceinline__ void store_f32(const Args& P, const float (&v)[16], u
         store_rows<false>(P, v, grp, col0, lane);
 }
 
-// A 32 x 32 block in LDS (row-major) to row group grp, columns col0 .. + 31 of
-// the tiled MXFP4 output, by one wave: a quad of lanes holds a row's block.
-// Pad rows are products of zero rows and quantise to zero.
+// Where the 16 bytes of codes and the scale byte of token row 0 of group grp,
+// columns col0 .. + 31 of the MXFP4 output lie; row r's are 16 r and 4 r on.
+struct MxBlock {
+    uint8_t *codes, *scales;
+    __device__ __forceinline__ MxBlock(const Args& P, uint32_t grp, uint32_t col0) {
+        const uint32_t blk = col0 / 32u;
+        codes = P.h_codes + ((uint64_t)grp * (P.n / 64u) + blk / 2u) * 1024u + (blk & 1u) * 512u;
+        scales = P.h_scales + ((uint64_t)grp * (P.n / 256u) + blk / 8u) * 256u + (blk & 1u) * 128u + (blk / 2u) % 4u;
+    }
+};
+
+// A 32 x 32 block in LDS (tokens x columns) quantised by one wave: a quad of
+// lanes holds a row's block.  Pad rows are products of zero rows and quantise
+// to zero.
 __device__ __forceinline__ void quantise_block(const Args& P, uint32_t grp, uint32_t col0, uint32_t lane, const float* lds) {
     if (grp * 32u >= P.m) return;
-    const uint32_t blk = col0 / 32u, part = lane & 3u;
-    uint8_t* codes = P.h_codes + ((uint64_t)grp * (P.n / 64u) + blk / 2u) * 1024u + (blk & 1u) * 512u;
-    uint8_t* scales = P.h_scales + ((uint64_t)grp * (P.n / 256u) + blk / 8u) * 256u + (blk & 1u) * 128u + (blk / 2u) % 4u;
+    const uint32_t part = lane & 3u;
+    const MxBlock o(P, grp, col0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t row = 16u * i + (lane >> 2);
@@ -140,22 +150,41 @@ __device__ __forceinline__ void quantise_block(const Args& P, uint32_t grp, uint
         *reinterpret_cast<f32x4*>(x + 4) = *reinterpret_cast<const f32x4*>(lds + row * 32 + part * 8 + 4);
         uint32_t byte;
         const uint32_t c = quantise8(x, byte);
-        *reinterpret_cast<uint32_t*>(codes + row * 16u + part * 4u) = c;
-        if (part == 0) scales[row * 4u] = (uint8_t)byte;
+        *reinterpret_cast<uint32_t*>(o.codes + row * 16u + part * 4u) = c;
+        if (part == 0) o.scales[row * 4u] = (uint8_t)byte;
     }
 }
 
-// The block v (as store_f32 takes it) quantised by its wave, through 4 KB of
-// LDS that no other wave uses.
-__device__ __forceinline__ void store_mx(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane,
-                                         float* lds) {
+// A block with the tokens along the lanes quantised in registers: v[e] is
+// token lane%32, column 8 (e/4) + 4 (lane/32) + e%4, so a lane and its
+// partner 32 on hold a token's block.  They share its largest value, and each
+// gets the other's codes of the eight bytes it stores.
+__device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane) {
+    if (grp * 32u >= P.m) return;
+    uint32_t key = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) lds[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * 32 + (lane & 31)] = v[e];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    quantise_block(P, grp, col0, lane, lds);
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    for (int e = 0; e < 16; ++e) {
+        const uint32_t a = mag_key(v[e]);
+        key = key > a ? key : a;
+    }
+    const uint32_t other = (uint32_t)__shfl_xor((int)key, 32, 64);
+    const uint32_t byte = scale_byte(key > other ? key : other);
+    float lo[8], hi[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lo[e] = v[e];
+        hi[e] = v[8 + e];
+    }
+    // 16 bits of codes for each e/4: columns 0-3 of eight (lane < 32) or 4-7
+    const uint32_t w0 = encode8(lo, cvt_scale(byte)), w1 = encode8(hi, cvt_scale(byte));
+    const bool upper = lane >= 32u;  // stores bytes 8..15
+    const uint32_t got = (uint32_t)__shfl_xor((int)(upper ? w0 : w1), 32, 64);
+    const uint32_t a = upper ? got : w0, b = upper ? w1 : got;  // the lower and the upper lane's codes
+    u32x2 c = {(a & 0xFFFFu) | (b << 16), (a >> 16) | (b & 0xFFFF0000u)};
+    if (byte == kNanByte) c = (u32x2){0u, 0u};
+    const MxBlock o(P, grp, col0);
+    *reinterpret_cast<u32x2*>(o.codes + (lane & 31u) * 16u + (lane >> 5) * 8u) = c;
+    if (!upper) o.scales[lane * 4u] = (uint8_t)byte;
 }
 
 // ---------------------------------------------------------------------------
@@ -261,7 +290,12 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
                 load_a(p - 8, s2);
             }
 #pragma unroll
-            for (int i = 0; i < kWN; ++i) acc[i][j] = mma<q>(a[p % 3], w[b][i][q], acc[i][j], sa[b][j], sw[b][i]);
+            for (int i = 0; i < kWN; ++i) {
+                if constexpr (OUT == kOutMX)  // tokens along the lanes
+                    acc[i][j] = mma<q>(w[b][i][q], a[p % 3], acc[i][j], sw[b][i], sa[b][j]);
+                else
+                    acc[i][j] = mma<q>(a[p % 3], w[b][i][q], acc[i][j], sa[b][j], sw[b][i]);
+            }
             __builtin_amdgcn_sched_barrier(0);
         });
     };
@@ -285,7 +319,6 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
         if (s + 1 < slabs) step(std::integral_constant<int, 1>{}, s + 1);
     }
 
-    if constexpr (OUT == kOutMX) __syncthreads();  // the stages become the waves' exchange space
 #pragma unroll
     for (int j = 0; j < kTM; ++j)
 #pragma unroll
@@ -295,7 +328,7 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = GATED ? silu(acc[i][j][e]) * acc[kWN - kCols + i][j][e] : acc[i][j][e];
             if constexpr (OUT == kOutMX) {
-                if (col < P.n) store_mx(P, v, g0 + j, col, lane, reinterpret_cast<float*>(smem) + wave * 1024);
+                if (col < P.n) quantise_lanes(P, v, g0 + j, col, lane);
             } else {
                 store_f32(P, v, g0 + j, col, lane);
             }
@@ -411,7 +444,7 @@ __global__ __launch_bounds__(64 * KS, 2) void mx_gemm_split_kernel(Args P) {
             }
         } else {
             __syncthreads();
-            float* blk = &sums[0][0][0][0];  // the output blocks as 32 x 32 rows, for store_mx
+            float* blk = &sums[0][0][0][0];  // the output blocks as 32 x 32 rows
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
                 const uint32_t e = wave * kPer + u;
