@@ -136,8 +136,8 @@ struct MxBlock {
 };
 
 // A 32 x 32 block in LDS (tokens x columns) quantised by one wave: a quad of
-// lanes holds a row's block.  Pad rows are products of zero rows and quantise
-// to zero.
+// lanes holds a row's block.  Pad rows become zeros whatever they hold (their
+// products are zeros but for a NaN weight's).
 __device__ __forceinline__ void quantise_block(const Args& P, uint32_t grp, uint32_t col0, uint32_t lane, const float* lds) {
     if (grp * 32u >= P.m) return;
     const uint32_t part = lane & 3u;
@@ -149,7 +149,8 @@ __device__ __forceinline__ void quantise_block(const Args& P, uint32_t grp, uint
         *reinterpret_cast<f32x4*>(x) = *reinterpret_cast<const f32x4*>(lds + row * 32 + part * 8);
         *reinterpret_cast<f32x4*>(x + 4) = *reinterpret_cast<const f32x4*>(lds + row * 32 + part * 8 + 4);
         uint32_t byte;
-        const uint32_t c = quantise8(x, byte);
+        uint32_t c = quantise8(x, byte);
+        if (grp * 32u + row >= P.m) c = byte = 0u;
         *reinterpret_cast<uint32_t*>(o.codes + row * 16u + part * 4u) = c;
         if (part == 0) o.scales[row * 4u] = (uint8_t)byte;
     }
@@ -158,7 +159,7 @@ __device__ __forceinline__ void quantise_block(const Args& P, uint32_t grp, uint
 // A block with the tokens along the lanes quantised in registers: v[e] is
 // token lane%32, column 8 (e/4) + 4 (lane/32) + e%4, so a lane and its
 // partner 32 on hold a token's block.  They share its largest value, and each
-// gets the other's codes of the eight bytes it stores.
+// gets the other's codes of the eight bytes it stores.  Pad rows as above.
 __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane) {
     if (grp * 32u >= P.m) return;
     uint32_t key = 0;
@@ -168,7 +169,7 @@ __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[1
         key = key > a ? key : a;
     }
     const uint32_t other = (uint32_t)__shfl_xor((int)key, 32, 64);
-    const uint32_t byte = scale_byte(key > other ? key : other);
+    uint32_t byte = scale_byte(key > other ? key : other);
     float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -182,6 +183,10 @@ __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[1
     const uint32_t a = upper ? got : w0, b = upper ? w1 : got;  // the lower and the upper lane's codes
     u32x2 c = {(a & 0xFFFFu) | (b << 16), (a >> 16) | (b & 0xFFFF0000u)};
     if (byte == kNanByte) c = (u32x2){0u, 0u};
+    if (grp * 32u + (lane & 31u) >= P.m) {
+        c = (u32x2){0u, 0u};
+        byte = 0u;
+    }
     const MxBlock o(P, grp, col0);
     *reinterpret_cast<u32x2*>(o.codes + (lane & 31u) * 16u + (lane >> 5) * 8u) = c;
     if (!upper) o.scales[lane * 4u] = (uint8_t)byte;

@@ -155,6 +155,29 @@ def test_write_then_read_prompt_and_steps(rz, fmt):
         assert torch.equal(outs[i].cpu(), torch.from_numpy(want).to(torch.bfloat16))
 
 
+def test_on_a_stream_and_refusals(rz):
+    """A write and a read on a side stream, as on the current one; a refused call leaves the cache as it was."""
+    heads, dim, n = 2, 64, 9
+    x = dev(W.act_normal(70, n, heads * dim).reshape(n, heads, dim))
+    slots = dev(W.rng(71).permutation(12)[:n].astype(np.int64))
+    table, offsets = slots.to(torch.int32).view(1, n), dev(np.array([0, n], dtype=np.int32))
+    got = []
+    for stream in (None, torch.cuda.Stream()):
+        _, cache = caches(kv_cache.MXFP4, 12, heads, dim)
+        torch.cuda.synchronize()
+        rz.rz_kv_cache_write(kv_cache.MXFP4, x, x, slots, *cache, stream=stream)
+        got.append(rz.rz_kv_cache_read(kv_cache.MXFP4, *cache, 1, table, offsets, n, dtype=torch.float16, stream=stream))
+        torch.cuda.synchronize()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    _, cache = caches(kv_cache.E4M3, 4, 1, 48)
+    before = [host(c) for c in cache]
+    with pytest.raises(rz.RzError, match="multiple of 32") as e:
+        rz.rz_kv_cache_write(kv_cache.E4M3, torch.zeros((1, 1, 48), device="cuda"), torch.zeros((1, 1, 48), device="cuda"),
+                             torch.zeros(1, dtype=torch.int64, device="cuda"), *cache)
+    assert e.value.status == -3 and all(np.array_equal(host(c), b) for c, b in zip(cache, before))
+
+
 def test_projection_to_cache(rz):
     """One layer's step: activation -> MXFP4 product -> cache -> read back, captured and replayed."""
     m, d, heads, dim = 37, 512, 2, 64

@@ -246,6 +246,24 @@ def test_gated_quant_is_quant_of_gated(rz, m, n, k):
     same(hc, tc)
 
 
+@pytest.mark.parametrize("m,n", [(40, 256), (400, 1024), (1600, 2048)])
+def test_gated_quant_nan_rows(rz, m, n):
+    """NaN blocks in one token and in one gate row: exactly their blocks read as NaN, the rest as without them."""
+    k = 512
+    a, g, u = random_tensor(43, m, k, 2), small_scale(random_tensor(44, n, k, 2), 8), small_scale(random_tensor(45, n, k, 2), 8)
+    clean = host(rz.rz_mxfp4_dequant(*rz.rz_mxfp4_gated_quant(*tiled(a), m, tiled(g), tiled(u), n), m))
+    a[1][33, 5] = 255
+    g[1][70, 9] = 255
+    hc, hs = rz.rz_mxfp4_gated_quant(*tiled(a), m, tiled(g), tiled(u), n)
+    got = host(rz.rz_mxfp4_dequant(hc, hs, m))
+    nan = np.zeros((m, n), dtype=bool)
+    nan[33], nan[:, 64:96] = True, True
+    assert np.array_equal(np.isnan(got), nan) and np.array_equal(got[~nan], clean[~nan])
+    tc, ts = mxfp4.quant_tiled(host(rz.rz_mxfp4_gated(*tiled(a), m, tiled(g), tiled(u), n)))
+    same(hs, ts)
+    same(hc, tc)
+
+
 @pytest.mark.parametrize("n,k", [(1, 256), (37, 512), (100, 3584), (64, 18944), (48, 4096), (5000, 2304)])
 @pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 6, 7, 8])
 def test_gemv(rz, m, n, k):
@@ -341,6 +359,41 @@ def test_streams_and_repeats(rz):
     torch.cuda.synchronize()
     for i, y in enumerate(got):
         assert np.array_equal(host(y), alone[i % 2])
+
+
+def test_every_call_on_a_stream(rz):
+    """Each function on a side stream, its outputs made there: the same bits as on the current one."""
+    m, n, k = 70, 512, 768
+    x = dev(W.act_normal(85, m, k))
+    a, g, u = tiled(random_tensor(86, m, k, 2)), tiled(random_tensor(87, n, k, 2)), tiled(random_tensor(88, n, k, 2))
+    blocks = dev(W.weight_blocks(W.Q6_K, 89, n, k))
+    calls = [lambda **kw: rz.rz_mxfp4_quant(x, **kw), lambda **kw: rz.rz_mxfp4_pack_weight(W.Q6_K, blocks, n, k, **kw),
+             lambda **kw: rz.rz_mxfp4_dequant(*a, m, dtype=torch.bfloat16, **kw), lambda **kw: rz.rz_mxfp4_gemm(*a, m, *g, n, **kw),
+             lambda **kw: rz.rz_mxfp4_gated(*a, m, g, u, n, **kw), lambda **kw: rz.rz_mxfp4_gated_quant(*a, m, g, u, n, **kw),
+             lambda **kw: rz.rz_mxfp4_gemv(*g, n, x[:3], **kw), lambda **kw: rz.rz_mxfp4_gated_gemv(g, u, n, x[:1], **kw)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for i, f in enumerate(calls):
+        got, want = f(stream=side), f()
+        torch.cuda.synchronize()
+        for p, q in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+            assert torch.equal(p, q), i
+
+
+def test_refusals_of_the_library(rz):
+    """What the binding lets through and the library refuses: RzError with its status, outputs untouched."""
+    a, w = tiled(random_tensor(94, 3, 256)), tiled(random_tensor(95, 96, 256))
+    with pytest.raises(rz.RzError, match="n=96 must be a multiple of 256") as e:
+        rz.rz_mxfp4_gated_quant(*a, 3, w, w, 96)
+    assert e.value.status == -3
+    with pytest.raises(rz.RzError, match="m=9 exceeds 8"):
+        rz.rz_mxfp4_gemv(*w, 96, torch.zeros((9, 256), device="cuda"))
+    y = torch.full((3 * 96 + 1,), 7.0, device="cuda")
+    with pytest.raises(rz.RzError, match="16-byte aligned"):
+        rz.rz_mxfp4_gemm(*a, 3, *w, 96, y=y[1:].view(3, 96))
+    assert (host(y) == 7).all()
+    with pytest.raises(ValueError, match="one device expected"):
+        rz.rz_mxfp4_gemm(a[0], a[1].cpu(), 3, *w, 96)
 
 
 def test_graph_replays(rz):
