@@ -420,6 +420,7 @@ int rz_fp16_gemm(const uint16_t* a_f16, const uint16_t* w_f16, uint32_t m, uint3
  *          is (((r/32)*(k/256) + c/256)*2 + c/32%2)*128 + r%32*4 + c/64%4
  * k, n <= RZ_MAX_GEMM_K.  No entry point here uses a workspace or waits on
  * the host, and every sum has a fixed order.  Outputs must not overlap inputs.
+ * Products ignore what the pad rows of their operands hold.
  * --------------------------------------------------------------------- */
 
 /* Element types of the outputs that are read back. */

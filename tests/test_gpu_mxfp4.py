@@ -175,6 +175,31 @@ def test_gemm(rz, m, n, k):
     assert (host(y[m:]) == 7).all()
 
 
+@pytest.mark.parametrize("m,n", [(5, 40), (100, 2500), (290, 3001), (1541, 4001)])
+def test_pad_rows_do_not_matter(rz, m, n):
+    """NaN scales and random codes in the operands' pad rows: the same bits as with zeros, gated (and its MXFP4 output) too."""
+    k = 512
+    g = W.rng(15)
+
+    def spoilt(t):
+        rows = t[0].shape[0]
+        pad = mxfp4.pad_rows(rows) - rows
+        more = g.integers(0, 16, (pad, k)).astype(np.uint8), np.full((pad, k // 32), 255, dtype=np.uint8)
+        return tiled((np.concatenate([t[0], more[0]]), np.concatenate([t[1], more[1]])))
+
+    n2 = -(-n // 256) * 256
+    a, w = random_tensor(16, m, k, 2), random_tensor(17, n, k, 2)
+    wide = small_scale(random_tensor(18, n2, k, 2), 8)
+    small = small_scale(w, 8)
+    assert torch.equal(rz.rz_mxfp4_gemm(*spoilt(a), m, *spoilt(w), n), rz.rz_mxfp4_gemm(*tiled(a), m, *tiled(w), n))
+    assert torch.equal(rz.rz_mxfp4_gated(*spoilt(a), m, spoilt(small), spoilt(small), n), rz.rz_mxfp4_gated(*tiled(a), m, tiled(small), tiled(small), n))
+    for p, q in zip(rz.rz_mxfp4_gated_quant(*spoilt(a), m, tiled(wide), tiled(wide), n2), rz.rz_mxfp4_gated_quant(*tiled(a), m, tiled(wide), tiled(wide), n2)):
+        assert torch.equal(p, q)
+    x = dev(W.act_normal(19, 3, k))
+    assert torch.equal(rz.rz_mxfp4_gemv(*spoilt(w), n, x), rz.rz_mxfp4_gemv(*tiled(w), n, x))
+    assert torch.equal(rz.rz_mxfp4_gated_gemv(spoilt(small), spoilt(small), n, x[:1]), rz.rz_mxfp4_gated_gemv(tiled(small), tiled(small), n, x[:1]))
+
+
 @pytest.mark.parametrize("m,n,k", [(40, 96, 18944), (2048, 3500, 512)])
 def test_gemm_exact_sums(rz, m, n, k):
     """With one scale every sum is a multiple of 2^-2 below 2^22: exact in fp32, so equal."""
