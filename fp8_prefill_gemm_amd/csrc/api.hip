@@ -754,7 +754,7 @@ int rz_kv_cache_write(int format, const float* k, const float* v, uint32_t token
     const uint64_t row = (uint64_t)heads * dim;
     if (tokens > 1 && (k_stride < row || v_stride < row || k_stride % 4u != 0 || v_stride % 4u != 0))
         return fail(RZ_ERR_SHAPE, "%s: token strides must be multiples of 4, at least heads*dim", fn);
-    if ((uint64_t)tokens * row > RZ_MAX_ELEMS || k_stride > RZ_MAX_ELEMS || v_stride > RZ_MAX_ELEMS)
+    if ((uint64_t)tokens * row > RZ_KV_MAX_CALL || k_stride > RZ_MAX_ELEMS || v_stride > RZ_MAX_ELEMS)
         return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) ||
         !aligned16(v_scales) || ((uintptr_t)slots & 7u))
@@ -777,7 +777,7 @@ int rz_kv_cache_read(int format, const uint8_t* k_codes, const void* k_scales, c
     if (rows == 0 || seqs == 0) return RZ_OK;  // nothing to read or write
     if (!k_codes || !k_scales || !v_codes || !v_scales || (max_pages != 0 && !page_table) || !offsets || !k_out || !v_out)
         return fail(RZ_ERR_NULL, "%s: null pointer", fn);
-    if ((uint64_t)rows * heads * dim > RZ_MAX_ELEMS || rows > 0x7FFFFFFFu)
+    if ((uint64_t)rows * heads * dim > RZ_KV_MAX_CALL || rows > 0x7FFFFFFFu || seqs > 0x7FFFFFFEu)
         return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
     if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) || !aligned16(v_scales) || !aligned16(k_out) ||
         !aligned16(v_out) || (((uintptr_t)page_table | (uintptr_t)offsets) & 3u))

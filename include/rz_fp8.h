@@ -473,7 +473,8 @@ int rz_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, c
  *   h[i][j] = g / (1 + e^-g) * u,  g = a gate^T, u = a up^T   for i < m, j < n
  *   gate_*, up_*   MXFP4 [n][k] each
  *   h              device out, fp32 [m][n] row-major
- * m == 0 or n == 0 is a no-op.  (Forward only: weights here are frozen codes.)
+ * m == 0 or n == 0 is a no-op.  A factor g / (1 + e^-g) under 2^-112 in size
+ * may count as 0.  (Forward only: weights here are frozen codes.)
  */
 int rz_mxfp4_gated(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* gate_codes,
                    const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales, uint32_t n,
@@ -526,8 +527,10 @@ int rz_mxfp4_gated_gemv(const uint8_t* gate_codes, const uint8_t* gate_scales, c
  */
 typedef enum { RZ_KV_E4M3 = 0, RZ_KV_MXFP4 = 1 } rz_kv_format;
 
-/* Largest dim (a multiple of 32); heads*dim is at most 2^26. */
+/* Largest dim (a multiple of 32); heads*dim is at most 2^26, and one call
+ * writes or reads at most RZ_KV_MAX_CALL values each of keys and values. */
 #define RZ_KV_MAX_DIM 512u
+#define RZ_KV_MAX_CALL ((uint64_t)1 << 33)
 
 /*
  * Quantise tokens' keys and values into slots of the cache.

@@ -111,6 +111,14 @@ def test_kv_write(L):
     assert L.rz_kv_cache_write(1, None, None, 0, 2, 64, 0, 0, None, 10, None, None, None, None, None) == OK
 
 
+def test_kv_call_too_large(L):
+    """Grids count lanes in 32 bits: more than 2^33 values in one call are refused, as are 2^31 sequences."""
+    for tokens, heads, dim, status in (((1 << 28) + 1, 1, 32, SHAPE), ((1 << 20) + 1, 64, 128, SHAPE), (1 << 31, 1, 32, SHAPE)):
+        assert L.rz_kv_cache_write(0, P, P, tokens, heads, dim, heads * dim, heads * dim, P, 10, P, P, P, P, None) == status
+        assert L.rz_kv_cache_read(1, P, P, P, P, 64, heads, dim, 16, P, 3, 4, P, tokens, 2, P, P, None) == status
+    assert L.rz_kv_cache_read(1, P, P, P, P, 64, 1, 32, 16, P, 0xFFFFFFFF, 4, P, 1, 2, P, P, None) == SHAPE
+
+
 def test_kv_read(L):
     good = [1, P, P, P, P, 64, 2, 64, 16, P, 3, 4, P, 20, 2, P, P, None]
     refuses_each(L.rz_kv_cache_read, good, (1, 2, 3, 4, 9, 12, 15, 16))
