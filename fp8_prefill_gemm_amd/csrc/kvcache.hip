@@ -11,8 +11,8 @@
 // lane holds eight values, 8..64 lanes a row; keys and values share a launch
 // (grid y).  Measured, 4 heads of 128: writing 131072 tokens 145 us (E4M3, 4.7
 // TB/s), 64 tokens 3.1 us; reading 131072 tokens back in bf16 81 us (E4M3, 5.0
-// TB/s) and 78 us (MXFP4, 4.4 TB/s; 88 and 83 us with one row a lane in
-// flight), 4096 tokens 4.9 us.
+// TB/s) and 72 us (MXFP4, 4.7 TB/s), 4096 tokens 4.9 us.  With one row a lane
+// in flight E4M3 took 88 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

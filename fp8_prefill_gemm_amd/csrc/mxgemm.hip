@@ -116,7 +116,9 @@ __device__ __forceinline__ void store_rows(const Args& P, const float (&v)[16], 
 // Non-temporal where every row of y starts on 64 bytes (2048 x 18944 x 3584:
 // 77 us, 99 with ordinary stores); other widths leave parts of lines that the
 // L2 has to put together first (2048 x 9000 x 3584: 47 us, non-temporal 59;
-// 4096 x 9000 x 512: 46 and 81).
+// 4096 x 9000 x 512: 46 and 81).  Wider runs store no faster: with a quad's values
+// transposed for 16 bytes a lane, 128 of eight rows a store, the first shape
+// takes 86 us, with the wave's halves swapped for 256 bytes of one row 81.
 __device__ __forceinline__ void store_f32(const Args& P, const float (&v)[16], uint32_t grp, uint32_t col0, uint32_t lane) {
     if (P.nt)
         store_rows<true>(P, v, grp, col0, lane);
