@@ -195,9 +195,9 @@ __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[1
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel: 128 tokens x 256 weight rows a workgroup (gated: 128 gate and
-// 128 up rows of the same columns), four waves along the weight rows, each
-// 128 x 64: kTM activation blocks x kWN weight blocks.
+// Tile kernel: 32 TM tokens (128, or 64) x 256 weight rows a workgroup (gated:
+// 128 gate and 128 up rows of the same columns), four waves along the weight
+// rows, each 32 TM x 64: TM activation blocks x kWN weight blocks.
 //
 // The four waves read the same activation blocks, so those go through LDS
 // (two 16 KB stages of 256 columns, one barrier each); a weight block is
@@ -217,14 +217,14 @@ __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[1
 // us where this takes 73 (2048 x 18944 x 3584, not gated).  Three weight
 // buffers, one workgroup a CU: 68 us for the down product.
 // ---------------------------------------------------------------------------
-constexpr int kTM = 4, kWN = 2, kNW = 4;
+constexpr int kWN = 2, kNW = 4;
 
-template <bool GATED, int OUT>
+template <int TM, bool GATED, int OUT>
 __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
     constexpr int kCols = GATED ? kWN / 2 : kWN;  // output blocks of a wave
     constexpr int kSides = GATED ? 2 : 1;
     static_assert(64 * kNW == 256, "a thread stages 16 of a row group's 4096 bytes");
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2][kTM * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2][TM * 4096];
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t slabs = P.k / 256u;
@@ -235,26 +235,26 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
     // one, all uniform.  A group past the tensor's last is replaced by the
     // last: what it gives is not stored.
     const uint32_t a_groups = pad32(P.m) / 32u, w_groups = pad32(P.n) / 32u;
-    const uint32_t g0 = tm * kTM, w0 = (tn * kNW + wave) * kCols, wb = min_u32(w0, w_groups - 1u);
-    const __amdgpu_buffer_rsrc_t arc = group_rsrc(P.a_codes, g0, slabs, 4096u, kTM);
-    const __amdgpu_buffer_rsrc_t ars = group_rsrc(P.a_scales, g0, slabs, 256u, kTM);
+    const uint32_t g0 = tm * TM, w0 = (tn * kNW + wave) * kCols, wb = min_u32(w0, w_groups - 1u);
+    const __amdgpu_buffer_rsrc_t arc = group_rsrc(P.a_codes, g0, slabs, 4096u, TM);
+    const __amdgpu_buffer_rsrc_t ars = group_rsrc(P.a_scales, g0, slabs, 256u, TM);
     __amdgpu_buffer_rsrc_t wrc[kSides], wrs[kSides];
 #pragma unroll
     for (int g = 0; g < kSides; ++g) {
         wrc[g] = group_rsrc(P.w.codes[g], wb, slabs, 4096u, kCols);
         wrs[g] = group_rsrc(P.w.scales[g], wb, slabs, 256u, kCols);
     }
-    uint32_t ag[kTM], wg[kCols];
+    uint32_t ag[TM], wg[kCols];
 #pragma unroll
-    for (int j = 0; j < kTM; ++j) ag[j] = (min_u32(g0 + j, a_groups - 1u) - g0) * slabs;
+    for (int j = 0; j < TM; ++j) ag[j] = (min_u32(g0 + j, a_groups - 1u) - g0) * slabs;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) wg[i] = (min_u32(wb + i, w_groups - 1u) - wb) * slabs;
     const uint32_t avo = tid * 16u, wvo = lane * 16u, svo = lane * 4u;
 
-    v16f acc[kWN][kTM] = {};
-    u32x4 st[kTM];       // activation rows on their way to LDS
+    v16f acc[kWN][TM] = {};
+    u32x4 st[TM];       // activation rows on their way to LDS
     u32x4 w[2][kWN][4];  // weight blocks of this step and the next
-    uint32_t sa[2][kTM], sw[2][kWN];
+    uint32_t sa[2][TM], sw[2][kWN];
 
     auto load_a = [&](int j, uint32_t s) { st[j] = load16(arc, avo, (ag[j] + s) * 4096u); };
     auto put_a = [&](uint8_t* dst, int j) { *reinterpret_cast<u32x4*>(dst + j * 4096 + avo) = st[j]; };
@@ -264,17 +264,17 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
     auto load_sw = [&](int b, int i, uint32_t s) { sw[b][i] = load4(wrs[i / kCols], svo, (wg[i % kCols] + s) * 256u); };
     auto load_sa = [&](int b, int j, uint32_t s) { sa[b][j] = load4(ars, svo, (ag[j] + s) * 256u); };
 
-    // One 256-column step: 16 pieces (64-column slab q, activation block j) of
-    // two MFMAs each, their order kept by the barriers to the scheduler.  In
+    // One 256-column step: 4 TM pieces (64-column slab q, activation block j)
+    // of two MFMAs each, their order kept by the barriers to the scheduler.  In
     // the shadow of a piece's MFMAs: the read of the activation block two
     // pieces on; in the first eight the loads of the next step's weights and
-    // scales; in the next four the write of an activation block to the other
-    // stage and the load of the one two steps on.  So every load has a whole
-    // step to land.
+    // scales; in TM of them from kPut on the write of an activation block to
+    // the other stage and the load of the one two steps on.  So every load has
+    // a whole step to land.
     auto step = [&](auto bc, uint32_t s) {
         constexpr int b = decltype(bc)::value;
-        constexpr int kPieces = 4 * kTM;
-        static_assert(kPieces == 16 && 4 * kWN == 8 && kTM == 4, "the loads' places below");
+        constexpr int kPieces = 4 * TM, kPut = 4 + TM;
+        static_assert(4 * kWN == 8 && kPieces >= 8 && kPut + TM <= kPieces, "the loads' places below");
         const uint8_t* cur = smem[b] + wvo;
         uint8_t* nxt = smem[b ^ 1];
         const uint32_t s1 = min_u32(s + 1u, slabs - 1u), s2 = min_u32(s + 2u, slabs - 1u);
@@ -284,17 +284,17 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
         a[1] = *reinterpret_cast<const u32x4*>(cur + 4096);
         __builtin_amdgcn_sched_barrier(0);
         for_each_index<kPieces>([&](auto pc) {
-            constexpr int p = decltype(pc)::value, q = p / kTM, j = p % kTM;
+            constexpr int p = decltype(pc)::value, q = p / TM, j = p % TM;
             if constexpr (p < kPieces - 2) {
                 constexpr int pn = p + 2;
-                a[pn % 3] = *reinterpret_cast<const u32x4*>(cur + (pn % kTM) * 4096 + (pn / kTM) * 1024);
+                a[pn % 3] = *reinterpret_cast<const u32x4*>(cur + (pn % TM) * 4096 + (pn / TM) * 1024);
             }
             if constexpr (p < 8) load_w(b ^ 1, p % kWN, p / kWN, s1);
             if constexpr (p >= 2 && p < 4) load_sw(b ^ 1, p - 2, s1);
-            if constexpr (p >= 4 && p < 8) load_sa(b ^ 1, p - 4, s1);
-            if constexpr (p >= 8 && p < 12) {
-                put_a(nxt, p - 8);
-                load_a(p - 8, s2);
+            if constexpr (p >= 4 && p < kPut) load_sa(b ^ 1, p - 4, s1);
+            if constexpr (p >= kPut && p < kPut + TM) {
+                put_a(nxt, p - kPut);
+                load_a(p - kPut, s2);
             }
 #pragma unroll
             for (int i = 0; i < kWN; ++i) {
@@ -307,9 +307,9 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
         });
     };
 #pragma unroll
-    for (int j = 0; j < kTM; ++j) load_a(j, 0);
+    for (int j = 0; j < TM; ++j) load_a(j, 0);
 #pragma unroll
-    for (int j = 0; j < kTM; ++j) load_sa(0, j, 0);
+    for (int j = 0; j < TM; ++j) load_sa(0, j, 0);
 #pragma unroll
     for (int i = 0; i < kWN; ++i) {
         load_sw(0, i, 0);
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
         for (int q = 0; q < 4; ++q) load_w(0, i, q, 0);
     }
 #pragma unroll
-    for (int j = 0; j < kTM; ++j) {
+    for (int j = 0; j < TM; ++j) {
         put_a(smem[0], j);
         load_a(j, min_u32(1u, slabs - 1u));
     }
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
     }
 
 #pragma unroll
-    for (int j = 0; j < kTM; ++j)
+    for (int j = 0; j < TM; ++j)
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
             float v[16];
@@ -474,32 +474,56 @@ void launch_split(Args& P, uint32_t a_groups, uint32_t w_groups, hipStream_t st)
     mx_gemm_split_kernel<TM, WN, KS, GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * KS, 0, st>>>(P);
 }
 
+template <int TM, bool GATED, int OUT>
+void launch_tile(Args& P, uint32_t a_groups, hipStream_t st) {
+    P.tiles_m = (a_groups + TM - 1) / TM;
+    P.group_m = min_u32(P.tiles_m, 32u / TM);
+    mx_gemm_tile_kernel<TM, GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * kNW, 0, st>>>(P);
+}
+
 // The kernel goes by the number of 32 x 32 block products of a K step, the
 // gate's and the up's counted: few blocks take small workgroups with K split
-// eight ways, then larger ones split four ways, many the tile kernel.  K
-// itself does not matter: every candidate's time is nearly linear in it.
-// Measured around the bounds, K = 3584 (us: 1x1 / 2x1 / 2x2 blocks / tile):
-//   256 blocks (512 x 512)     3.9 /  4.7 /  5.5 / 11.7
-//   288        (37 x 4608)     5.1 /  4.7 /  5.6 / 11.3
-//   448        (128 x 3584)    5.4 /  5.0 /  5.8 / 11.8
-//   896        (256 x 3584)    8.5 /  7.3 /  6.4 / 11.9   (K = 18944: 28 / 22 / 17 / 46)
-//   1024       (2048 x 512)   10.2 /  9.7 /  8.3 / 12.0
-//   1792       (512 x 3584)   13.2 / 12.3 /  9.5 / 12.1
-//   2048       (4096 x 512)   20.1 / 20.6 / 12.9 / 12.3
-//   2368       (128 x 18944)  18.0 / 15.4 / 13.7 / 12.6
-// gated (us: 1x2 / 2x2 / tile): 1152 blocks (128 x 4608) 10.0 / 9.5 / 12.4,
-// 2368 (37 x 18944) 16.5 / 16.3 / 14.4.  A single row group keeps the 1-high
-// workgroups (16 x 18944 gated, 1184 blocks: 13.9 / 15.3 / 13.8).
+// eight ways, then larger ones split four ways, many the tile kernel.  The
+// splits' times are nearly linear in K like the tile kernel's, so K does not
+// matter between them; a 64-token tile starts and ends sooner than a four-way
+// split but takes longer a step, so short K moves to it earlier.
+// Measured, K = 3584 (us: 1x1 / 2x1 / 2x2 blocks / 64-token tile):
+//   256 blocks (512 x 512)     3.9 /  4.7 /  5.5 /
+//   288        (37 x 4608)     5.1 /  4.7 /  5.6 /
+//   448        (128 x 3584)    5.4 /  5.0 /  5.8 /
+//   896        (256 x 3584)    8.5 /  7.3 /  6.4 /  9.6
+//   1024       (2048 x 512)   10.2 /  9.7 /  8.3 /  9.5
+//   1792       (512 x 3584)   13.2 / 12.3 /  9.6 /  9.7
+//   2304       (512 x 4608)           /     / 13.1 / 10.0
+// and (2x2 blocks / tile) 256 x 4608, 1152 blocks, with K = 1024 5.7 / 4.5,
+// 2048 6.8 / 5.9, 2560 7.5 / 7.7, 18944 28.5 / 37; 512 x 3584 with K = 1024
+// 6.1 / 4.6, 2560 8.2 / 7.9, 18944 29.6 / 36.6.  Gated (1x2 / 2x2): 1152
+// blocks (128 x 4608) 10.0 / 9.5.  A single row group keeps the 1-high
+// workgroups until the tile (16 x 18944 gated, 1184 blocks: 13.9, 15.3 with
+// 2x2, 12.8 the tile).  An odd number of row groups counts as the even one
+// that 2x2 blocks and tiles compute (96 x 18944: 13.1 / 10.3).
+//
+// Tiles of 64 tokens do 0.8 of the work a second that those of 128 do (the
+// weights' loads serve half as many MFMAs), but where they still fit the 256
+// CUs once, more of the CUs work (640 x 3584: 11.9 -> 10.0 us, K = 18944 44 ->
+// 37; 1024 x 3584 x 18944 47.6 -> 43.1), and they waste less on ragged
+// batches (gated 160 x 18944: 28.7 -> 18.9).  So turns of the 256 CUs are
+// counted for both, a 64-token turn as two thirds of the other (10 of 14 us
+// at K = 3584, 78 of 113 at K = 18944).  Where that chooses 128: 1280 x 3584 14.1,
+// 18.1 with 64; 2048 x 3584 x 18944 65 and 78.
 template <bool GATED, int OUT>
 void launch_as(Args P, hipStream_t st) {
     const uint32_t a_groups = pad32(P.m) / 32u, w_groups = pad32(P.n) / 32u;
-    const uint64_t blocks = (uint64_t)a_groups * w_groups * (GATED ? 2 : 1);
-    if (blocks > (a_groups == 1 ? 1200u : 2000u)) {
+    const uint64_t row = (uint64_t)w_groups * (GATED ? 2 : 1), blocks = a_groups * row;
+    const uint64_t paired = a_groups == 1 ? row : ((a_groups + 1u) & ~1u) * row;
+    if (paired > (a_groups == 1 || P.k <= 2048u ? 1100u : 2100u)) {
         constexpr uint32_t cols = (GATED ? kWN / 2 : kWN) * kNW;
-        P.tiles_m = (a_groups + kTM - 1) / kTM;
         P.tiles_n = (w_groups + cols - 1) / cols;
-        P.group_m = min_u32(P.tiles_m, 8u);
-        mx_gemm_tile_kernel<GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * kNW, 0, st>>>(P);
+        const uint32_t high = (a_groups + 3u) / 4u * P.tiles_n, low = (a_groups + 1u) / 2u * P.tiles_n;
+        if (2u * ((low + 255u) / 256u) < 3u * ((high + 255u) / 256u))
+            launch_tile<2, GATED, OUT>(P, a_groups, st);
+        else
+            launch_tile<4, GATED, OUT>(P, a_groups, st);
     } else if (a_groups > 1 && blocks > (GATED ? 600u : 800u)) {
         launch_split<2, 2, 4, GATED, OUT>(P, a_groups, w_groups, st);
     } else if constexpr (GATED) {
