@@ -195,15 +195,15 @@ __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[1
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel: 32 TM tokens (128, or 64) x 256 weight rows a workgroup (gated:
+// Tile kernel: 32 TM tokens (64 to 192) x 256 weight rows a workgroup (gated:
 // 128 gate and 128 up rows of the same columns), four waves along the weight
 // rows, each 32 TM x 64: TM activation blocks x kWN weight blocks.
 //
 // The four waves read the same activation blocks, so those go through LDS
 // (two 16 KB stages of 256 columns, one barrier each); a weight block is
 // used by one wave only and goes from the L2 straight to registers, a step
-// ahead.  With 242 registers and 32 KB of LDS two workgroups share a CU:
-// while one stores its tile or waits, the other computes.
+// ahead.  At 128 tokens, with 242 registers and 32 KB of LDS, two workgroups
+// share a CU: while one stores its tile or waits, the other computes.
 //
 // Measured (random codes, M = 2048): gated N=18944 K=3584 133 us, 4.2
 // PFLOP/s, of it 11 us that a copy without the store does not take; down
@@ -220,7 +220,7 @@ __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[1
 constexpr int kWN = 2, kNW = 4;
 
 template <int TM, bool GATED, int OUT>
-__global__ __launch_bounds__(64 * kNW, 2) void mx_gemm_tile_kernel(Args P) {
+__global__ __launch_bounds__(64 * kNW, TM > 4 ? 1 : 2) void mx_gemm_tile_kernel(Args P) {
     constexpr int kCols = GATED ? kWN / 2 : kWN;  // output blocks of a wave
     constexpr int kSides = GATED ? 2 : 1;
     static_assert(64 * kNW == 256, "a thread stages 16 of a row group's 4096 bytes");
@@ -481,6 +481,47 @@ void launch_tile(Args& P, uint32_t a_groups, hipStream_t st) {
     mx_gemm_tile_kernel<TM, GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * kNW, 0, st>>>(P);
 }
 
+// Row groups of a tile: those with the least cost, turns of the 256 CUs times
+// what a turn of that height takes.  Two 128-token tiles on a CU do the most
+// work a second; lower ones fill the CUs and waste less of a ragged batch
+// where there are few, higher ones (one workgroup a CU, 330 to 430 registers)
+// save a second turn that would be mostly idle, where a long K outweighs their
+// slower start and end.  Measured (us, by tokens a tile, the one taken
+// in brackets; the others with the same choice of everything else):
+//                                 64     96    128    160    192
+//   640 x 3584 x 3584          [10.0]          11.9
+//   gated 160 x 18944 x 3584   [18.9]   24.7   28.7   18.1   19.3
+//   2048 x 4608 x 3584          26.5  [22.6]   29.7   22.5   23.7
+//   1280 x 3584 x 3584          18.1    13.2 [14.1]   15.2   16.6
+//   1024 x 3584 x 18944        [43.1]          47.6
+//   2048 x 4608 x 18944        114      95    107   [81.9]   87.7
+//   2300 x 4608 x 18944                 98    111    138   [94.3]
+//   1500 x 3584 x 18944               [52.8]   57.7   63.3   64.7
+//   2048 x 3584 x 18944         78            [65]            72
+//   2048 x 18944 x 3584         90            [76]            89
+// A 96-token tile alone on a CU is not surely faster than a 128-token one
+// unless the batch is ragged or K long (1500 x 3584 with K = 2048: 11.9 and
+// 10.7).  Tiles of 224 and 256 tokens: 94 and 90 for 2048 x 4608 x 18944, 110
+// and 128 (of 118 and 127) for 3500 x 3584 and 3400 x 4608, and the gated ones
+// spill registers.
+uint32_t tile_height(uint32_t a_groups, uint32_t tiles_n, uint32_t k) {
+    auto tiles = [&](uint32_t tm) { return (a_groups + tm - 1) / tm * tiles_n; };
+    auto cost = [&](uint32_t tm, uint32_t turn) { return (tiles(tm) + 255u) / 256u * turn; };
+    const bool deep = k > 4096u;
+    uint32_t best = 4, least = cost(4, 32);
+    auto consider = [&](uint32_t tm, uint32_t turn) {
+        if (cost(tm, turn) < least) {
+            best = tm;
+            least = cost(tm, turn);
+        }
+    };
+    consider(2, 22);
+    if (deep || tiles(3) > 256u || tiles(3) == tiles(4)) consider(3, 28);
+    if (deep && tiles(5) <= 256u) consider(5, 36);
+    if (deep && tiles(6) <= 256u) consider(6, 40);
+    return best;
+}
+
 // The kernel goes by the number of 32 x 32 block products of a K step, the
 // gate's and the up's counted: few blocks take small workgroups with K split
 // eight ways, then larger ones split four ways, many the tile kernel.  The
@@ -502,15 +543,6 @@ void launch_tile(Args& P, uint32_t a_groups, hipStream_t st) {
 // workgroups until the tile (16 x 18944 gated, 1184 blocks: 13.9, 15.3 with
 // 2x2, 12.8 the tile).  An odd number of row groups counts as the even one
 // that 2x2 blocks and tiles compute (96 x 18944: 13.1 / 10.3).
-//
-// Tiles of 64 tokens do 0.8 of the work a second that those of 128 do (the
-// weights' loads serve half as many MFMAs), but where they still fit the 256
-// CUs once, more of the CUs work (640 x 3584: 11.9 -> 10.0 us, K = 18944 44 ->
-// 37; 1024 x 3584 x 18944 47.6 -> 43.1), and they waste less on ragged
-// batches (gated 160 x 18944: 28.7 -> 18.9).  So turns of the 256 CUs are
-// counted for both, a 64-token turn as two thirds of the other (10 of 14 us
-// at K = 3584, 78 of 113 at K = 18944).  Where that chooses 128: 1280 x 3584 14.1,
-// 18.1 with 64; 2048 x 3584 x 18944 65 and 78.
 template <bool GATED, int OUT>
 void launch_as(Args P, hipStream_t st) {
     const uint32_t a_groups = pad32(P.m) / 32u, w_groups = pad32(P.n) / 32u;
@@ -519,11 +551,13 @@ void launch_as(Args P, hipStream_t st) {
     if (paired > (a_groups == 1 || P.k <= 2048u ? 1100u : 2100u)) {
         constexpr uint32_t cols = (GATED ? kWN / 2 : kWN) * kNW;
         P.tiles_n = (w_groups + cols - 1) / cols;
-        const uint32_t high = (a_groups + 3u) / 4u * P.tiles_n, low = (a_groups + 1u) / 2u * P.tiles_n;
-        if (2u * ((low + 255u) / 256u) < 3u * ((high + 255u) / 256u))
-            launch_tile<2, GATED, OUT>(P, a_groups, st);
-        else
-            launch_tile<4, GATED, OUT>(P, a_groups, st);
+        switch (tile_height(a_groups, P.tiles_n, P.k)) {
+            case 2: return launch_tile<2, GATED, OUT>(P, a_groups, st);
+            case 3: return launch_tile<3, GATED, OUT>(P, a_groups, st);
+            case 5: return launch_tile<5, GATED, OUT>(P, a_groups, st);
+            case 6: return launch_tile<6, GATED, OUT>(P, a_groups, st);
+            default: return launch_tile<4, GATED, OUT>(P, a_groups, st);
+        }
     } else if (a_groups > 1 && blocks > (GATED ? 600u : 800u)) {
         launch_split<2, 2, 4, GATED, OUT>(P, a_groups, w_groups, st);
     } else if constexpr (GATED) {

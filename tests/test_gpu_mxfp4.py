@@ -163,11 +163,13 @@ SHAPES = [(1, 1, 256), (1, 33, 512), (31, 64, 768), (37, 129, 3584), (64, 32, 23
 MEDIUM = [(100, 2500, 1024), (70, 3300, 512), (290, 3001, 768), (97, 8100, 256), (250, 7000, 2304)]
 # ... for tiles of 64 tokens: short K, ragged, odd numbers of K steps, one row group ...
 LOW = [(449, 4608, 512), (513, 2050, 1280), (129, 19000, 256), (33, 18944, 2304), (64, 12000, 256), (17, 40000, 768)]
-# ... and for those of 128
+# ... of 96, 160 and 192 (long K) ...
+TALL = [(1700, 4800, 512), (96, 35000, 256), (4135, 2300, 4352), (4135, 2500, 4352)]
+# ... and of 128
 LARGE = [(2048, 3328, 256), (1541, 4001, 768), (4097, 1500, 512), (20, 38500, 256)]
 
 
-@pytest.mark.parametrize("m,n,k", SHAPES + MEDIUM + LOW + LARGE)
+@pytest.mark.parametrize("m,n,k", SHAPES + MEDIUM + LOW + TALL + LARGE)
 def test_gemm(rz, m, n, k):
     print(f"mxfp4 gemm m={m} n={n} k={k}", flush=True)
     a, w = random_tensor(1000 + m, m, k, 3), random_tensor(2000 + n, n, k, 3)
@@ -177,7 +179,7 @@ def test_gemm(rz, m, n, k):
     assert (host(y[m:]) == 7).all()
 
 
-@pytest.mark.parametrize("m,n", [(5, 40), (100, 2500), (290, 3001), (450, 3001), (1541, 4001)])
+@pytest.mark.parametrize("m,n", [(5, 40), (100, 2500), (290, 3001), (450, 3001), (1700, 4801), (1541, 4001)])
 def test_pad_rows_do_not_matter(rz, m, n):
     """NaN scales and random codes in the operands' pad rows: the same bits as with zeros, gated (and its MXFP4 output) too."""
     k = 512
@@ -253,7 +255,8 @@ def small_scale(t, by):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 1, 256), (37, 129, 3584), (65, 300, 512), (130, 64, 2304), (300, 1000, 768), (2049, 1700, 512),
-                                   (1024, 3500, 768), (7, 19300, 256), (130, 9000, 768), (65, 6100, 256)])
+                                   (1024, 3500, 768), (7, 19300, 256), (130, 9000, 768), (65, 6100, 256),
+                                   (1700, 2400, 768), (4135, 1100, 4352), (4135, 1250, 4352)])
 def test_gated(rz, m, n, k):
     print(f"mxfp4 gated m={m} n={n} k={k}", flush=True)
     a, g, u = random_tensor(30 + m, m, k, 2), small_scale(random_tensor(31, n, k, 2), 8), small_scale(random_tensor(32, n, k, 2), 8)
@@ -263,7 +266,8 @@ def test_gated(rz, m, n, k):
     assert (host(h[m:]) == 7).all()
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 256, 256), (37, 512, 512), (100, 256, 3584), (333, 1024, 512), (200, 4608, 512), (97, 4864, 1792), (1990, 1792, 512)])
+@pytest.mark.parametrize("m,n,k", [(1, 256, 256), (37, 512, 512), (100, 256, 3584), (333, 1024, 512), (200, 4608, 512), (97, 4864, 1792), (1990, 1792, 512),
+                                   (1700, 2560, 768), (4135, 1024, 4352), (4135, 1280, 4352)])
 def test_gated_quant_is_quant_of_gated(rz, m, n, k):
     """Codes and bytes equal those of quantising the fp32 result, pad rows included."""
     a, g, u = tiled(random_tensor(40, m, k, 2)), tiled(small_scale(random_tensor(41, n, k, 2), 8)), tiled(small_scale(random_tensor(42, n, k, 2), 8))
@@ -273,7 +277,7 @@ def test_gated_quant_is_quant_of_gated(rz, m, n, k):
     same(hc, tc)
 
 
-@pytest.mark.parametrize("m,n", [(40, 256), (400, 1024), (269, 4096), (1600, 2048)])
+@pytest.mark.parametrize("m,n", [(40, 256), (400, 1024), (269, 4096), (1700, 2560), (1600, 2048)])
 def test_gated_quant_nan_rows(rz, m, n):
     """NaN blocks in one token and in one gate row: exactly their blocks read as NaN, the rest as without them."""
     k = 512
