@@ -48,6 +48,24 @@ std::string shape_text(c10::IntArrayRef s) {
     refuse(o.str());
 }
 
+void in_range(int64_t v, const char* what, int64_t lo, int64_t hi) {
+    if (v < lo || v > hi) {
+        std::ostringstream o;
+        o << what << "=" << v << ": expected " << lo << " to " << hi;
+        refuse(o.str());
+    }
+}
+
+// Every size here goes to the library as a uint32.
+constexpr int64_t kMaxSize = 0xFFFFFFFFll;
+
+// Size `axis` of t times `per`, in that range.
+int64_t size_of(const Tensor& t, int64_t axis, const char* what, int64_t per = 1) {
+    const int64_t v = t.size(axis);
+    in_range(v > kMaxSize ? v : v * per, what, 0, kMaxSize);
+    return v * per;
+}
+
 // The arguments of one call, in order.
 struct Args {
     PyObject* const* a;
@@ -59,17 +77,13 @@ struct Args {
     }
     bool none(Py_ssize_t i) const { return a[i] == Py_None; }
     // a whole number in [lo, hi]
-    int64_t number(Py_ssize_t i, const char* what, int64_t lo = 0, int64_t hi = 0xFFFFFFFFll) const {
+    int64_t number(Py_ssize_t i, const char* what, int64_t lo = 0, int64_t hi = kMaxSize) const {
         PyObject* x = PyNumber_Index(a[i]);
         if (!x) throw python_error();
         const int64_t v = PyLong_AsLongLong(x);
         Py_DECREF(x);
         if (v == -1 && PyErr_Occurred()) throw python_error();
-        if (v < lo || v > hi) {
-            std::ostringstream o;
-            o << what << "=" << v << ": expected " << lo << " to " << hi;
-            refuse(o.str());
-        }
+        in_range(v, what, lo, hi);
         return v;
     }
 };
@@ -136,7 +150,7 @@ struct Mx {
     const Tensor &codes, &scales;
     int64_t k;
     Mx(const Args& A, Py_ssize_t i, int64_t rows, const char* what)
-        : codes(A.tensor(i, what)), scales(A.tensor(i + 1, what)), k(codes.dim() == 3 ? codes.size(1) * 64 : 0) {
+        : codes(A.tensor(i, what)), scales(A.tensor(i + 1, what)), k(codes.dim() == 3 ? size_of(codes, 1, "k", 64) : 0) {
         const int64_t g = (rows + 31) / 32;
         need(codes, what, at::kByte, Shape{g, k / 64, 1024});
         need(scales, what, at::kByte, Shape{g, k / 256, 256});
@@ -172,7 +186,7 @@ at::ScalarType dtype_of(int64_t id) { return id == RZ_F32 ? at::kFloat : id == R
 PyObject* mxfp4_quant(const Args& A) {
     const Tensor& x = A.tensor(0, "x");
     if (x.dim() != 2) refuse("x: expected 2 dimensions, got " + shape_text(x.sizes()));
-    const int64_t m = x.size(0), k = x.size(1);
+    const int64_t m = size_of(x, 0, "m"), k = size_of(x, 1, "k");
     need(x, "x", at::kFloat, Shape{m, k});
     const Device dev(x);
     MxOut o(A, 1, m, k, "output", dev);
@@ -252,7 +266,7 @@ PyObject* mxfp4_gated_quant(const Args& A) {
 
 // x fp32 [m][k] of a GEMV.
 int64_t gemv_rows(const Tensor& x, int64_t k) {
-    const int64_t m = x.dim() == 2 ? x.size(0) : 0;
+    const int64_t m = x.dim() == 2 ? size_of(x, 0, "m") : 0;
     need(x, "x", at::kFloat, Shape{m, k});
     return m;
 }
@@ -296,9 +310,9 @@ struct Cache {
           vc(A.tensor(j + 2, "v_codes")), vs(A.tensor(j + 3, "v_scales")) {
         if (kc.dim() != 3) refuse("k_codes: expected 3 dimensions, got " + shape_text(kc.sizes()));
         slots = kc.size(0);
-        heads = kc.size(1);
+        heads = size_of(kc, 1, "heads");
         const int64_t width = kc.size(2);
-        dim = fmt == RZ_KV_E4M3 ? width : 2 * width;
+        dim = size_of(kc, 2, "dim", fmt == RZ_KV_E4M3 ? 1 : 2);
         need(kc, "k_codes", at::kByte, Shape{slots, heads, width});
         need(vc, "v_codes", at::kByte, Shape{slots, heads, width});
         for (const Tensor* s : {&ks, &vs}) {
@@ -325,7 +339,7 @@ int64_t token_stride(const Tensor& t, const char* what, int64_t tokens, int64_t 
 PyObject* kv_cache_write(const Args& A) {
     const Cache c(A, 0, 4);
     const Tensor &k = A.tensor(1, "k"), &v = A.tensor(2, "v"), &slots = A.tensor(3, "slots");
-    const int64_t tokens = k.dim() == 3 ? k.size(0) : 0;
+    const int64_t tokens = k.dim() == 3 ? size_of(k, 0, "tokens") : 0;
     const int64_t ks = token_stride(k, "k", tokens, c.heads, c.dim), vs = token_stride(v, "v", tokens, c.heads, c.dim);
     need(slots, "slots", at::kLong, Shape{tokens});
     const Device dev(k);
@@ -343,7 +357,7 @@ PyObject* kv_cache_read(const Args& A) {
     const int64_t page_len = A.number(5, "page_len", 1), rows = A.number(8, "rows"), id = A.number(11, "dtype", 0, 2);
     const Tensor &table = A.tensor(6, "page_table"), &offsets = A.tensor(7, "offsets");
     if (table.dim() != 2) refuse("page_table: expected 2 dimensions, got " + shape_text(table.sizes()));
-    const int64_t seqs = table.size(0), pages = table.size(1);
+    const int64_t seqs = size_of(table, 0, "sequences"), pages = size_of(table, 1, "pages");
     need(table, "page_table", at::kInt, Shape{seqs, pages});
     need(offsets, "offsets", at::kInt, Shape{seqs + 1});
     const Device dev(c.kc);
