@@ -484,25 +484,13 @@ def rz_mxfp4_pad_rows(rows: int) -> int:
     return (rows + 31) // 32 * 32
 
 
-def _mx_empty(rows, k, codes, scales, device, stream):
-    """The outputs of a call on another stream than the current one."""
-    u8 = _torch().uint8
-    g = (rows + 31) // 32
-    return (_empty((g, k // 64, 1024), u8, device, stream) if codes is None else codes,
-            _empty((g, k // 256, 256), u8, device, stream) if scales is None else scales)
-
-
 def rz_mxfp4_quant(x, codes=None, scales=None, stream=None):
     """x fp32 [m][k] -> MXFP4 (codes, scales), pad rows included."""
-    if stream is not None:
-        codes, scales = _mx_empty(*x.shape, codes, scales, x.device, stream)
     return _native().mxfp4_quant(x, codes, scales, _handle(stream))
 
 
 def rz_mxfp4_pack_weight(qtype: int, blocks, n: int, k: int, codes=None, scales=None, stream=None):
     """A K-quant weight -> MXFP4 (codes, scales)."""
-    if stream is not None:
-        codes, scales = _mx_empty(n, k, codes, scales, blocks.device, stream)
     return _native().mxfp4_pack_weight(qtype, blocks, n, k, codes, scales, _handle(stream))
 
 
@@ -522,31 +510,23 @@ def rz_mxfp4_dequant(codes, scales, rows: int, out=None, dtype=None, stream=None
     """MXFP4 -> out [rows][k] of dtype (default: out's, or float32)."""
     if dtype is None:
         dtype = _torch().float32 if out is None else out.dtype
-    if stream is not None and out is None:
-        out = _empty((rows, codes.shape[1] * 64), dtype, codes.device, stream)
     return _native().mxfp4_dequant(codes, scales, rows, out, _dtype_id(dtype), _handle(stream))
 
 
 def rz_mxfp4_gemm(a_codes, a_scales, m: int, w_codes, w_scales, n: int, y=None, stream=None):
     """-> y fp32 [m][n] = a @ w^T of MXFP4 a [m][k] and w [n][k]."""
-    if stream is not None and y is None:
-        y = _empty((m, n), _torch().float32, a_codes.device, stream)
     return _native().mxfp4_gemm(a_codes, a_scales, m, w_codes, w_scales, n, y, _handle(stream))
 
 
 def rz_mxfp4_gated(a_codes, a_scales, m: int, gate, up, n: int, h=None, stream=None):
     """-> h fp32 [m][n] = silu(a @ gate^T) * (a @ up^T); gate and up are
     MXFP4 (codes, scales) pairs of [n][k]."""
-    if stream is not None and h is None:
-        h = _empty((m, n), _torch().float32, a_codes.device, stream)
     return _native().mxfp4_gated(a_codes, a_scales, m, *gate, *up, n, h, _handle(stream))
 
 
 def rz_mxfp4_gated_quant(a_codes, a_scales, m: int, gate, up, n: int, h_codes=None, h_scales=None, stream=None):
     """rz_mxfp4_gated with its result as MXFP4 -> (h_codes, h_scales), the
     down projection's operand (n a multiple of 256)."""
-    if stream is not None:
-        h_codes, h_scales = _mx_empty(m, n, h_codes, h_scales, a_codes.device, stream)
     return _native().mxfp4_gated_quant(a_codes, a_scales, m, *gate, *up, n, h_codes, h_scales, _handle(stream))
 
 
@@ -555,16 +535,12 @@ MXFP4_GEMV_MAX_M = 8
 
 def rz_mxfp4_gemv(w_codes, w_scales, n: int, x, y=None, stream=None):
     """-> y fp32 [m][n] = x @ w^T, x fp32 [m][k] with m <= MXFP4_GEMV_MAX_M."""
-    if stream is not None and y is None:
-        y = _empty((x.shape[0], n), _torch().float32, x.device, stream)
     return _native().mxfp4_gemv(w_codes, w_scales, n, x, y, _handle(stream))
 
 
 def rz_mxfp4_gated_gemv(gate, up, n: int, x, h=None, stream=None):
     """-> h fp32 [m][n] = silu(x @ gate^T) * (x @ up^T), x fp32 [m][k] with
     m <= MXFP4_GEMV_MAX_M."""
-    if stream is not None and h is None:
-        h = _empty((x.shape[0], n), _torch().float32, x.device, stream)
     return _native().mxfp4_gated_gemv(*gate, *up, n, x, h, _handle(stream))
 
 
@@ -590,10 +566,6 @@ def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: i
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else _torch().float32
     did = _dtype_id(dtype)
-    if stream is not None:
-        shape = (rows, k_codes.shape[1], k_codes.shape[2] * (1 if fmt == KV_E4M3 else 2))
-        k_out = _empty(shape, dtype, k_codes.device, stream) if k_out is None else k_out
-        v_out = _empty(shape, dtype, k_codes.device, stream) if v_out is None else v_out
     return _native().kv_cache_read(fmt, k_codes, k_scales, v_codes, v_scales, page_len, page_table, offsets, rows, k_out, v_out, did,
                                    _handle(stream))
 

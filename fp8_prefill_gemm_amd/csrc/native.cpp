@@ -110,32 +110,44 @@ struct Device {
     }
 };
 
-// The output argument i, checked, or a new tensor from torch's allocator
-// (for the current stream: a call on another one passes its outputs).
-Tensor output(const Args& A, Py_ssize_t i, const char* what, at::ScalarType dtype, c10::IntArrayRef shape, const Device& dev) {
-    if (A.none(i)) return at::empty(shape, dev.first.options().dtype(dtype).layout(at::kStrided).requires_grad(false));
+// The stream of a call, argument i: a handle, or None for torch's current
+// stream on the call's device.  For the object's life it is torch's current
+// one there, so that the outputs made below are the allocator's blocks for it.
+struct OnStream {
+    const Device& dev;
+    const c10::hip::HIPStream before;
+    void* handle;
+    OnStream(const Args& A, Py_ssize_t i, const Device& d)
+        : dev(d), before(c10::hip::getCurrentHIPStream(d.first.get_device())), handle(before.stream()) {
+        if (A.none(i)) return;
+        handle = PyLong_AsVoidPtr(A.a[i]);
+        if (PyErr_Occurred()) throw python_error();
+        if (other()) c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(static_cast<hipStream_t>(handle), d.first.get_device()));
+    }
+    ~OnStream() {
+        if (other()) c10::hip::setCurrentHIPStream(before);
+    }
+    bool other() const { return handle != before.stream(); }
+    OnStream(const OnStream&) = delete;
+};
+
+// The output argument i, checked, or a new tensor.
+Tensor output(const Args& A, Py_ssize_t i, const char* what, at::ScalarType dtype, c10::IntArrayRef shape, const OnStream& on) {
+    if (A.none(i)) return at::empty(shape, on.dev.first.options().dtype(dtype).layout(at::kStrided).requires_grad(false));
     const Tensor& t = A.tensor(i, what);
     need(t, what, dtype, shape);
-    dev.same({&t});
+    on.dev.same({&t});
     return t;
 }
 
-// Calls f(stream) with `dev` current; stream argument i: a handle, or None
-// for torch's current stream.
+// Calls f(stream) with the call's device current.
 template <typename F>
-void call(const Args& A, Py_ssize_t i, const Device& dev, F&& f) {
-    const int index = dev.first.get_device();
-    void* stream;
-    if (A.none(i)) {
-        stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)index).stream();
-    } else {
-        stream = PyLong_AsVoidPtr(A.a[i]);
-        if (PyErr_Occurred()) throw python_error();
-    }
+void call(const OnStream& on, F&& f) {
+    const int index = on.dev.first.get_device();
     int current = index;
     const bool other = hipGetDevice(&current) == hipSuccess && current != index;
     if (other) (void)hipSetDevice(index);
-    const int status = f(stream);
+    const int status = f(on.handle);
     if (other) (void)hipSetDevice(current);
     if (status != RZ_OK) throw Failed{status};
 }
@@ -163,10 +175,10 @@ void same_k(const Mx& a, const Mx& b, const char* what) {
 
 struct MxOut {
     Tensor codes, scales;
-    MxOut(const Args& A, Py_ssize_t i, int64_t rows, int64_t k, const char* what, const Device& dev) {
+    MxOut(const Args& A, Py_ssize_t i, int64_t rows, int64_t k, const char* what, const OnStream& on) {
         const int64_t g = (rows + 31) / 32;
-        codes = output(A, i, what, at::kByte, Shape{g, k / 64, 1024}, dev);
-        scales = output(A, i + 1, what, at::kByte, Shape{g, k / 256, 256}, dev);
+        codes = output(A, i, what, at::kByte, Shape{g, k / 64, 1024}, on);
+        scales = output(A, i + 1, what, at::kByte, Shape{g, k / 256, 256}, on);
     }
 };
 
@@ -189,8 +201,9 @@ PyObject* mxfp4_quant(const Args& A) {
     const int64_t m = size_of(x, 0, "m"), k = size_of(x, 1, "k");
     need(x, "x", at::kFloat, Shape{m, k});
     const Device dev(x);
-    MxOut o(A, 1, m, k, "output", dev);
-    call(A, 3, dev, [&](void* st) { return rz_mxfp4_quant(ptr<float>(x), m, k, ptr(o.codes), ptr(o.scales), st); });
+    const OnStream on(A, 3, dev);
+    MxOut o(A, 1, m, k, "output", on);
+    call(on, [&](void* st) { return rz_mxfp4_quant(ptr<float>(x), m, k, ptr(o.codes), ptr(o.scales), st); });
     return wrap2(o.codes, o.scales);
 }
 
@@ -202,8 +215,9 @@ PyObject* mxfp4_pack_weight(const Args& A) {
     const int64_t bytes = (int64_t)rz_weight_bytes((int)qtype, n, k);
     if (b.numel() < bytes) refuse("blocks: " + std::to_string(b.numel()) + " bytes, " + std::to_string(bytes) + " needed");
     const Device dev(b);
-    MxOut o(A, 4, n, k, "output", dev);
-    call(A, 6, dev, [&](void* st) { return rz_mxfp4_pack_weight((int)qtype, ptr(b), n, k, ptr(o.codes), ptr(o.scales), st); });
+    const OnStream on(A, 6, dev);
+    MxOut o(A, 4, n, k, "output", on);
+    call(on, [&](void* st) { return rz_mxfp4_pack_weight((int)qtype, ptr(b), n, k, ptr(o.codes), ptr(o.scales), st); });
     return wrap2(o.codes, o.scales);
 }
 
@@ -213,8 +227,9 @@ PyObject* mxfp4_dequant(const Args& A) {
     const Mx c(A, 0, rows, "input");
     const Device dev(c.codes);
     dev.same({&c.scales});
-    const Tensor out = output(A, 3, "out", dtype_of(id), Shape{rows, c.k}, dev);
-    call(A, 5, dev, [&](void* st) { return rz_mxfp4_dequant(ptr(c.codes), ptr(c.scales), rows, c.k, (int)id, ptr<void>(out), st); });
+    const OnStream on(A, 5, dev);
+    const Tensor out = output(A, 3, "out", dtype_of(id), Shape{rows, c.k}, on);
+    call(on, [&](void* st) { return rz_mxfp4_dequant(ptr(c.codes), ptr(c.scales), rows, c.k, (int)id, ptr<void>(out), st); });
     return wrap(out);
 }
 
@@ -225,8 +240,9 @@ PyObject* mxfp4_gemm(const Args& A) {
     same_k(a, w, "a and w");
     const Device dev(a.codes);
     dev.same({&a.scales, &w.codes, &w.scales});
-    const Tensor y = output(A, 6, "y", at::kFloat, Shape{m, n}, dev);
-    call(A, 7, dev, [&](void* st) {
+    const OnStream on(A, 7, dev);
+    const Tensor y = output(A, 6, "y", at::kFloat, Shape{m, n}, on);
+    call(on, [&](void* st) {
         return rz_mxfp4_gemm(ptr(a.codes), ptr(a.scales), m, ptr(w.codes), ptr(w.scales), n, a.k, ptr<float>(y), st);
     });
     return wrap(y);
@@ -240,8 +256,9 @@ PyObject* mxfp4_gated(const Args& A) {
     same_k(a, u, "a and up");
     const Device dev(a.codes);
     dev.same({&a.scales, &g.codes, &g.scales, &u.codes, &u.scales});
-    const Tensor h = output(A, 8, "h", at::kFloat, Shape{m, n}, dev);
-    call(A, 9, dev, [&](void* st) {
+    const OnStream on(A, 9, dev);
+    const Tensor h = output(A, 8, "h", at::kFloat, Shape{m, n}, on);
+    call(on, [&](void* st) {
         return rz_mxfp4_gated(ptr(a.codes), ptr(a.scales), m, ptr(g.codes), ptr(g.scales), ptr(u.codes), ptr(u.scales), n, a.k,
                               ptr<float>(h), st);
     });
@@ -256,8 +273,9 @@ PyObject* mxfp4_gated_quant(const Args& A) {
     same_k(a, u, "a and up");
     const Device dev(a.codes);
     dev.same({&a.scales, &g.codes, &g.scales, &u.codes, &u.scales});
-    MxOut o(A, 8, m, n, "h", dev);
-    call(A, 10, dev, [&](void* st) {
+    const OnStream on(A, 10, dev);
+    MxOut o(A, 8, m, n, "h", on);
+    call(on, [&](void* st) {
         return rz_mxfp4_gated_quant(ptr(a.codes), ptr(a.scales), m, ptr(g.codes), ptr(g.scales), ptr(u.codes), ptr(u.scales), n,
                                     a.k, ptr(o.codes), ptr(o.scales), st);
     });
@@ -279,8 +297,9 @@ PyObject* mxfp4_gemv(const Args& A) {
     const int64_t m = gemv_rows(x, w.k);
     const Device dev(x);
     dev.same({&w.codes, &w.scales});
-    const Tensor y = output(A, 4, "y", at::kFloat, Shape{m, n}, dev);
-    call(A, 5, dev, [&](void* st) { return rz_mxfp4_gemv(ptr(w.codes), ptr(w.scales), n, w.k, ptr<float>(x), m, ptr<float>(y), st); });
+    const OnStream on(A, 5, dev);
+    const Tensor y = output(A, 4, "y", at::kFloat, Shape{m, n}, on);
+    call(on, [&](void* st) { return rz_mxfp4_gemv(ptr(w.codes), ptr(w.scales), n, w.k, ptr<float>(x), m, ptr<float>(y), st); });
     return wrap(y);
 }
 
@@ -293,8 +312,9 @@ PyObject* mxfp4_gated_gemv(const Args& A) {
     const int64_t m = gemv_rows(x, g.k);
     const Device dev(x);
     dev.same({&g.codes, &g.scales, &u.codes, &u.scales});
-    const Tensor h = output(A, 6, "h", at::kFloat, Shape{m, n}, dev);
-    call(A, 7, dev, [&](void* st) {
+    const OnStream on(A, 7, dev);
+    const Tensor h = output(A, 6, "h", at::kFloat, Shape{m, n}, on);
+    call(on, [&](void* st) {
         return rz_mxfp4_gated_gemv(ptr(g.codes), ptr(g.scales), ptr(u.codes), ptr(u.scales), n, g.k, ptr<float>(x), m,
                                    ptr<float>(h), st);
     });
@@ -344,7 +364,8 @@ PyObject* kv_cache_write(const Args& A) {
     need(slots, "slots", at::kLong, Shape{tokens});
     const Device dev(k);
     dev.same({&v, &slots, &c.kc, &c.ks, &c.vc, &c.vs});
-    call(A, 8, dev, [&](void* st) {
+    const OnStream on(A, 8, dev);
+    call(on, [&](void* st) {
         return rz_kv_cache_write((int)c.fmt, ptr<float>(k), ptr<float>(v), tokens, c.heads, c.dim, ks, vs, ptr<int64_t>(slots),
                                  c.slots, ptr(c.kc), ptr<void>(c.ks), ptr(c.vc), ptr<void>(c.vs), st);
     });
@@ -362,9 +383,10 @@ PyObject* kv_cache_read(const Args& A) {
     need(offsets, "offsets", at::kInt, Shape{seqs + 1});
     const Device dev(c.kc);
     dev.same({&c.ks, &c.vc, &c.vs, &table, &offsets});
-    const Tensor k = output(A, 9, "k_out", dtype_of(id), Shape{rows, c.heads, c.dim}, dev);
-    const Tensor v = output(A, 10, "v_out", dtype_of(id), Shape{rows, c.heads, c.dim}, dev);
-    call(A, 12, dev, [&](void* st) {
+    const OnStream on(A, 12, dev);
+    const Tensor k = output(A, 9, "k_out", dtype_of(id), Shape{rows, c.heads, c.dim}, on);
+    const Tensor v = output(A, 10, "v_out", dtype_of(id), Shape{rows, c.heads, c.dim}, on);
+    call(on, [&](void* st) {
         return rz_kv_cache_read((int)c.fmt, ptr(c.kc), ptr<void>(c.ks), ptr(c.vc), ptr<void>(c.vs), c.slots, c.heads, c.dim,
                                 page_len, ptr<int32_t>(table), seqs, pages, ptr<int32_t>(offsets), rows, (int)id, ptr<void>(k),
                                 ptr<void>(v), st);
