@@ -464,7 +464,7 @@ def _native():
         import importlib.util
         lib()
         _torch()
-        path = _build.NATIVE_PATH
+        path = _build.native_path()
         if not os.path.exists(path):
             raise ImportError(
                 f"{path} is missing: build it with `python -m fp8_prefill_gemm_amd.build`; there is no fallback implementation")

@@ -1,13 +1,15 @@
-"""Ahead-of-time build of librz_fp8.so for gfx950 (hipcc, in-tree) and of the
-binding's native half (g++, against torch and that library).
+"""Ahead-of-time build of librz_fp8.so for gfx950 (hipcc, in-tree) and, as a
+step of its own, of the binding's native half (g++, against torch and that
+library).
 
 The library is the product: HIP kernels plus the C ABI declared in
 include/rz_fp8.h.  It is compiled for gfx950 only, without fast-math, with
 floating-point contraction off and IEEE fp32 division, and with packed fp32
-instructions disabled.
+instructions disabled.  It needs neither Python's nor torch's headers.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -22,8 +24,6 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "kquant.hip", "actquant.hip", "gemm.hip", "gemm_edge.hip", "kgemv.hip", "kqgemm.hip",
            "q8gemm.hip", "mxquant.hip", "mxgemm.hip", "mxgemv.hip", "kvcache.hip"]
 ARCH = "gfx950"
-NATIVE_NAME = "_rz_native.so"
-NATIVE_PATH = os.path.join(PKG_DIR, NATIVE_NAME)
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -46,8 +46,7 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into LIB_PATH and the native half of the
-    binding into NATIVE_PATH (always rebuilds)."""
+    """Compile every HIP source into LIB_PATH (always rebuilds)."""
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), *srcs, "-o", tmp]
@@ -62,15 +61,25 @@ def build(verbose: bool = False) -> str:
     if verbose and msgs:
         print("\n".join(msgs), flush=True)
     os.replace(tmp, LIB_PATH)
-    build_native(verbose)
     return LIB_PATH
 
 
+def native_path() -> str:
+    """The native half's file, named after the torch and Python it is built
+    against: another one's copy is not found rather than loaded."""
+    torch = importlib.metadata.version("torch")
+    return os.path.join(PKG_DIR, f"_rz_native.torch-{torch}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_native(verbose: bool = False) -> str:
-    """csrc/native.cpp -> NATIVE_PATH, linked to the library beside it."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """csrc/native.cpp -> native_path(), linked to the library beside it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("the binding's native half is built against torch, which is not installed")
+    torch_dir = os.path.dirname(spec.origin)
+    path = native_path()
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
-    tmp = NATIVE_PATH + ".tmp"
+    tmp = path + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
            "-isystem", os.path.join(torch_dir, "include"),
@@ -84,9 +93,19 @@ def build_native(verbose: bool = False) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
-    os.replace(tmp, NATIVE_PATH)
-    return NATIVE_PATH
+    os.replace(tmp, path)
+    return path
+
+
+def build_all(verbose: bool = False) -> list[str]:
+    """The library and, where torch is installed, the binding's native half."""
+    made = [build(verbose)]
+    if importlib.util.find_spec("torch") is None:
+        print("torch is not installed: the binding's native half is left out", file=sys.stderr, flush=True)
+    else:
+        made.append(build_native(verbose))
+    return made
 
 
 if __name__ == "__main__":
-    print(build(verbose="-v" in sys.argv))
+    print("\n".join(build_all(verbose="-v" in sys.argv)))
