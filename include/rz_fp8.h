@@ -461,8 +461,11 @@ int rz_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, uint32_t rows,
  *   a_codes, a_scales   MXFP4 [m][k]
  *   w_codes, w_scales   MXFP4 [n][k]
  *   y                   device out, fp32 [m][n] row-major
- * Products are exact; sums are accumulated in fp32.  m == 0 or n == 0 is a
- * no-op (any pointer may then be NULL).
+ * Products are exact, sums fp32: where no partial sum overflows,
+ *   |y - exact| <= gamma_{2k} sum |a w| + 2k 2^-126,
+ * gamma_t = t eps / (1 - t eps), eps = 2^-24: the matrix cores truncate, and
+ * may flush products and partial sums under 2^-126 to zero.  m == 0 or n == 0
+ * is a no-op (any pointer may then be NULL).
  */
 int rz_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* w_codes,
                   const uint8_t* w_scales, uint32_t n, uint32_t k, float* y, void* stream);
@@ -473,8 +476,11 @@ int rz_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, c
  *   h[i][j] = g / (1 + e^-g) * u,  g = a gate^T, u = a up^T   for i < m, j < n
  *   gate_*, up_*   MXFP4 [n][k] each
  *   h              device out, fp32 [m][n] row-major
- * m == 0 or n == 0 is a no-op.  A factor g / (1 + e^-g) under 2^-112 in size
- * may count as 0.  (Forward only: weights here are frozen codes.)
+ * With e_g and e_u the two products' errors (rz_mxfp4_gemm) and s = g / (1 + e^-g),
+ *   |h - exact| <= |h| (2 |g| + 9) eps + 1.1 e_g (|u| + e_u) + |s| e_u + 2^-112 |u|:
+ * the exponential's argument is rounded to fp32, and a factor s under 2^-112
+ * in size may count as 0.  m == 0 or n == 0 is a no-op.  (Forward only:
+ * weights here are frozen codes.)
  */
 int rz_mxfp4_gated(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* gate_codes,
                    const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales, uint32_t n,
@@ -498,12 +504,14 @@ int rz_mxfp4_gated_quant(const uint8_t* a_codes, const uint8_t* a_scales, uint32
  * quantised:  y = x w^T  and  h = silu(x gate^T) * (x up^T)
  *   x   device, fp32 [m][k] row-major, m <= RZ_MXFP4_GEMV_MAX_M
  *   y, h   device out, fp32 [m][n] row-major
- * Products are exact, sums fp32: |y - exact| <= gamma_{2 (k + k/32)} sum |x w|,
- * gamma_t = t u / (1 - t u), u = 2^-24.  For m > 1 this takes |x| >= 2^-110
+ * Products are exact, sums fp32: where no partial sum overflows,
+ *   |y - exact| <= gamma_{2 (k + k/32)} sum |x w| + 2k 2^-126
+ * (h: as rz_mxfp4_gated with these errors).  For m > 1 this takes |x| >= 2^-110
  * or 0: x passes as three bf16 parts, and what lies below 2^-133 is lost.
- * Weights beyond the fp32 range (scale bytes 253 and 254, which
- * rz_mxfp4_quant never writes) count as infinite here.  m == 0 or n == 0 is
- * a no-op.
+ * A weight beyond the fp32 range (scale bytes 253 and 254, which
+ * rz_mxfp4_quant never writes, reach it) gives an infinity or a NaN in every
+ * sum it enters, which of the two may differ between m == 1 and m > 1.
+ * m == 0 or n == 0 is a no-op.
  */
 int rz_mxfp4_gemv(const uint8_t* w_codes, const uint8_t* w_scales, uint32_t n, uint32_t k, const float* x, uint32_t m,
                   float* y, void* stream);

@@ -78,7 +78,8 @@ def gemm(a: np.ndarray, w: np.ndarray):
     Products of E2M1 values are exact.  Each fp32 addition, inside the matrix
     core or outside, errs by at most 2u relative (truncation; u to nearest),
     and there are fewer than K on the way of any term, so the error is at most
-    gamma_K(2u) sum |a w|, plus the float64 sum's own gamma_K(2^-53)."""
+    gamma_K(2u) sum |a w|, plus the float64 sum's own gamma_K(2^-53).  Results
+    under 2^-126, which the matrix core may flush, are not counted."""
     k = a.shape[1]
     g = 2 * k * U / (1 - 2 * k * U) + k * 2.0 ** -53
     return a @ w.T, g * (np.abs(a) @ np.abs(w).T)
