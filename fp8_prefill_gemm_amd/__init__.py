@@ -68,6 +68,7 @@ _SIGS = {
     "rz_mxfp4_pack_weight": (_i32, [_i32, _vp, _u32, _u32, _vp, _vp, _vp]),
     "rz_mxfp4_dequant": (_i32, [_vp, _vp, _u32, _u32, _i32, _vp, _vp]),
     "rz_mxfp4_gemm": (_i32, [_vp, _vp, _u32, _vp, _vp, _u32, _u32, _vp, _vp]),
+    "rz_mxfp4_gemm_plan": (_i32, [_u32, _u32, _u32, _i32, _vp]),
     "rz_mxfp4_gated": (_i32, [_vp, _vp, _u32, _vp, _vp, _vp, _vp, _u32, _u32, _vp, _vp]),
     "rz_mxfp4_gated_quant": (_i32, [_vp, _vp, _u32, _vp, _vp, _vp, _vp, _u32, _u32, _vp, _vp, _vp]),
     "rz_mxfp4_gemv": (_i32, [_vp, _vp, _u32, _u32, _vp, _u32, _vp, _vp]),
@@ -190,6 +191,12 @@ def rz_workspace_bytes() -> int:
 def rz_fp8_gemm_plan(m: int, n: int, k: int) -> tuple[int, int, int, int]:
     out = (ctypes.c_int32 * 4)()
     _check(lib().rz_fp8_gemm_plan(m, n, k, ctypes.cast(out, ctypes.c_void_p)))
+    return tuple(out)
+
+
+def rz_mxfp4_gemm_plan(m: int, n: int, k: int, gated: bool = False) -> tuple[int, int, int, int]:
+    out = (ctypes.c_int32 * 4)()
+    _check(lib().rz_mxfp4_gemm_plan(m, n, k, gated, ctypes.cast(out, ctypes.c_void_p)))
     return tuple(out)
 
 

@@ -687,6 +687,19 @@ int rz_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, c
     return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
 }
 
+int rz_mxfp4_gemm_plan(uint32_t m, uint32_t n, uint32_t k, int gated, int32_t* cfg_out) {
+    static const char* fn = "rz_mxfp4_gemm_plan";
+    if (!cfg_out) return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if (int r = check_mx_k(fn, k)) return r;
+    if (int r = check_mx(fn, m, n, k, {})) return r;
+    const rz::MxPlan p = m == 0 || n == 0 ? rz::MxPlan{} : rz::plan_mx_gemm(m, n, k, gated != 0);
+    cfg_out[0] = (int32_t)(p.row_groups * 32u);
+    cfg_out[1] = (int32_t)(p.col_groups * 32u);
+    cfg_out[2] = (int32_t)p.ways;
+    cfg_out[3] = (int32_t)p.workgroups;
+    return RZ_OK;
+}
+
 int rz_mxfp4_gated(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const uint8_t* gate_codes,
                    const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales, uint32_t n, uint32_t k,
                    float* h, void* stream) {

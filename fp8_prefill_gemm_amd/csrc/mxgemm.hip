@@ -466,21 +466,6 @@ __global__ __launch_bounds__(64 * KS, 2) void mx_gemm_split_kernel(Args P) {
     });
 }
 
-template <int TM, int WN, int KS, bool GATED, int OUT>
-void launch_split(Args& P, uint32_t a_groups, uint32_t w_groups, hipStream_t st) {
-    constexpr uint32_t cols = GATED ? WN / 2 : WN;
-    P.tiles_m = P.group_m = (a_groups + TM - 1) / TM;
-    P.tiles_n = (w_groups + cols - 1) / cols;
-    mx_gemm_split_kernel<TM, WN, KS, GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * KS, 0, st>>>(P);
-}
-
-template <int TM, bool GATED, int OUT>
-void launch_tile(Args& P, uint32_t a_groups, hipStream_t st) {
-    P.tiles_m = (a_groups + TM - 1) / TM;
-    P.group_m = min_u32(P.tiles_m, 32u / TM);
-    mx_gemm_tile_kernel<TM, GATED, OUT><<<P.tiles_m * P.tiles_n, 64 * kNW, 0, st>>>(P);
-}
-
 // Row groups of a tile: those with the least cost, turns of the 256 CUs times
 // what a turn of that height takes.  Two 128-token tiles on a CU do the most
 // work a second; lower ones fill the CUs and waste less of a ragged batch
@@ -543,33 +528,62 @@ uint32_t tile_height(uint32_t a_groups, uint32_t tiles_n, uint32_t k) {
 // workgroups until the tile (16 x 18944 gated, 1184 blocks: 13.9, 15.3 with
 // 2x2, 12.8 the tile).  An odd number of row groups counts as the even one
 // that 2x2 blocks and tiles compute (96 x 18944: 13.1 / 10.3).
+MxPlan plan(uint32_t m, uint32_t n, uint32_t k, bool gated) {
+    const uint32_t a_groups = pad32(m) / 32u, w_groups = pad32(n) / 32u;
+    const uint64_t row = (uint64_t)w_groups * (gated ? 2 : 1), blocks = a_groups * row;
+    const uint64_t paired = a_groups == 1 ? row : ((a_groups + 1u) & ~1u) * row;
+    auto of = [&](uint32_t tm, uint32_t cols, uint32_t ways) {
+        return MxPlan{tm, cols, ways, (a_groups + tm - 1) / tm * ((w_groups + cols - 1) / cols)};
+    };
+    if (paired > (a_groups == 1 || k <= 2048u ? 1100u : 2100u)) {
+        const uint32_t cols = (gated ? kWN / 2 : kWN) * kNW;
+        return of(tile_height(a_groups, (w_groups + cols - 1) / cols, k), cols, 1);
+    }
+    if (a_groups > 1 && blocks > (gated ? 600u : 800u)) return of(2, gated ? 1 : 2, 4);
+    if (!gated && a_groups > 1 && blocks > 272u) return of(2, 1, 8);
+    return of(1, 1, 8);
+}
+
+template <int TM, int WN, int KS, bool GATED, int OUT>
+void launch_split(Args& P, const MxPlan& p, hipStream_t st) {
+    P.tiles_m = P.group_m = (pad32(P.m) / 32u + TM - 1) / TM;
+    P.tiles_n = p.workgroups / P.tiles_m;
+    mx_gemm_split_kernel<TM, WN, KS, GATED, OUT><<<p.workgroups, 64 * KS, 0, st>>>(P);
+}
+
+template <int TM, bool GATED, int OUT>
+void launch_tile(Args& P, const MxPlan& p, hipStream_t st) {
+    P.tiles_m = (pad32(P.m) / 32u + TM - 1) / TM;
+    P.tiles_n = p.workgroups / P.tiles_m;
+    P.group_m = min_u32(P.tiles_m, 32u / TM);
+    mx_gemm_tile_kernel<TM, GATED, OUT><<<p.workgroups, 64 * kNW, 0, st>>>(P);
+}
+
 template <bool GATED, int OUT>
 void launch_as(Args P, hipStream_t st) {
-    const uint32_t a_groups = pad32(P.m) / 32u, w_groups = pad32(P.n) / 32u;
-    const uint64_t row = (uint64_t)w_groups * (GATED ? 2 : 1), blocks = a_groups * row;
-    const uint64_t paired = a_groups == 1 ? row : ((a_groups + 1u) & ~1u) * row;
-    if (paired > (a_groups == 1 || P.k <= 2048u ? 1100u : 2100u)) {
-        constexpr uint32_t cols = (GATED ? kWN / 2 : kWN) * kNW;
-        P.tiles_n = (w_groups + cols - 1) / cols;
-        switch (tile_height(a_groups, P.tiles_n, P.k)) {
-            case 2: return launch_tile<2, GATED, OUT>(P, a_groups, st);
-            case 3: return launch_tile<3, GATED, OUT>(P, a_groups, st);
-            case 5: return launch_tile<5, GATED, OUT>(P, a_groups, st);
-            case 6: return launch_tile<6, GATED, OUT>(P, a_groups, st);
-            default: return launch_tile<4, GATED, OUT>(P, a_groups, st);
+    const MxPlan p = plan(P.m, P.n, P.k, GATED);
+    if (p.ways == 1) {
+        switch (p.row_groups) {
+            case 2: return launch_tile<2, GATED, OUT>(P, p, st);
+            case 3: return launch_tile<3, GATED, OUT>(P, p, st);
+            case 5: return launch_tile<5, GATED, OUT>(P, p, st);
+            case 6: return launch_tile<6, GATED, OUT>(P, p, st);
+            default: return launch_tile<4, GATED, OUT>(P, p, st);
         }
-    } else if (a_groups > 1 && blocks > (GATED ? 600u : 800u)) {
-        launch_split<2, 2, 4, GATED, OUT>(P, a_groups, w_groups, st);
+    } else if (p.ways == 4) {
+        launch_split<2, 2, 4, GATED, OUT>(P, p, st);
     } else if constexpr (GATED) {
-        launch_split<1, 2, 8, GATED, OUT>(P, a_groups, w_groups, st);
-    } else if (a_groups > 1 && blocks > 272u) {
-        launch_split<2, 1, 8, GATED, OUT>(P, a_groups, w_groups, st);
+        launch_split<1, 2, 8, GATED, OUT>(P, p, st);
+    } else if (p.row_groups == 2) {
+        launch_split<2, 1, 8, GATED, OUT>(P, p, st);
     } else {
-        launch_split<1, 1, 8, GATED, OUT>(P, a_groups, w_groups, st);
+        launch_split<1, 1, 8, GATED, OUT>(P, p, st);
     }
 }
 
 }  // namespace
+
+MxPlan plan_mx_gemm(uint32_t m, uint32_t n, uint32_t k, bool gated) { return plan(m, n, k, gated); }
 
 hipError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, uint32_t m, const MxWeights& W, bool gated,
                           uint32_t n, uint32_t k, float* y, uint8_t* h_codes, uint8_t* h_scales, hipStream_t st) {

@@ -124,6 +124,14 @@ struct MxWeights {
 };
 
 // ---- mxgemm.hip
+// The launch for a shape: 32-row groups of tokens and of weight rows (of the
+// gate and of the up weight each) a workgroup, waves that share K (1: the
+// tile kernel), workgroups.  m, n > 0.
+struct MxPlan {
+    uint32_t row_groups, col_groups, ways, workgroups;
+};
+MxPlan plan_mx_gemm(uint32_t m, uint32_t n, uint32_t k, bool gated);
+
 // y fp32 [m][n] = a w^T, or silu(a wg^T) * (a wu^T) when gated; a tiled MXFP4.
 // With h_codes (gated, n a multiple of 256) the result goes to h_codes and
 // h_scales as tiled MXFP4 instead of y.

@@ -612,6 +612,13 @@ int rz_fp8_scales(const float* absmax_dev, uint64_t count, float* q_out_dev,
  * when K is split. */
 int rz_fp8_gemm_plan(uint32_t m, uint32_t n, uint32_t k, int32_t* cfg_out);
 
+/* What rz_mxfp4_gemm (gated == 0) or rz_mxfp4_gated and rz_mxfp4_gated_quant
+ * launch for this shape: writes {tokens, weight rows, ways, workgroups} to
+ * cfg_out[4] (host): a workgroup computes that many tokens by that many rows
+ * (of each of the two weights when gated); its waves share K that many ways,
+ * 256 columns a turn (1: every wave takes all of K).  All 0 if m or n is. */
+int rz_mxfp4_gemm_plan(uint32_t m, uint32_t n, uint32_t k, int gated, int32_t* cfg_out);
+
 const char* rz_status_string(int status);
 const char* rz_last_error_string(void);
 
