@@ -298,8 +298,8 @@ def cpu_baseline(x_ffn, x_down, gate_blocks, down_blocks, gate, dn, m_rows=128):
         host_cores = len(os.sched_getaffinity(0))
     except AttributeError:
         host_cores = os.cpu_count() or 1
-    # the GPU machine's CPU share is 16 threads per GPU whatever the affinity
-    # mask shows; BLAS gets all of that share
+    # one GPU's share of the CPUs is 16 threads whatever the affinity mask
+    # shows; BLAS gets all of that share
     threads = max(1, min(host_cores, 16))
     try:
         from threadpoolctl import threadpool_limits
@@ -841,9 +841,11 @@ def q8_gemm(args, dev) -> int:
 def mxfp4(args, dev) -> int:
     """The MXFP4 path on configuration 3's FFN (M=2048; gate and up 18944 x
     3584, down 3584 x 18944) beside the FP8 path (one line): warm times, HIP
-    events around 50 launches after 10 warm-up launches, and the accuracy of
-    both paths' gate GEMM on 64 rows against a float64 product of the fp32
-    activation and the fp32 dequantised weight."""
+    events around 50 launches after --clock-settle seconds of the same ones
+    (the first 60 of the gated product after an idle second take 160 us, later
+    ones 130 to 136), and the accuracy of both paths' gate GEMM on 64 rows
+    against a float64 product of the fp32 activation and the fp32 dequantised
+    weight."""
     import torch
 
     import fp8_prefill_gemm_amd as rz
@@ -852,8 +854,11 @@ def mxfp4(args, dev) -> int:
     stream = torch.cuda.current_stream(dev)
 
     def timed(fn, reps=TIMED_LAUNCHES):
-        for _ in range(WARM_LAUNCHES):
-            fn()
+        t0 = time.monotonic()
+        while time.monotonic() - t0 < args.clock_settle:
+            for _ in range(WARM_LAUNCHES):
+                fn()
+            torch.cuda.synchronize()
         e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         e0.record(stream)
         for _ in range(reps):

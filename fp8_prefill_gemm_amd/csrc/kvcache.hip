@@ -9,10 +9,10 @@
 //          [slot][head][dim/2], scale bytes [slot][head][dim/32].
 // Both directions are bound by memory (a decoding step by its launch).  A
 // lane holds eight values, 8..64 lanes a row; keys and values share a launch
-// (grid y).  Measured, 4 heads of 128: writing 131072 tokens 145 us (E4M3, 4.7
-// TB/s), 64 tokens 3.1 us; reading 131072 tokens back in bf16 81 us (E4M3, 5.0
-// TB/s) and 72 us (MXFP4, 4.7 TB/s), 4096 tokens 4.9 us.  With one row a lane
-// in flight E4M3 took 88 us.
+// (grid y).  Measured, 4 heads of 128: writing 131072 tokens 134 us (E4M3) and
+// 121 us (MXFP4), both 5.0 TB/s, 64 tokens 3 us; reading 131072 tokens back in
+// bf16 82 us (E4M3, 5.0 TB/s) and 67 us (MXFP4, 5.1 TB/s), in fp32 171 and 161
+// us (3.9 TB/s), 4096 tokens 5 us.  With one row a lane in flight E4M3 took 88.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -206,11 +206,12 @@ __device__ __forceinline__ void quantise_lanes(const Args& P, const float (&v)[1
 // share a CU: while one stores its tile or waits, the other computes.
 //
 // Measured (random codes, M = 2048): gated N=18944 K=3584 133 us, 4.2
-// PFLOP/s, of it 11 us that a copy without the store does not take; down
-// N=3584 K=18944 65 us, 4.3 PFLOP/s.  What bounds it is the power limit: with
-// every code 1.0 the same launches run at 5.5 and 5.7 PFLOP/s (2.4 GHz instead
-// of 1.7 to 2.0), and the MFMA alone, on random register operands, reaches
-// 6.6 (9.4 on constant ones).  Left to the compiler's own order, which moves
+// PFLOP/s, of it 11 us that a copy without the store does not take, with MXFP4
+// output 128; down N=3584 K=18944 64 us, 4.3 PFLOP/s.  What bounds it is the
+// power limit: the socket draws its cap of 1400 W at 1.52 GHz (down 1.68), and
+// with every code 1.0 the gated launches run at 6.0 and 6.6 PFLOP/s, at 2.35
+// GHz.  The MFMA alone, on random register operands, reaches 6.6 (9.4 on
+// constant ones).  Left to the compiler's own order, which moves
 // the loads next to their use, 156 and 82 us.  A 256 x 256 tile of eight
 // waves reads a third less through the L2 but has one workgroup a CU: 138
 // and 85 us; one of four waves of 128 x 128, with half the LDS reads, takes 91
@@ -469,10 +470,10 @@ __global__ __launch_bounds__(64 * KS, 2) void mx_gemm_split_kernel(Args P) {
 // Row groups of a tile: those with the least cost, turns of the 256 CUs times
 // what a turn of that height takes.  Two 128-token tiles on a CU do the most
 // work a second; lower ones fill the CUs and waste less of a ragged batch
-// where there are few, higher ones (one workgroup a CU, 330 to 430 registers)
-// save a second turn that would be mostly idle, where a long K outweighs their
-// slower start and end.  Measured (us, by tokens a tile, the one taken
-// in brackets; the others with the same choice of everything else):
+// where there are few, higher ones (one workgroup a CU, 278 and 316 registers,
+// 330 to 426 gated) save a second turn that would be mostly idle, where a long
+// K outweighs their slower start and end.  Measured (us, by tokens a tile, the
+// one taken in brackets; the others with the same choice of everything else):
 //                                 64     96    128    160    192
 //   640 x 3584 x 3584          [10.0]          11.9
 //   gated 160 x 18944 x 3584   [18.9]   24.7   28.7   18.1   19.3
@@ -484,6 +485,11 @@ __global__ __launch_bounds__(64 * KS, 2) void mx_gemm_split_kernel(Args P) {
 //   1500 x 3584 x 18944               [52.8]   57.7   63.3   64.7
 //   2048 x 3584 x 18944         78            [65]            72
 //   2048 x 18944 x 3584         90            [76]            89
+//   gated 160 x 18944 x 4608    29.1   33.0   35.3  [24.4]   25.2
+//   gated 384 x 14336 x 4608    32.1   27.4   30.9   39.7  [27.1]
+//   gated 1024 x 4608 x 8192    49.4   44.1   47.3  [39.7]   42.0
+//   gated 1536 x 3584 x 8192    55.0   45.2   49.5   61.9  [43.2]
+// (the MXFP4 output's within 3% of these).
 // A 96-token tile alone on a CU is not surely faster than a 128-token one
 // unless the batch is ragged or K long (1500 x 3584 with K = 2048: 11.9 and
 // 10.7).  Tiles of 224 and 256 tokens: 94 and 90 for 2048 x 4608 x 18944, 110

@@ -11,10 +11,11 @@
 // are 256-byte runs of eight rows, each wave writes 128-byte runs of codes,
 // and the four 64-column slabs of a lane are in flight together.
 //
-// Measured: quantising 2048 x 18944 31.4 us (5.6 TB/s), reading it back in
-// bf16 16.0 us (6.1 TB/s), packing 18944 x 3584 from Q4_K 22.0 us in a trace,
-// 18.5 back to back (4.0 TB/s; 19.9 with neighbouring tiles on different
-// XCDs, whose caches then fetch the 144-byte blocks' shared lines twice).
+// Measured: quantising 2048 x 18944 31.0 us (5.7 TB/s), reading it back in
+// bf16 and fp16 15.5 us (6.4 TB/s), in fp32 28.6 us; packing 18944 x 3584 from
+// Q4_K 19.5 us in a trace, 18.5 back to back (4.0 TB/s; 19.9 with neighbouring
+// tiles on different XCDs, whose caches then fetch the 144-byte blocks' shared
+// lines twice), 3584 x 18944 from Q6_K 23.5 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
