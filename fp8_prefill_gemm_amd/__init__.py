@@ -513,11 +513,18 @@ def _dtype_id(dtype):
     return _DTYPES[dtype]
 
 
+def _out_dtype(*outs):
+    """The first output's dtype, or float32 (what is no tensor is refused with its name later)."""
+    for o in outs:
+        if o is not None:
+            return getattr(o, "dtype", _torch().float32)
+    return _torch().float32
+
+
 def rz_mxfp4_dequant(codes, scales, rows: int, out=None, dtype=None, stream=None):
     """MXFP4 -> out [rows][k] of dtype (default: out's, or float32)."""
-    if dtype is None:
-        dtype = _torch().float32 if out is None else out.dtype
-    return _native().mxfp4_dequant(codes, scales, rows, out, _dtype_id(dtype), _handle(stream))
+    did = _dtype_id(_out_dtype(out) if dtype is None else dtype)
+    return _native().mxfp4_dequant(codes, scales, rows, out, did, _handle(stream))
 
 
 def rz_mxfp4_gemm(a_codes, a_scales, m: int, w_codes, w_scales, n: int, y=None, stream=None):
@@ -570,9 +577,7 @@ def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: i
     page_table int32 [seqs][max_pages]; offsets int32 [seqs + 1]: sequence b
     is rows offsets[b] .. offsets[b+1] - 1.  Rows of no sequence are left as
     they are (undefined in a new output)."""
-    if dtype is None:
-        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else _torch().float32
-    did = _dtype_id(dtype)
+    did = _dtype_id(_out_dtype(k_out, v_out) if dtype is None else dtype)
     return _native().kv_cache_read(fmt, k_codes, k_scales, v_codes, v_scales, page_len, page_table, offsets, rows, k_out, v_out, did,
                                    _handle(stream))
 

@@ -494,9 +494,9 @@ __global__ __launch_bounds__(64 * KS, 2) void mx_gemm_split_kernel(Args P) {
 // unless the batch is ragged or K long: its time depends on where the operands
 // lie, by a cause that was not found (1280 x 3584 with K = 2048: 9.8 in one
 // process and 11.5 in the next, 128 tokens 10.0 to 10.4 in both; 1500 x 3584
-// 10.4 and 11.2, 128 tokens 10.9 to 11.1).  Tiles of 224 and 256 tokens: 94 and 90 for 2048 x 4608 x 18944, 110
-// and 128 (of 118 and 127) for 3500 x 3584 and 3400 x 4608, and the gated ones
-// spill registers.
+// 10.4 and 11.2, 128 tokens 10.9 to 11.1).  Tiles of 224 and 256 tokens: 94
+// and 90 for 2048 x 4608 x 18944, 110 and 128 (of 118 and 127) for 3500 x 3584
+// and 3400 x 4608, and the gated ones spill registers.
 uint32_t tile_height(uint32_t a_groups, uint32_t tiles_n, uint32_t k) {
     auto tiles = [&](uint32_t tm) { return (a_groups + tm - 1) / tm * tiles_n; };
     auto cost = [&](uint32_t tm, uint32_t turn) { return (tiles(tm) + 255u) / 256u * turn; };

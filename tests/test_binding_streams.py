@@ -47,3 +47,16 @@ def test_wants_tensors(on_a_stream):
         rz.rz_mxfp4_quant([1.0])
     with pytest.raises(TypeError, match="w: expected a tensor, got NoneType"):
         rz.rz_mxfp4_gemv(None, None, 70, torch.zeros(2, 512))
+
+
+def test_outputs_that_are_no_tensors(on_a_stream):
+    """The element type is taken from the outputs only where they are tensors."""
+    codes, scales = torch.zeros(2, 8, 1024, dtype=torch.uint8), torch.zeros(2, 2, 256, dtype=torch.uint8)
+    cache = [torch.zeros(10, 2, 64, dtype=torch.uint8), torch.zeros(10, 2)] * 2
+    table, offsets = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    for bad in ([1.0], 7):
+        for call in (lambda: rz.rz_mxfp4_dequant(codes, scales, 37, out=bad),
+                     lambda: rz.rz_kv_cache_read(0, *cache, 16, table, offsets, 5, k_out=bad),
+                     lambda: rz.rz_kv_cache_read(0, *cache, 16, table, offsets, 5, v_out=bad)):
+            with pytest.raises((TypeError, ValueError), match="expected a tensor|works on device"):
+                call()
