@@ -76,6 +76,14 @@ _SIGS = {
     "rz_kv_cache_write": (_i32, [_i32, _vp, _vp, _u32, _u32, _u32, _u64, _u64, _vp, _u64, _vp, _vp, _vp, _vp, _vp]),
     "rz_kv_cache_read": (_i32, [_i32, _vp, _vp, _vp, _vp, _u64, _u32, _u32, _u32, _vp, _u32, _u32, _vp, _u32, _i32,
                                 _vp, _vp, _vp]),
+    "rz_kv_plan_workspace_bytes": (ctypes.c_size_t, [_u32, _u32]),
+    "rz_kv_plan": (_i32, [_vp, _vp, _vp, _u32, _u32, _u32, _vp, _u32, _vp, _u32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "rz_kv_attention_workspace_bytes": (ctypes.c_size_t, [_u32, _u32, _u32, _u32]),
+    "rz_kv_attention": (_i32, [_i32, _vp, _u32, _u64, _vp, _vp, _vp, _vp, _u64, _u32, _u32, _u32, _vp, _u32, _u32, _vp, _vp,
+                               _u32, _f32, _i32, _vp, _vp, _vp, _vp]),
+    "rz_kv_bounds": (_i32, [_i32, _vp, _vp, _u64, _u32, _u32, _u32, _vp, _u32, _vp, _vp, _vp]),
+    "rz_kv_select_workspace_bytes": (ctypes.c_size_t, [_u32, _u32, _u32]),
+    "rz_kv_select": (_i32, [_vp, _u32, _u64, _vp, _vp, _u32, _u32, _u32, _u32, _vp, _u32, _u32, _vp, _u32, _vp, _vp, _vp]),
     "rz_status_string": (ctypes.c_char_p, [_i32]),
     "rz_last_error_string": (ctypes.c_char_p, []),
     "rz_version": (ctypes.c_char_p, []),
@@ -580,6 +588,53 @@ def rz_kv_cache_read(fmt: int, k_codes, k_scales, v_codes, v_scales, page_len: i
     did = _dtype_id(_out_dtype(k_out, v_out) if dtype is None else dtype)
     return _native().kv_cache_read(fmt, k_codes, k_scales, v_codes, v_scales, page_len, page_table, offsets, rows, k_out, v_out, did,
                                    _handle(stream))
+
+
+def rz_kv_plan(lens, offsets, tokens: int, page_len: int, page_table, free_pages, free_count, keep=None, lens_out=None,
+               count_out=None, slots=None, stream=None):
+    """A step's pages and slots -> (slots, lens_out, count_out).  Sequence b
+    keeps keep[b] of its lens[b] tokens (default: all) and adds offsets[b+1] -
+    offsets[b]; pages no longer needed go onto the stack free_pages[0 ..
+    free_count[0]), lacking ones come from its top.  int32 lens, keep [seqs],
+    offsets [seqs + 1], page_table [seqs][max_pages] and free_pages [pages]
+    (both updated), free_count [1]; slots int64 [tokens] for
+    rz_kv_cache_write, -1 where a sequence was refused (too few pages free,
+    or too many for its row): its lens_out is its lens then.  lens_out may be
+    lens, count_out free_count."""
+    return _native().kv_plan(lens, keep, offsets, tokens, page_len, page_table, free_pages, free_count, lens_out, count_out, slots,
+                             _handle(stream))
+
+
+def rz_kv_attention(fmt: int, q, k_codes, k_scales, v_codes, v_scales, page_len: int, page_table, lens, scale: float, pages=None,
+                    out=None, dtype=None, lse=None, stream=None):
+    """Attention of one new token a sequence over the paged cache -> out
+    [seqs][q_heads][dim] of dtype (default: out's, or float32): the values of
+    the positions below lens[b] (int32 [seqs]) weighted by softmax(scale *
+    q . k).  q fp32 [seqs][q_heads][dim] (sequences may be strided), query
+    head h reads key head h // (q_heads // heads).  pages int32
+    [seqs][heads][budget]: only positions in these columns of page_table count
+    (-1: none), as rz_kv_select gives them.  lse fp32 [seqs][q_heads], if
+    passed, gets log sum exp of the scores.  A row without a position gives
+    zeros and -inf."""
+    did = _dtype_id(_out_dtype(out) if dtype is None else dtype)
+    return _native().kv_attention(fmt, q, k_codes, k_scales, v_codes, v_scales, page_len, page_table, lens, scale, pages, out, did,
+                                  lse, _handle(stream))
+
+
+def rz_kv_bounds(fmt: int, k_codes, k_scales, slots, page_len: int, bounds, bound_scales, stream=None):
+    """Bounds of the keys in the pages that `slots` names (int64 [tokens], as
+    just written; tokens of a page together and ascending), a page counting up
+    to its last named slot: bounds int8 [slots // page_len][heads][2][dim]
+    (largest, smallest) times bound_scales fp32 [slots // page_len][heads],
+    both updated."""
+    _native().kv_bounds(fmt, k_codes, k_scales, slots, page_len, bounds, bound_scales, _handle(stream))
+
+
+def rz_kv_select(q, bounds, bound_scales, page_len: int, page_table, lens, budget: int, pages=None, stream=None):
+    """The `budget` pages of each sequence and key head that may hold the
+    largest q . k by their bounds, the first and the last among them -> pages
+    int32 [seqs][heads][budget]: columns of page_table, ascending, then -1."""
+    return _native().kv_select(q, bounds, bound_scales, page_len, page_table, lens, budget, pages, _handle(stream))
 
 
 def rz_dequant_f32(qtype: int, blocks, n: int, k: int, out=None, stream=None):

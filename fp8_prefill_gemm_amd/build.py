@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "librz_fp8.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "kquant.hip", "actquant.hip", "gemm.hip", "gemm_edge.hip", "kgemv.hip", "kqgemm.hip",
-           "q8gemm.hip", "mxquant.hip", "mxgemm.hip", "mxgemv.hip", "kvcache.hip"]
+           "q8gemm.hip", "mxquant.hip", "mxgemm.hip", "mxgemv.hip", "kvcache.hip",
+           "kvplan.hip", "kvattn.hip", "kvselect.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -120,6 +120,20 @@ int check_kv(const char* fn, int format, uint32_t heads, uint32_t dim, uint64_t 
     return RZ_OK;
 }
 
+// The queries of a serving call: one row of q_heads*dim a sequence.
+int check_kv_query(const char* fn, uint32_t q_heads, uint32_t heads, uint32_t dim, uint32_t page_len, uint32_t seqs,
+                   uint64_t q_stride) {
+    if (page_len == 0) return fail(RZ_ERR_SHAPE, "%s: page_len must be positive", fn);
+    if (q_heads == 0 || q_heads % heads != 0)
+        return fail(RZ_ERR_SHAPE, "%s: q_heads=%u must be a positive multiple of heads=%u", fn, q_heads, heads);
+    const uint64_t row = (uint64_t)q_heads * dim;
+    if (row > (1u << 26) || seqs * row > RZ_KV_MAX_CALL || q_stride > RZ_MAX_ELEMS)
+        return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    if (seqs > 1 && (q_stride < row || q_stride % 4u != 0))
+        return fail(RZ_ERR_SHAPE, "%s: q_stride must be a multiple of 4, at least q_heads*dim", fn);
+    return RZ_OK;
+}
+
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 }  // namespace
@@ -799,6 +813,105 @@ int rz_kv_cache_read(int format, const uint8_t* k_codes, const void* k_scales, c
     const rz::KvRead A = {{k_codes, v_codes}, {k_scales, v_scales}, {k_out, v_out}, page_table, offsets, num_slots,
                           heads,              dim,                  page_len,       seqs,       max_pages, rows};
     hipError_t e = rz::launch_kv_read(format, A, dtype, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+size_t rz_kv_plan_workspace_bytes(uint32_t seqs, uint32_t tokens) { return rz::kv_plan_ws_bytes(seqs, tokens); }
+
+int rz_kv_plan(const int32_t* lens, const int32_t* keep, const int32_t* offsets, uint32_t seqs, uint32_t tokens,
+               uint32_t page_len, int32_t* page_table, uint32_t max_pages, int32_t* free_pages, uint32_t num_pages,
+               const int32_t* free_count, int32_t* lens_out, int32_t* count_out, int64_t* slots, void* ws, void* stream) {
+    static const char* fn = "rz_kv_plan";
+    if (page_len == 0) return fail(RZ_ERR_SHAPE, "%s: page_len must be positive", fn);
+    if (seqs > 0x7FFFFFFEu || tokens > 0x7FFFFFFFu || num_pages > 0x7FFFFFFFu || (uint64_t)seqs * max_pages > RZ_MAX_ELEMS)
+        return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    if (!free_count || !count_out || (num_pages != 0 && !free_pages) || (tokens != 0 && !slots) ||
+        (seqs != 0 && (!lens || !offsets || !lens_out || (max_pages != 0 && !page_table))) ||
+        (rz::kv_plan_ws_bytes(seqs, tokens) != 0 && !ws))
+        return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if ((((uintptr_t)lens | (uintptr_t)keep | (uintptr_t)offsets | (uintptr_t)page_table | (uintptr_t)free_pages |
+          (uintptr_t)free_count | (uintptr_t)lens_out | (uintptr_t)count_out) & 3u) || ((uintptr_t)slots & 7u) || !aligned16(ws))
+        return fail(RZ_ERR_ALIGN, "%s: tables must be 4-byte aligned (slots: 8, ws: 16)", fn);
+    if (int r = check_device(fn)) return r;
+    const rz::KvPlan A = {lens,  keep, offsets, free_count, page_table, free_pages, lens_out, count_out,
+                          slots, ws,   seqs,    tokens,     page_len,   max_pages,  num_pages};
+    hipError_t e = rz::launch_kv_plan(A, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+size_t rz_kv_attention_workspace_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint32_t dim) {
+    if (seqs == 0 || heads == 0 || q_heads == 0 || q_heads % heads != 0 || dim == 0 || dim > RZ_KV_MAX_DIM) return 0;
+    return rz::kv_attend_ws_bytes(q_heads, heads, dim, device_cus());
+}
+
+int rz_kv_attention(int format, const float* q, uint32_t q_heads, uint64_t q_stride, const uint8_t* k_codes,
+                    const void* k_scales, const uint8_t* v_codes, const void* v_scales, uint64_t num_slots,
+                    uint32_t heads, uint32_t dim, uint32_t page_len, const int32_t* page_table, uint32_t seqs,
+                    uint32_t max_pages, const int32_t* lens, const int32_t* pages, uint32_t budget, float scale,
+                    int dtype, void* out, float* lse, void* ws, void* stream) {
+    static const char* fn = "rz_kv_attention";
+    if (int r = check_kv(fn, format, heads, dim, num_slots)) return r;
+    if (int r = check_kv_query(fn, q_heads, heads, dim, page_len, seqs, q_stride)) return r;
+    if (dtype != RZ_F32 && dtype != RZ_F16 && dtype != RZ_BF16) return fail(RZ_ERR_VALUE, "%s: unknown dtype %d", fn, dtype);
+    if (scale - scale != 0.0f) return fail(RZ_ERR_VALUE, "%s: scale must be finite", fn);
+    if (pages && (uint64_t)budget * page_len > 0x7FFFFFFFu) return fail(RZ_ERR_SHAPE, "%s: budget*page_len exceeds 2^31 - 1", fn);
+    if (seqs == 0) return RZ_OK;  // nothing to read or write
+    if (!q || (num_slots != 0 && (!k_codes || !k_scales || !v_codes || !v_scales)) || (max_pages != 0 && !page_table) || !lens || !out)
+        return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) || !aligned16(v_scales) ||
+        !aligned16(out) || !aligned16(ws) || (((uintptr_t)page_table | (uintptr_t)lens | (uintptr_t)pages | (uintptr_t)lse) & 3u))
+        return fail(RZ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned (tables and lse: 4)", fn);
+    if (int r = check_device(fn)) return r;
+    const rz::KvAttend A = {q,   {k_codes, v_codes}, {k_scales, v_scales}, page_table, lens,    pages, out, lse,
+                            ws,  q_stride,           num_slots,            scale,      q_heads, heads, dim, page_len,
+                            seqs, max_pages,         budget};
+    hipError_t e = rz::launch_kv_attend(format, A, dtype, device_cus(), as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+int rz_kv_bounds(int format, const uint8_t* k_codes, const void* k_scales, uint64_t num_slots, uint32_t heads,
+                 uint32_t dim, uint32_t page_len, const int64_t* slots, uint32_t tokens, int8_t* bounds,
+                 float* bound_scales, void* stream) {
+    static const char* fn = "rz_kv_bounds";
+    if (int r = check_kv(fn, format, heads, dim, num_slots)) return r;
+    if (page_len == 0) return fail(RZ_ERR_SHAPE, "%s: page_len must be positive", fn);
+    if (tokens == 0 || num_slots < page_len) return RZ_OK;  // no token, or no page
+    if (!k_codes || !k_scales || !slots || !bounds || !bound_scales) return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if ((uint64_t)tokens * heads * dim > RZ_KV_MAX_CALL) return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    if (!aligned16(k_codes) || !aligned16(k_scales) || !aligned16(bounds) || !aligned16(bound_scales) || ((uintptr_t)slots & 7u))
+        return fail(RZ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned (slots: 8)", fn);
+    if (int r = check_device(fn)) return r;
+    const rz::KvBounds A = {k_codes, k_scales, slots, bounds, bound_scales, num_slots, num_slots / page_len, tokens, heads, dim, page_len};
+    hipError_t e = rz::launch_kv_bounds(format, A, as_stream(stream));
+    return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
+}
+
+size_t rz_kv_select_workspace_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages) {
+    return rz::kv_select_ws_bytes(seqs, heads, max_pages);
+}
+
+int rz_kv_select(const float* q, uint32_t q_heads, uint64_t q_stride, const int8_t* bounds, const float* bound_scales,
+                 uint32_t num_pages, uint32_t heads, uint32_t dim, uint32_t page_len, const int32_t* page_table,
+                 uint32_t seqs, uint32_t max_pages, const int32_t* lens, uint32_t budget, int32_t* pages, void* ws,
+                 void* stream) {
+    static const char* fn = "rz_kv_select";
+    if (int r = check_kv(fn, RZ_KV_E4M3, heads, dim, num_pages)) return r;
+    if (int r = check_kv_query(fn, q_heads, heads, dim, page_len, seqs, q_stride)) return r;
+    if (budget == 0) return fail(RZ_ERR_SHAPE, "%s: budget must be positive", fn);
+    if (seqs == 0) return RZ_OK;  // nothing to read or write
+    if ((uint64_t)seqs * heads * max_pages > RZ_KV_MAX_SCORES || (uint64_t)seqs * heads * budget > RZ_MAX_ELEMS ||
+        (uint64_t)seqs * heads > RZ_KV_MAX_SCORES / 64u)
+        return fail(RZ_ERR_SHAPE, "%s: operand too large", fn);
+    if (!q || (num_pages != 0 && (!bounds || !bound_scales)) || (max_pages != 0 && !page_table) || !lens || !pages ||
+        (rz::kv_select_ws_bytes(seqs, heads, max_pages) != 0 && !ws))
+        return fail(RZ_ERR_NULL, "%s: null pointer", fn);
+    if (!aligned16(q) || !aligned16(bounds) || !aligned16(bound_scales) || !aligned16(ws) ||
+        (((uintptr_t)page_table | (uintptr_t)lens | (uintptr_t)pages) & 3u))
+        return fail(RZ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned (tables: 4)", fn);
+    if (int r = check_device(fn)) return r;
+    const rz::KvSelect A = {q,       bounds, bound_scales, page_table, lens,     pages, ws,        q_stride,
+                            q_heads, heads,  dim,          num_pages,  page_len, seqs,  max_pages, budget};
+    hipError_t e = rz::launch_kv_select(A, as_stream(stream));
     return e == hipSuccess ? RZ_OK : hip_fail(e, fn);
 }
 

@@ -87,6 +87,12 @@ struct Args {
         in_range(v, what, lo, hi);
         return v;
     }
+    // a floating-point number, as the library takes it
+    float real(Py_ssize_t i) const {
+        const double v = PyFloat_AsDouble(a[i]);
+        if (v == -1.0 && PyErr_Occurred()) throw python_error();
+        return (float)v;
+    }
 };
 
 void need(const Tensor& t, const char* what, at::ScalarType dtype, c10::IntArrayRef shape) {
@@ -322,27 +328,33 @@ PyObject* mxfp4_gated_gemv(const Args& A) {
     return wrap(h);
 }
 
-// A cache: format argument i, then k_codes, k_scales, v_codes, v_scales from argument j on.
-struct Cache {
+// One tensor pair of a cache (its keys): format argument i, codes and scales from argument j on.
+struct KeyRows {
     int64_t fmt, slots, heads, dim;
-    const Tensor &kc, &ks, &vc, &vs;
-    Cache(const Args& A, Py_ssize_t i, Py_ssize_t j)
-        : fmt(A.number(i, "fmt", 0, 1)), kc(A.tensor(j, "k_codes")), ks(A.tensor(j + 1, "k_scales")),
-          vc(A.tensor(j + 2, "v_codes")), vs(A.tensor(j + 3, "v_scales")) {
+    const Tensor &kc, &ks;
+    KeyRows(const Args& A, Py_ssize_t i, Py_ssize_t j)
+        : fmt(A.number(i, "fmt", 0, 1)), kc(A.tensor(j, "k_codes")), ks(A.tensor(j + 1, "k_scales")) {
         if (kc.dim() != 3) refuse("k_codes: expected 3 dimensions, got " + shape_text(kc.sizes()));
         slots = kc.size(0);
         heads = size_of(kc, 1, "heads");
-        const int64_t width = kc.size(2);
         dim = size_of(kc, 2, "dim", fmt == RZ_KV_E4M3 ? 1 : 2);
-        need(kc, "k_codes", at::kByte, Shape{slots, heads, width});
-        need(vc, "v_codes", at::kByte, Shape{slots, heads, width});
-        for (const Tensor* s : {&ks, &vs}) {
-            const char* what = s == &ks ? "k_scales" : "v_scales";
-            if (fmt == RZ_KV_E4M3)
-                need(*s, what, at::kFloat, Shape{slots, heads});
-            else
-                need(*s, what, at::kByte, Shape{slots, heads, width / 16});
-        }
+        need(kc, "k_codes", at::kByte, kc.sizes());
+    }
+    void scales_of(const Tensor& s, const char* what) const {
+        if (fmt == RZ_KV_E4M3)
+            need(s, what, at::kFloat, Shape{slots, heads});
+        else
+            need(s, what, at::kByte, Shape{slots, heads, kc.size(2) / 16});
+    }
+};
+
+// A whole cache: k_codes, k_scales, v_codes, v_scales from argument j on.
+struct Cache : KeyRows {
+    const Tensor &vc, &vs;
+    Cache(const Args& A, Py_ssize_t i, Py_ssize_t j) : KeyRows(A, i, j), vc(A.tensor(j + 2, "v_codes")), vs(A.tensor(j + 3, "v_scales")) {
+        need(vc, "v_codes", at::kByte, Shape{slots, heads, kc.size(2)});
+        scales_of(ks, "k_scales");
+        scales_of(vs, "v_scales");
     }
 };
 
@@ -395,6 +407,155 @@ PyObject* kv_cache_read(const Args& A) {
     return wrap2(k, v);
 }
 
+// A new workspace of the call's stream (null where it is empty).
+Tensor workspace(size_t bytes, const OnStream& on) {
+    if (bytes == 0) return Tensor();
+    return at::empty({(int64_t)bytes}, on.dev.first.options().dtype(at::kByte).layout(at::kStrided).requires_grad(false));
+}
+void* at_or_null(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// (lens, keep, offsets, tokens, page_len, page_table, free_pages, free_count, lens_out, count_out, slots, stream)
+PyObject* kv_plan(const Args& A) {
+    const Tensor &lens = A.tensor(0, "lens"), &offsets = A.tensor(2, "offsets"), &table = A.tensor(5, "page_table"),
+                 &free = A.tensor(6, "free_pages"), &count = A.tensor(7, "free_count");
+    const int64_t tokens = A.number(3, "tokens"), page_len = A.number(4, "page_len", 1);
+    if (table.dim() != 2) refuse("page_table: expected 2 dimensions, got " + shape_text(table.sizes()));
+    const int64_t seqs = size_of(table, 0, "sequences"), max_pages = size_of(table, 1, "pages");
+    if (free.dim() != 1) refuse("free_pages: expected 1 dimension, got " + shape_text(free.sizes()));
+    const int64_t pages = size_of(free, 0, "num_pages");
+    need(lens, "lens", at::kInt, Shape{seqs});
+    need(offsets, "offsets", at::kInt, Shape{seqs + 1});
+    need(table, "page_table", at::kInt, Shape{seqs, max_pages});
+    need(free, "free_pages", at::kInt, Shape{pages});
+    need(count, "free_count", at::kInt, Shape{1});
+    const Tensor& keep = A.none(1) ? lens : A.tensor(1, "keep");  // all of them by default
+    need(keep, "keep", at::kInt, Shape{seqs});
+    const Device dev(lens);
+    dev.same({&keep, &offsets, &table, &free, &count});
+    const OnStream on(A, 11, dev);
+    const Tensor then = output(A, 8, "lens_out", at::kInt, Shape{seqs}, on), left = output(A, 9, "count_out", at::kInt, Shape{1}, on),
+                 slots = output(A, 10, "slots", at::kLong, Shape{tokens}, on);
+    const Tensor ws = workspace(rz_kv_plan_workspace_bytes(seqs, tokens), on);
+    call(on, [&](void* st) {
+        return rz_kv_plan(ptr<int32_t>(lens), ptr<int32_t>(keep), ptr<int32_t>(offsets), seqs, tokens, page_len, ptr<int32_t>(table), max_pages,
+                          ptr<int32_t>(free), pages, ptr<int32_t>(count), ptr<int32_t>(then), ptr<int32_t>(left),
+                          ptr<int64_t>(slots), at_or_null(ws), st);
+    });
+    PyObject *x = wrap(slots), *y = wrap(then), *z = wrap(left);
+    PyObject* r = x && y && z ? PyTuple_Pack(3, x, y, z) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_XDECREF(z);
+    return r;
+}
+
+// The queries, page table and lengths of a serving call.
+struct Queries {
+    const Tensor &q, &table, &lens;
+    int64_t seqs, q_heads, max_pages, stride;
+    Queries(const Args& A, Py_ssize_t iq, Py_ssize_t it, Py_ssize_t il, int64_t dim)
+        : q(A.tensor(iq, "q")), table(A.tensor(it, "page_table")), lens(A.tensor(il, "lens")) {
+        if (table.dim() != 2) refuse("page_table: expected 2 dimensions, got " + shape_text(table.sizes()));
+        seqs = size_of(table, 0, "sequences");
+        max_pages = size_of(table, 1, "pages");
+        q_heads = q.dim() == 3 ? size_of(q, 1, "q_heads") : 0;
+        stride = token_stride(q, "q", seqs, q_heads, dim);
+        need(table, "page_table", at::kInt, Shape{seqs, max_pages});
+        need(lens, "lens", at::kInt, Shape{seqs});
+    }
+};
+
+// (fmt, q, k_codes, k_scales, v_codes, v_scales, page_len, page_table, lens, scale, pages, out, dtype id, lse, stream)
+PyObject* kv_attention(const Args& A) {
+    const Cache c(A, 0, 2);
+    const int64_t page_len = A.number(6, "page_len", 1), id = A.number(12, "dtype", 0, 2);
+    const Queries s(A, 1, 7, 8, c.dim);
+    const float scale = A.real(9);
+    const Tensor* chosen = nullptr;
+    int64_t budget = 0;
+    if (!A.none(10)) {
+        chosen = &A.tensor(10, "pages");
+        if (chosen->dim() != 3) refuse("pages: expected 3 dimensions, got " + shape_text(chosen->sizes()));
+        budget = size_of(*chosen, 2, "budget");
+        need(*chosen, "pages", at::kInt, Shape{s.seqs, c.heads, budget});
+    }
+    const Tensor* lse = nullptr;
+    if (!A.none(13)) {
+        lse = &A.tensor(13, "lse");
+        need(*lse, "lse", at::kFloat, Shape{s.seqs, s.q_heads});
+    }
+    const Device dev(s.q);
+    dev.same({&c.kc, &c.ks, &c.vc, &c.vs, &s.table, &s.lens});
+    if (chosen) dev.same({chosen});
+    if (lse) dev.same({lse});
+    // an empty choice has no memory, which the library would take for no choice
+    const int32_t* pages = !chosen ? nullptr : budget ? ptr<int32_t>(*chosen) : ptr<int32_t>(s.lens);
+    const OnStream on(A, 14, dev);
+    const Tensor out = output(A, 11, "out", dtype_of(id), Shape{s.seqs, s.q_heads, c.dim}, on);
+    const Tensor ws = workspace(rz_kv_attention_workspace_bytes(s.seqs, s.q_heads, c.heads, c.dim), on);
+    call(on, [&](void* st) {
+        return rz_kv_attention((int)c.fmt, ptr<float>(s.q), s.q_heads, s.stride, ptr(c.kc), ptr<void>(c.ks), ptr(c.vc),
+                               ptr<void>(c.vs), c.slots, c.heads, c.dim, page_len, ptr<int32_t>(s.table), s.seqs, s.max_pages,
+                               ptr<int32_t>(s.lens), pages, budget, scale, (int)id, ptr<void>(out), lse ? ptr<float>(*lse) : nullptr,
+                               at_or_null(ws), st);
+    });
+    return wrap(out);
+}
+
+// int8 [num_pages][heads][2][dim] and fp32 [num_pages][heads]
+struct PageBounds {
+    const Tensor &codes, &scales;
+    int64_t pages, heads, dim;
+    PageBounds(const Args& A, Py_ssize_t i) : codes(A.tensor(i, "bounds")), scales(A.tensor(i + 1, "bound_scales")) {
+        if (codes.dim() != 4) refuse("bounds: expected 4 dimensions, got " + shape_text(codes.sizes()));
+        pages = size_of(codes, 0, "num_pages");
+        heads = size_of(codes, 1, "heads");
+        dim = size_of(codes, 3, "dim");
+        need(codes, "bounds", at::kChar, Shape{pages, heads, 2, dim});
+        need(scales, "bound_scales", at::kFloat, Shape{pages, heads});
+    }
+};
+
+// (fmt, k_codes, k_scales, slots, page_len, bounds, bound_scales, stream)
+PyObject* kv_bounds(const Args& A) {
+    const KeyRows c(A, 0, 1);
+    c.scales_of(c.ks, "k_scales");
+    const Tensor& slots = A.tensor(3, "slots");
+    const int64_t page_len = A.number(4, "page_len", 1);
+    const PageBounds b(A, 5);
+    if (slots.dim() != 1) refuse("slots: expected 1 dimension, got " + shape_text(slots.sizes()));
+    const int64_t tokens = size_of(slots, 0, "tokens");
+    need(slots, "slots", at::kLong, Shape{tokens});
+    if (b.pages != c.slots / page_len || b.heads != c.heads || b.dim != c.dim)
+        refuse_tensor(b.codes, "bounds", at::kChar, {c.slots / page_len, c.heads, 2, c.dim});
+    const Device dev(c.kc);
+    dev.same({&c.ks, &slots, &b.codes, &b.scales});
+    const OnStream on(A, 7, dev);
+    call(on, [&](void* st) {
+        return rz_kv_bounds((int)c.fmt, ptr(c.kc), ptr<void>(c.ks), c.slots, c.heads, c.dim, page_len, ptr<int64_t>(slots), tokens,
+                            ptr<int8_t>(b.codes), ptr<float>(b.scales), st);
+    });
+    Py_RETURN_NONE;
+}
+
+// (q, bounds, bound_scales, page_len, page_table, lens, budget, pages, stream)
+PyObject* kv_select(const Args& A) {
+    const PageBounds b(A, 1);
+    const int64_t page_len = A.number(3, "page_len", 1), budget = A.number(6, "budget", 1);
+    const Queries s(A, 0, 4, 5, b.dim);
+    const Device dev(s.q);
+    dev.same({&b.codes, &b.scales, &s.table, &s.lens});
+    const OnStream on(A, 8, dev);
+    const Tensor pages = output(A, 7, "pages", at::kInt, Shape{s.seqs, b.heads, budget}, on);
+    const Tensor ws = workspace(rz_kv_select_workspace_bytes(s.seqs, b.heads, s.max_pages), on);
+    call(on, [&](void* st) {
+        return rz_kv_select(ptr<float>(s.q), s.q_heads, s.stride, ptr<int8_t>(b.codes), ptr<float>(b.scales), b.pages, b.heads, b.dim,
+                            page_len, ptr<int32_t>(s.table), s.seqs, s.max_pages, ptr<int32_t>(s.lens), budget,
+                            ptr<int32_t>(pages), at_or_null(ws), st);
+    });
+    return wrap(pages);
+}
+
 // One Python-callable function of N arguments.
 template <PyObject* (*F)(const Args&), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -430,7 +591,8 @@ PyMethodDef methods[] = {
     RZ_ENTRY(mxfp4_quant, 4),      RZ_ENTRY(mxfp4_pack_weight, 7), RZ_ENTRY(mxfp4_dequant, 6),
     RZ_ENTRY(mxfp4_gemm, 8),       RZ_ENTRY(mxfp4_gated, 10),      RZ_ENTRY(mxfp4_gated_quant, 11),
     RZ_ENTRY(mxfp4_gemv, 6),       RZ_ENTRY(mxfp4_gated_gemv, 8),  RZ_ENTRY(kv_cache_write, 9),
-    RZ_ENTRY(kv_cache_read, 13),   {"set_error", set_error, METH_O, nullptr},
+    RZ_ENTRY(kv_cache_read, 13),   RZ_ENTRY(kv_plan, 12),          RZ_ENTRY(kv_attention, 15),
+    RZ_ENTRY(kv_bounds, 8),        RZ_ENTRY(kv_select, 9),         {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 #undef RZ_ENTRY
 

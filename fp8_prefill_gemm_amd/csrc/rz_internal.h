@@ -166,4 +166,55 @@ struct KvRead {
 hipError_t launch_kv_write(int format, const KvWrite& A, hipStream_t st);
 hipError_t launch_kv_read(int format, const KvRead& A, int dtype, hipStream_t st);
 
+// ---- kvplan.hip
+struct KvPlan {
+    const int32_t *lens, *keep, *offsets, *free_count;
+    int32_t *page_table, *free_pages, *lens_out, *count_out;
+    int64_t* slots;
+    void* ws;  // kv_plan_ws_bytes()
+    uint32_t seqs, tokens, page_len, max_pages, num_pages;
+};
+size_t kv_plan_ws_bytes(uint32_t seqs, uint32_t tokens);
+hipError_t launch_kv_plan(const KvPlan& A, hipStream_t st);
+
+// ---- kvattn.hip
+struct KvAttend {
+    const float* q;
+    const uint8_t* codes[2];
+    const void* scales[2];
+    const int32_t *page_table, *lens, *pages;  // pages: null for every page
+    void* out;
+    float* lse;  // or null
+    void* ws;    // kv_attend_ws_bytes(), or null: one workgroup a row of heads
+    uint64_t q_stride, num_slots;
+    float scale;
+    uint32_t q_heads, heads, dim, page_len, seqs, max_pages, budget;
+};
+size_t kv_attend_ws_bytes(uint32_t q_heads, uint32_t heads, uint32_t dim, int cus);
+hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, hipStream_t st);
+
+// ---- kvselect.hip
+struct KvBounds {
+    const uint8_t* codes;
+    const void* scales;
+    const int64_t* slots;
+    int8_t* bounds;
+    float* bound_scales;
+    uint64_t num_slots, num_pages;
+    uint32_t tokens, heads, dim, page_len;
+};
+struct KvSelect {
+    const float* q;
+    const int8_t* bounds;
+    const float* bound_scales;
+    const int32_t *page_table, *lens;
+    int32_t* pages;
+    void* ws;  // kv_select_ws_bytes()
+    uint64_t q_stride;
+    uint32_t q_heads, heads, dim, num_pages, page_len, seqs, max_pages, budget;
+};
+hipError_t launch_kv_bounds(int format, const KvBounds& A, hipStream_t st);
+size_t kv_select_ws_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages);
+hipError_t launch_kv_select(const KvSelect& A, hipStream_t st);
+
 }  // namespace rz

@@ -540,6 +540,9 @@ typedef enum { RZ_KV_E4M3 = 0, RZ_KV_MXFP4 = 1 } rz_kv_format;
 #define RZ_KV_MAX_DIM 512u
 #define RZ_KV_MAX_CALL ((uint64_t)1 << 33)
 
+/* Largest seqs*heads*max_pages of one rz_kv_select call. */
+#define RZ_KV_MAX_SCORES ((uint64_t)1 << 26)
+
 /*
  * Quantise tokens' keys and values into slots of the cache.
  *   k, v          device, fp32 [tokens][heads][dim]; consecutive tokens are
@@ -574,6 +577,127 @@ int rz_kv_cache_read(int format, const uint8_t* k_codes, const void* k_scales, c
                      const void* v_scales, uint64_t num_slots, uint32_t heads, uint32_t dim, uint32_t page_len,
                      const int32_t* page_table, uint32_t seqs, uint32_t max_pages, const int32_t* offsets,
                      uint32_t rows, int dtype, void* k_out, void* v_out, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Serving from the paged cache: which pages a sequence holds, attention of
+ * one new token a sequence, and its form over chosen pages of a long cache.
+ * Forward only, as the cache itself: its rows are frozen codes.
+ * --------------------------------------------------------------------- */
+
+/*
+ * A step's pages and slots, from the sequences' lengths.
+ *   lens          device, int32 [seqs]: tokens that sequence b holds, in
+ *                 pages page_table[b][0 .. ceil(lens[b] / page_len) - 1]
+ *   keep          device, int32 [seqs]: how many of them it keeps (0: the
+ *                 sequence has ended), or NULL: all
+ *   offsets       device, int32 [seqs + 1], not decreasing: tokens
+ *                 offsets[b] .. offsets[b+1] - 1 of the step are new ones of b
+ *   page_table    device, int32 [seqs][max_pages], updated
+ *   free_pages    device, int32 [num_pages], updated: a stack of the pages
+ *                 that nobody holds, [0 .. free_count[0]) of it in use
+ *   lens_out      device out, int32 [seqs]: keep + new
+ *   count_out     device out, int32 [1]: the stack's new height
+ *   slots         device out, int64 [tokens]: slot of each new token for
+ *                 rz_kv_cache_write, -1 where it has none
+ *   ws            device workspace of rz_kv_plan_workspace_bytes(seqs, tokens)
+ *                 bytes (any contents), or NULL if that is 0
+ * First the pages that keep + new tokens no longer need go onto the stack, in
+ * order of sequence and page; then the pages that are lacking are taken from
+ * its top, in the same order.  A sequence is refused where keep is not in
+ * [0, lens], where new is negative, where lens or keep + new needs more than
+ * max_pages, and, if it lacks pages, from the first sequence on that the stack
+ * cannot serve: it gives and takes nothing, lens_out is its lens, and its
+ * tokens get -1.  Tokens of no sequence get -1 too.  Entries of page_table
+ * behind a sequence's pages are left as they are, and so is the stack above
+ * its largest height of the call.  lens_out may be lens or keep, count_out
+ * free_count; no other output may overlap an input.  With outputs of its own
+ * the same call gives the same again.  seqs == 0 gives every token -1.
+ */
+size_t rz_kv_plan_workspace_bytes(uint32_t seqs, uint32_t tokens);
+int rz_kv_plan(const int32_t* lens, const int32_t* keep, const int32_t* offsets, uint32_t seqs, uint32_t tokens,
+               uint32_t page_len, int32_t* page_table, uint32_t max_pages, int32_t* free_pages, uint32_t num_pages,
+               const int32_t* free_count, int32_t* lens_out, int32_t* count_out, int64_t* slots, void* ws, void* stream);
+
+/*
+ * Attention of one query token a sequence over the cache as it lies:
+ *   out[b][h] = sum_p w_p v_p,  w = softmax(scale * q[b][h] . k_p)
+ * over the positions p < lens[b], with k_p and v_p what rz_kv_cache_read gives
+ * in fp32 for key head h / (q_heads / heads).
+ *   q             device, fp32 [seqs][q_heads][dim]; consecutive sequences
+ *                 are q_stride elements apart (a multiple of 4, at least
+ *                 q_heads*dim).  q_heads is a multiple of heads
+ *   lens          device, int32 [seqs] (negative: 0)
+ *   pages         device, int32 [seqs][heads][budget]: only positions in
+ *                 these pages of the sequence (columns of page_table) count,
+ *                 each as often as its page is named; entries outside
+ *                 [0, max_pages) name none.  NULL: every position
+ *   scale         finite
+ *   out           device out, [seqs][q_heads][dim] of type `dtype` (rz_dtype)
+ *   lse           device out, fp32 [seqs][q_heads], or NULL:
+ *                 log sum_p exp(scale * q . k_p)
+ *   ws            device workspace of rz_kv_attention_workspace_bytes() bytes
+ *                 (any contents), or NULL: then no sequence is split over
+ *                 workgroups, which is slow where there are few
+ * Positions whose page lies outside the table or the cache do not count, nor
+ * does anything that the cache holds in them or behind a sequence's end.  A
+ * row without a position, or with all its scores -inf, gives zeros and
+ * lse -inf.  Otherwise, for n positions and gamma_t = t eps / (1 - t eps), eps = 2^-24,
+ *   |out - exact| <= (2.5 e + gamma_{8 n + 64}) sum_p w_p |v_p| + rounding to dtype,
+ *   e = max_p (gamma_{8 dim} scale sum_d |q_d k_pd| + (4 |scale q . k_p| + 8) eps)
+ * where no sum overflows and q and the rows' scales are at least 2^-100 or 0.
+ * Sums have a fixed order for given sizes and workspace.  seqs == 0 is a no-op.
+ */
+size_t rz_kv_attention_workspace_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint32_t dim);
+int rz_kv_attention(int format, const float* q, uint32_t q_heads, uint64_t q_stride, const uint8_t* k_codes,
+                    const void* k_scales, const uint8_t* v_codes, const void* v_scales, uint64_t num_slots,
+                    uint32_t heads, uint32_t dim, uint32_t page_len, const int32_t* page_table, uint32_t seqs,
+                    uint32_t max_pages, const int32_t* lens, const int32_t* pages, uint32_t budget, float scale,
+                    int dtype, void* out, float* lse, void* ws, void* stream);
+
+/*
+ * Bounds of the keys in the pages that `slots` names, for rz_kv_select; call
+ * it after rz_kv_cache_write with the same slots.
+ *   slots         device, int64 [tokens]; negative or >= num_slots: no token.
+ *                 Tokens of one page stand together, in ascending order
+ *   bounds        device, int8 [num_slots / page_len][heads][2][dim], updated
+ *   bound_scales  device, fp32 [num_slots / page_len][heads], updated
+ * A page counts as filled up to the last of its slots that is named.  With hi
+ * and lo the largest and smallest value of a column over the filled rows (as
+ * rz_kv_cache_read gives them in fp32), a the largest magnitude of any (1
+ * where it is under 2^-100) and inv = RN(127 / a), every rounding to fp32:
+ *   bounds[0] = ceil(hi * inv), bounds[1] = floor(lo * inv), at most 127 in
+ *   size, bound_scale = RN(a / 127)
+ * so values lie within bounds * bound_scale up to its rounding.  A page and
+ * head that holds a NaN or an infinity gets 127, -127 and an infinite scale.
+ * Other pages, and slots behind the last whole page, are left out.  tokens ==
+ * 0 is a no-op.
+ */
+int rz_kv_bounds(int format, const uint8_t* k_codes, const void* k_scales, uint64_t num_slots, uint32_t heads,
+                 uint32_t dim, uint32_t page_len, const int64_t* slots, uint32_t tokens, int8_t* bounds,
+                 float* bound_scales, void* stream);
+
+/*
+ * The `budget` pages of each sequence and key head with the largest scores.
+ *   q, q_heads, q_stride, page_table, lens   as for rz_kv_attention
+ *   bounds, bound_scales   of num_pages pages
+ *   pages         device out, int32 [seqs][heads][budget]: columns of
+ *                 page_table, ascending, then -1
+ *   ws            device workspace of rz_kv_select_workspace_bytes() bytes (any contents)
+ * A query of the group is held as whole numbers n_d = rint(RN(q_d * inv)) (0
+ * for a NaN), at most 127 in size, of qs = RN(a / 127), with a = max |q_d|
+ * (NaN ignored; 1 where it is under 2^-100) and inv = RN(127 / a).  A page's
+ * score is the largest over the group's queries of
+ *   RN(RN(sum_d max(n_d hi_d, n_d lo_d) * bound_scale) * qs)
+ * (the sum is exact; NaN counts as +inf): to rounding, an upper bound of the
+ * page's q . k.  The first and the last of a sequence's pages score +inf.
+ * Ties go to the lower page.  A page outside the cache is never taken.
+ * seqs == 0 is a no-op.
+ */
+size_t rz_kv_select_workspace_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages);
+int rz_kv_select(const float* q, uint32_t q_heads, uint64_t q_stride, const int8_t* bounds, const float* bound_scales,
+                 uint32_t num_pages, uint32_t heads, uint32_t dim, uint32_t page_len, const int32_t* page_table,
+                 uint32_t seqs, uint32_t max_pages, const int32_t* lens, uint32_t budget, int32_t* pages, void* ws,
+                 void* stream);
 
 /* ---------------------------------------------------------------------
  * Diagnostics: the individual steps, exposed so that each can be checked
