@@ -841,7 +841,7 @@ int rz_kv_plan(const int32_t* lens, const int32_t* keep, const int32_t* offsets,
 
 size_t rz_kv_attention_workspace_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint32_t dim) {
     if (seqs == 0 || heads == 0 || q_heads == 0 || q_heads % heads != 0 || dim == 0 || dim > RZ_KV_MAX_DIM) return 0;
-    return rz::kv_attend_ws_bytes(q_heads, heads, dim, device_cus());
+    return rz::kv_attend_ws_bytes(seqs, q_heads, heads, dim, device_cus());
 }
 
 int rz_kv_attention(int format, const float* q, uint32_t q_heads, uint64_t q_stride, const uint8_t* k_codes,

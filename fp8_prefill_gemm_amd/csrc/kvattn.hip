@@ -62,38 +62,52 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
     return v;
 }
 
-// Blocks of all sequences, by each wave for itself.
-__device__ __forceinline__ int64_t total_blocks(const KvAttend& A) {
-    int64_t n = 0;
-    for (uint32_t b = threadIdx.x % kWave; b < A.seqs; b += kWave) n += blocks_of(A, b);
-    return wave_sum(n);
-}
+// Where the batch's blocks lie, as every wave finds it for itself: sequences
+// are looked at 64 at a time, a lane each.
+struct Batch {
+    int64_t total = 0;        // blocks of all sequences
+    uint32_t b0 = 0;          // the 64 that `count` is of
+    uint32_t count = 0, sum = 0;  // a lane's sequence's blocks, and those of the lanes before it and its own
+    int64_t base = 0;         // blocks before b0
 
-// The sequence that holds block g, and the first block of it.
-struct Place {
-    uint32_t b;
-    int64_t first;
-};
-__device__ __forceinline__ Place find_block(const KvAttend& A, int64_t g) {
-    const int lane = threadIdx.x % kWave;
-    int64_t base = 0;
-    for (uint32_t b0 = 0; b0 < A.seqs; b0 += kWave) {
-        const int64_t n = b0 + lane < A.seqs ? blocks_of(A, b0 + lane) : 0;
-        int64_t sum = n;
+    __device__ __forceinline__ void look(const KvAttend& A) {
+        const uint32_t lane = threadIdx.x % kWave, b = b0 + lane;
+        count = b < A.seqs ? blocks_of(A, b) : 0;
+        sum = count;  // 64 of at most 2^24
 #pragma unroll
         for (int off = 1; off < kWave; off <<= 1) {
-            const int64_t o = __shfl_up(sum, off, kWave);
+            const uint32_t o = __shfl_up(sum, off, kWave);
             if (lane >= off) sum += o;
         }
-        const uint64_t past = __ballot(base + sum > g);
-        if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1;
-            return {b0 + l, base + __shfl(sum - n, l, kWave)};
-        }
-        base += __shfl(sum, kWave - 1, kWave);
     }
-    return {A.seqs, base};
-}
+    __device__ __forceinline__ void begin(const KvAttend& A) {
+        look(A);
+        total = (uint32_t)__shfl((int)sum, kWave - 1, kWave);
+        if (A.seqs > kWave) {
+            int64_t n = 0;
+            for (uint32_t b = kWave + threadIdx.x % kWave; b < A.seqs; b += kWave) n += blocks_of(A, b);
+            total += wave_sum(n);
+        }
+    }
+    // A block's sequence, the blocks before that and in it; g < total, not below the last one asked for.
+    struct Place {
+        uint32_t b, count;
+        int64_t first;
+    };
+    __device__ __forceinline__ Place find(const KvAttend& A, int64_t g) {
+        for (;;) {
+            const uint64_t past = __ballot(base + sum > g);
+            if (past) {
+                const int l = __ffsll((unsigned long long)past) - 1;
+                const uint32_t n = (uint32_t)__shfl((int)count, l, kWave);
+                return {b0 + l, n, base + (uint32_t)__shfl((int)sum, l, kWave) - n};
+            }
+            base += (uint32_t)__shfl((int)sum, kWave - 1, kWave);
+            b0 += kWave;
+            look(A);
+        }
+    }
+};
 
 // Workers that get a block: each of them does.  The share of worker r: blocks [T r / R, T (r + 1) / R); and the worker of block g.
 __device__ __forceinline__ uint32_t workers_of(int64_t T, uint32_t R) { return T < R ? (uint32_t)T : R; }
@@ -237,6 +251,18 @@ __device__ __forceinline__ float head_sum(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+__device__ __forceinline__ void put(void* out, int dtype, uint64_t at, float v) {
+    if (dtype == kF32)
+        static_cast<float*>(out)[at] = v;
+    else if (dtype == kF16)
+        static_cast<_Float16*>(out)[at] = (_Float16)v;
+    else
+        static_cast<__bf16*>(out)[at] = (__bf16)v;
+}
+
+// log of the sum l of 2^(x - m), in natural units; l == 0: of nothing.
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : m * 0.693147180559945309f + logf(l); }
+
 // Where a running maximum is -inf nothing has been added: any base will do.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -266,16 +292,31 @@ struct State {
     float m, l;
 };
 
-// Where partial results lie in the workspace: part s is fp32 [rows][dim], then m [rows], l [rows].
-__device__ __forceinline__ uint64_t part_floats(uint32_t rows, uint32_t dim) { return (uint64_t)rows * (dim + 2u); }
+// Floats of one part in the workspace: [rows][dim], then m [rows], l [rows]; the next begins on 16 bytes.
+__host__ __device__ __forceinline__ uint64_t part_floats(uint32_t rows, uint32_t dim) { return ((uint64_t)rows * (dim + 2u) + 3u) & ~3ull; }
 
 struct Grid {
     uint32_t R;          // workers a key head (and 16 queries)
     uint32_t tiles;      // groups of 16 queries a key head
     uint32_t part_rows;  // queries that a part has room for
     bool whole;          // workers take whole sequences
+    uint64_t info;       // floats before the workspace's record of who holds which sequence
     int dtype;
 };
+
+// Zeros for sequence b's rows of (h, z).
+template <int C>
+__device__ __forceinline__ void empty(const KvAttend& A, const Grid& G, uint32_t b, uint32_t h, uint32_t z) {
+    const uint32_t group = A.q_heads / A.heads, rows = group - z * kHeads < kHeads ? group - z * kHeads : kHeads;
+    const uint64_t head0 = (uint64_t)b * A.q_heads + h * group + z * kHeads;
+    for (uint32_t i = threadIdx.x; i < rows * 32u * C; i += kThreads) {
+        if (G.dtype == kF32)
+            static_cast<float*>(A.out)[head0 * 32u * C + i] = 0.0f;
+        else
+            static_cast<uint16_t*>(A.out)[head0 * 32u * C + i] = 0;
+    }
+    if (A.lse && threadIdx.x < rows) A.lse[head0 + threadIdx.x] = -INFINITY;
+}
 
 template <int FMT, int C>
 struct Kernel {
@@ -289,87 +330,98 @@ struct Kernel {
         };
         float m[2][kWave], l[2][kWave];
         // two tiles a wave at a time, twice
-        int32_t slot[kWaves][2][kWave];
+        uint32_t row[kWaves][2][kWave];  // rows of the cache; row 0's stands in for what is none
         float scale[FMT == kKvE4M3 ? kWaves : 1][2][2][FMT == kKvE4M3 ? kWave : 1];  // keys, values
         uint8_t byte[FMT == kKvE4M3 ? 1 : kWaves][2][2][FMT == kKvE4M3 ? 1 : C][FMT == kKvE4M3 ? 4 : kWave];
     };
 
-    // Slot of position v of (b, h), -1: none.
-    static __device__ __forceinline__ int32_t slot_at(const KvAttend& A, uint32_t b, uint32_t h, uint32_t v, uint32_t n, uint32_t len) {
-        if (v >= n) return -1;
+    // Where position v of (b, h) lies, as far as the length need not be known: its page's number in the cache (-1: none)
+    // and its place in the sequence.
+    struct Spot {
+        int32_t id;
+        uint32_t at;    // in the page
+        uint64_t place;
+    };
+    static __device__ __forceinline__ Spot spot(const KvAttend& A, uint32_t b, uint32_t h, uint32_t v) {
         uint32_t page = v / A.page_len;
-        const uint32_t at = v - page * A.page_len;
-        if (A.pages) page = (uint32_t)A.pages[((uint64_t)b * A.heads + h) * A.budget + page];
-        if (page >= A.max_pages || (uint64_t)page * A.page_len + at >= len) return -1;
-        const int32_t id = A.page_table[(uint64_t)b * A.max_pages + page];
-        const uint64_t slot = (uint64_t)(uint32_t)id * A.page_len + at;
-        return id >= 0 && slot < A.num_slots ? (int32_t)slot : -1;
+        Spot s = {-1, v - page * A.page_len, 0};
+        if (A.pages) page = page < A.budget ? (uint32_t)A.pages[((uint64_t)b * A.heads + h) * A.budget + page] : ~0u;
+        s.place = (uint64_t)page * A.page_len + s.at;
+        if (page < A.max_pages) s.id = A.page_table[(uint64_t)b * A.max_pages + page];
+        return s;
+    }
+    static __device__ __forceinline__ int32_t slot_of(const KvAttend& A, const Spot& s, uint32_t len) {
+        const uint64_t slot = (uint64_t)(uint32_t)s.id * A.page_len + s.at;
+        return s.id >= 0 && s.place < len && slot < A.num_slots ? (int32_t)slot : -1;
     }
 
-    // A tile's rows as they are loaded.
-    struct Rows {
-        uint32_t k[2][kKWords<FMT, C>], v[8][kVWords<FMT, C>];
-    };
-
-    // Loads the rows of a tile: `slot` its 32 slots, `live` those that are slots (others read row 0).
-    static __device__ __forceinline__ void load(const KvAttend& A, uint32_t h, const int32_t* slot, uint32_t live, Rows& x) {
-        const uint32_t lane = threadIdx.x % kWave, n = lane % 16, g = lane / 16;
+    // A tile's rows as they are loaded; `row` its 32 rows of the cache.
+    static __device__ __forceinline__ void load_keys(const KvAttend& A, const uint32_t* row, uint32_t (&k)[2][kKWords<FMT, C>]) {
+        const uint32_t n = threadIdx.x % 16, g = threadIdx.x % kWave / 16;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) load_k<FMT, C>(A.codes[0] + (uint64_t)row[16 * t + n] * kRow, g, k[t]);
+    }
+    static __device__ __forceinline__ void load_values(const KvAttend& A, const uint32_t* row, uint32_t (&v)[8][kVWords<FMT, C>]) {
+        const uint32_t n = threadIdx.x % 16, g = threadIdx.x % kWave / 16;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t p = 16 * t + n, s = live >> p & 1 ? (uint32_t)slot[p] : 0u;
-            load_k<FMT, C>(A.codes[0] + ((uint64_t)s * A.heads + h) * kRow, g, x.k[t]);
-        }
+            const u32x4 at = *reinterpret_cast<const u32x4*>(row + 16 * t + 4 * g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t p = 16 * (e / 4) + 4 * g + e % 4, s = live >> p & 1 ? (uint32_t)slot[p] : 0u;
-            load_v<FMT, C>(A.codes[1] + ((uint64_t)s * A.heads + h) * kRow, n, x.v[e]);
+            for (int i = 0; i < 4; ++i) load_v<FMT, C>(A.codes[1] + (uint64_t)at[i] * kRow, n, v[4 * t + i]);
         }
     }
 
-    static __device__ __forceinline__ void compute(const Shared& S, int wave, int buf, int half, uint32_t live, Rows& x, State<C>& st) {
+    // Scores of a tile, in powers of two: p[4 t + i] of position 16 t + 4 g + i.
+    static __device__ __forceinline__ void scores(const Shared& S, int wave, int buf, int half, const uint32_t (&k)[2][kKWords<FMT, C>], float (&p)[8]) {
         const uint32_t lane = threadIdx.x % kWave, n = lane % 16, g = lane / 16;
         f32x4 hi[2] = {}, lo[2] = {};
 #pragma unroll
         for (int s = 0; s < C; ++s) {
             const u32x4 q0 = S.q[0][s][lane], q1 = S.q[1][s][lane], q2 = S.q[2][s][lane];
+            u32x4 a[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                u32x4 a;
                 if constexpr (FMT == kKvE4M3)
-                    a = widen8<FMT>(x.k[t][2 * s], x.k[t][2 * s + 1], 1.0f);
+                    a[t] = widen8<FMT>(k[t][2 * s], k[t][2 * s + 1], 1.0f);
                 else
-                    a = widen8<FMT>(x.k[t][s], 0u, cvt_scale(S.byte[wave][buf][0][k_column<FMT, C>(s, g) / 32][half * 32 + 16 * t + n]));
-                hi[t] = mfma(a, q0, hi[t]);
-                lo[t] = mfma(a, q1, lo[t]);
-                lo[t] = mfma(a, q2, lo[t]);
+                    a[t] = widen8<FMT>(k[t][s], 0u, cvt_scale(S.byte[wave][buf][0][k_column<FMT, C>(s, g) / 32][half * 32 + 16 * t + n]));
             }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) hi[t] = mfma(a[t], q0, hi[t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) lo[t] = mfma(a[t], q1, lo[t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) lo[t] = mfma(a[t], q2, lo[t]);
         }
-        // a lane's eight positions: 16 t + 4 g + i
-        float p[8], top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             f32x4 sc = hi[t] + lo[t];
             if constexpr (FMT == kKvE4M3) sc *= *reinterpret_cast<const f32x4*>(&S.scale[wave][buf][0][half * 32 + 16 * t + 4 * g]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[4 * t + i] = live >> (16 * t + 4 * g + i) & 1 ? sc[i] : -INFINITY;
-                top = fmaxf(top, p[4 * t + i]);
-            }
+            for (int i = 0; i < 4; ++i) p[4 * t + i] = sc[i];
         }
+    }
+
+    // Scores into weights relative to the running maximum, `live` the positions that count; E4M3: times the values' scales.
+    static __device__ __forceinline__ void weigh(const Shared& S, int wave, int buf, int half, uint32_t live, float (&p)[8], State<C>& st) {
+        const uint32_t g = threadIdx.x % kWave / 16;
+        if (live != 0xFFFFFFFFu) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = live >> (16 * (e / 4) + 4 * g + e % 4) & 1 ? p[e] : -INFINITY;
+        }
+        float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
         top = fmaxf(head_max(top), st.m);
+        const float base = base_of(top);
         if (__any(top > st.m)) {  // rarely, after the first tiles
-            const float f = __builtin_amdgcn_exp2f(st.m - base_of(top));
+            const float f = __builtin_amdgcn_exp2f(st.m - base);
 #pragma unroll
             for (int j = 0; j < 2 * C; ++j) st.o[j] *= f;
             st.l *= f;
             st.m = top;
         }
-        const float base = base_of(top);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(p[e] - base);
-            st.l += p[e];
-        }
+        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(p[e] - base);
+        st.l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
         if constexpr (FMT == kKvE4M3) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -378,6 +430,12 @@ struct Kernel {
                 for (int i = 0; i < 4; ++i) p[4 * t + i] *= sc[i];  // 0 where there is no row
             }
         }
+    }
+
+    // o += the tile's values times its weights.
+    static __device__ __forceinline__ void add_values(const Shared& S, int wave, int buf, int half, uint32_t live, const float (&p)[8],
+                                                      uint32_t (&v)[8][kVWords<FMT, C>], State<C>& st) {
+        const uint32_t n = threadIdx.x % 16, g = threadIdx.x % kWave / 16;
         u32x4 w[3];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -390,25 +448,30 @@ struct Kernel {
             for (int e = 0; e < 8; ++e) {
                 const bool on = live >> (16 * (e / 4) + 4 * g + e % 4) & 1;
 #pragma unroll
-                for (int i = 0; i < kVWords<FMT, C>; ++i) x.v[e][i] = on ? x.v[e][i] : 0u;
+                for (int i = 0; i < kVWords<FMT, C>; ++i) v[e][i] = on ? v[e][i] : 0u;
             }
         }
         using R = VRuns<C>;
         unrolled<R::count>([&](auto r_) {
             constexpr int r = decltype(r_)::value, at = R::template word<FMT>(r), wide = R::wide(r), j0 = R::product(r);
-            // positions e and e + 1 side by side, a column at a time
-            auto go = [&](int j, const u32x4& a) {
+            constexpr int step = wide < 4 ? wide : 4;  // columns at a time
+            [[maybe_unused]] float sc[8];
+            if constexpr (FMT == kKvMXFP4) {  // a lane's columns lie in one block of 32
+                const uint8_t* by = S.byte[wave][buf][1][(R::column(r) + wide * n) / 32] + half * 32;
 #pragma unroll
-                for (int i = 0; i < 3; ++i) st.o[j] = mfma(a, w[i], st.o[j]);
-            };
-            if constexpr (FMT == kKvE4M3) {
-                constexpr int step = wide < 4 ? wide : 4;
-                unrolled<wide / step>([&](auto k_) {
-                    constexpr int k = decltype(k_)::value;
-                    u32x4 a[step];
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t four = *reinterpret_cast<const uint32_t*>(by + 16 * t + 4 * g);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t x0 = x.v[2 * e][at + k], x1 = x.v[2 * e + 1][at + k];
+                    for (int i = 0; i < 4; ++i) sc[4 * t + i] = cvt_scale(four >> (8 * i) & 255u);
+                }
+            }
+            unrolled<wide / step>([&](auto k_) {
+                constexpr int k = decltype(k_)::value;
+                u32x4 a[step];  // positions e and e + 1 side by side, a column at a time
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (FMT == kKvE4M3) {
+                        const uint32_t x0 = v[2 * e][at + k], x1 = v[2 * e + 1][at + k];
                         const uint32_t y0 = __builtin_amdgcn_perm(x1, x0, 0x05010400u);
                         a[0][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y0, 1.0f, false));
                         a[1][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y0, 1.0f, true));
@@ -417,34 +480,21 @@ struct Kernel {
                             a[2][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y1, 1.0f, false));
                             a[3][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y1, 1.0f, true));
                         }
+                    } else {
+                        unrolled<step / 2>([&](auto c_) {
+                            constexpr int c = decltype(c_)::value, two = step / 2 * k + c;  // columns 2 two and 2 two + 1
+                            const uint32_t x0 = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[2 * e][at + two / 4], sc[2 * e], two % 4));
+                            const uint32_t x1 = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[2 * e + 1][at + two / 4], sc[2 * e + 1], two % 4));
+                            a[2 * c][e] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
+                            a[2 * c + 1][e] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+                        });
                     }
-#pragma unroll
-                    for (int i = 0; i < step; ++i) go(j0 + step * k + i, a[i]);
-                });
-            } else {
-                // a lane's columns lie in one block of 32
-                float sc[8];
-                const uint8_t* by = S.byte[wave][buf][1][(R::column(r) + wide * n) / 32] + half * 32;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t four = *reinterpret_cast<const uint32_t*>(by + 16 * t + 4 * g);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[4 * t + i] = cvt_scale(four >> (8 * i) & 255u);
                 }
-                unrolled<wide / 2>([&](auto c_) {
-                    constexpr int c = decltype(c_)::value;  // columns 2 c and 2 c + 1
-                    u32x4 a[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t x0 = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x.v[2 * e][at + c / 4], sc[2 * e], c % 4));
-                        const uint32_t x1 = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x.v[2 * e + 1][at + c / 4], sc[2 * e + 1], c % 4));
-                        a[0][e] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
-                        a[1][e] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
-                    }
-                    go(j0 + 2 * c, a[0]);
-                    go(j0 + 2 * c + 1, a[1]);
-                });
-            }
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int j = 0; j < step; ++j) st.o[j0 + step * k + j] = mfma(a[j], w[i], st.o[j0 + step * k + j]);
+            });
         });
     }
 
@@ -452,13 +502,12 @@ struct Kernel {
     struct Scales2 {
         uint32_t x[FMT == kKvE4M3 ? 2 : 2 * C];
     };
-    static __device__ __forceinline__ void load_scales(const KvAttend& A, uint32_t h, int32_t slot, Scales2& s) {
-        const uint64_t row = (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * A.heads + h;
+    static __device__ __forceinline__ void load_scales(const KvAttend& A, uint64_t row, bool live, Scales2& s) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if constexpr (FMT == kKvE4M3) {
                 s.x[c] = static_cast<const uint32_t*>(A.scales[c])[row];
-                if (slot < 0) s.x[c] = 0;
+                if (!live) s.x[c] = 0;
             } else {
                 const uint8_t* p = static_cast<const uint8_t*>(A.scales[c]) + row * C;
                 if constexpr (C % 4 == 0) {
@@ -479,7 +528,7 @@ struct Kernel {
 #pragma unroll
                     for (int i = 0; i < C; ++i) s.x[c * C + i] = p[i];
                 }
-                if (slot < 0)
+                if (!live)
 #pragma unroll
                     for (int i = 0; i < C; ++i) s.x[c * C + i] = 0;
             }
@@ -503,38 +552,54 @@ struct Kernel {
         __builtin_amdgcn_wave_barrier();
     }
 
-    // Blocks [first, last) of sequence b, by the workgroup: every wave's own tiles of 32 into `st`.
-    static __device__ __forceinline__ void blocks(const KvAttend& A, Shared& S, uint32_t b, uint32_t h, uint32_t first, uint32_t last, State<C>& st) {
+    // Two blocks at a time: lanes 0..31 take a wave's tile of the first, 32..63 that of the second.
+    static __device__ __forceinline__ Spot spot_in(const KvAttend& A, uint32_t b, uint32_t h, uint32_t block) {
+        const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+        return spot(A, b, h, (block + lane / 32) * kBlock + wave * kTile + lane % 32);
+    }
+
+    // Blocks [first, last) of sequence b, by the workgroup: every wave's own tiles of 32 into `st`.  `begin`: the first ones' spots.
+    static __device__ __forceinline__ void blocks(const KvAttend& A, Shared& S, uint32_t b, uint32_t h, const Spot& begin, uint32_t len, uint32_t first,
+                                                  uint32_t last, State<C>& st) {
         const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-        const uint32_t n = length_of(A, b), len = (uint32_t)A.lens[b];
-        // two blocks at a time: lanes 0..31 take the tile of the first, 32..63 that of the second
-        auto find = [&](uint32_t block) {
-            const uint32_t at = block + lane / 32;
-            return at < last ? slot_at(A, b, h, at * kBlock + wave * kTile + lane % 32, n, len) : -1;
-        };
-        int buf = 0;
-        int32_t slot = find(first);
-        uint64_t live = __ballot(slot >= 0);
-        S.slot[wave][0][lane] = slot;
+        auto slot_in = [&](const Spot& s, uint32_t block) { return block + lane / 32 < last ? slot_of(A, s, len) : -1; };
         Scales2 sc;
-        load_scales(A, h, slot, sc);
+        // the rows of two blocks' spots into buffer `buf`, their scales on their way
+        auto rows_of = [&](const Spot& s, uint32_t block, int buf) {
+            const int32_t slot = slot_in(s, block);
+            const uint32_t row = (uint32_t)((slot < 0 ? 0 : slot) * A.heads + h);  // below 2^31
+            S.row[wave][buf][lane] = row;
+            load_scales(A, row, slot >= 0, sc);
+            return __ballot(slot >= 0);
+        };
+        uint64_t live = rows_of(begin, first, 0);
         wave_sync();
-        Rows x0, x1;
-        load(A, h, S.slot[wave][0], (uint32_t)live, x0);
+        uint32_t k[2][kKWords<FMT, C>], v[8][kVWords<FMT, C>];
+        load_keys(A, S.row[wave][0], k);
+        load_values(A, S.row[wave][0], v);
         keep_scales(S, wave, 0, sc);
         wave_sync();
+        int buf = 0;
         for (uint32_t at = first; at < last; at += 2) {
-            int32_t ahead = at + 2 < last ? find(at + 2) : -1;  // uniform branch
-            load(A, h, S.slot[wave][buf] + 32, (uint32_t)(live >> 32), x1);
-            if ((uint32_t)live) compute(S, wave, buf, 0, (uint32_t)live, x0, st);
-            const uint64_t next = __ballot(ahead >= 0);
-            S.slot[wave][buf ^ 1][lane] = ahead;
-            load_scales(A, h, ahead, sc);
-            wave_sync();
-            load(A, h, S.slot[wave][buf ^ 1], (uint32_t)next, x0);
-            if ((uint32_t)(live >> 32)) compute(S, wave, buf, 1, (uint32_t)(live >> 32), x1, st);
-            keep_scales(S, wave, buf ^ 1, sc);
-            wave_sync();
+            Spot s = {-1, 0, 0};
+            if (at + 2 < last) s = spot_in(A, b, h, at + 2);
+            uint64_t next = 0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // the next tile's keys are loaded once this one's are used, its values likewise
+                const uint32_t on = (uint32_t)(live >> (32 * half));
+                const uint32_t* then = half ? S.row[wave][buf ^ 1] : S.row[wave][buf] + 32;
+                float p[8];
+                if (on) scores(S, wave, buf, half, k, p);
+                load_keys(A, then, k);
+                if (on) {
+                    weigh(S, wave, buf, half, on, p, st);
+                    add_values(S, wave, buf, half, on, p, v, st);
+                }
+                load_values(A, then, v);
+                if (half == 0) next = rows_of(s, at + 2, buf ^ 1);
+                if (half == 1) keep_scales(S, wave, buf ^ 1, sc);
+                wave_sync();
+            }
             live = next;
             buf ^= 1;
         }
@@ -562,27 +627,66 @@ struct Kernel {
         st.m = m;
     }
 
-    // Blocks [first, last) of (b, h, tile z); `part`: where they go if they are not the whole of a sequence.
-    static __device__ void piece(const KvAttend& A, const Grid& G, Shared& S, uint32_t b, uint32_t h, uint32_t z, uint32_t first, uint32_t last, float* part) {
+    // A lane's columns of its head, from element `at` on, times f.
+    template <int DT>
+    static __device__ __forceinline__ void store(void* out, uint64_t at, uint32_t g, float f, const State<C>& st) {
+        using T = std::conditional_t<DT == kF32, float, std::conditional_t<DT == kF16, _Float16, __bf16>>;
+        using R = VRuns<C>;
+        unrolled<R::count>([&](auto r_) {
+            constexpr int r = decltype(r_)::value, wide = R::wide(r), j0 = R::product(r);
+            typedef T vec __attribute__((ext_vector_type(wide < 4 ? wide : 4)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // `wide` consecutive columns
+#pragma unroll
+                for (int j = 0; j < wide; j += 4) {
+                    vec x;
+#pragma unroll
+                    for (int e = 0; e < (wide < 4 ? wide : 4); ++e) x[e] = (T)(st.o[j0 + j + e][i] * f);
+                    *reinterpret_cast<vec*>(static_cast<T*>(out) + at + R::column(r) + wide * (4 * g + i) + j) = x;
+                }
+        });
+    }
+
+    // Blocks [first, last) of (b, h, tile z), all of them if `last` is 0; `part`: where they go if they are not the whole of
+    // a sequence.  What needs no length is loaded beside it.
+    static __device__ __forceinline__ void piece(const KvAttend& A, const Grid& G, Shared& S, uint32_t b, uint32_t h, uint32_t z, uint32_t first, uint32_t last,
+                                                 float* part) {
         const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, n = lane % 16, g = lane / 16;
         const uint32_t group = A.q_heads / A.heads, rows = group - z * kHeads < kHeads ? group - z * kHeads : kHeads;
         const uint64_t head0 = (uint64_t)b * A.q_heads + h * group + z * kHeads;
+        const Spot begin = spot_in(A, b, h, first);
+        constexpr int kTurns = (C + kWaves - 1) / kWaves;
+        f32x4 q[kTurns][2] = {};
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const uint32_t s = i * kWaves + wave;
+            if (s < C && n < rows) {
+                const float* p = A.q + b * A.q_stride + (uint64_t)(h * group + z * kHeads + n) * D + k_column<FMT, C>(s, g);
+                q[i][0] = *reinterpret_cast<const f32x4*>(p);
+                q[i][1] = *reinterpret_cast<const f32x4*>(p + 4);
+            }
+        }
+        const uint32_t len = length_of(A, b);
+        if (last == 0) {
+            last = (len + kBlock - 1) / kBlock;
+            if (last == 0) return empty<C>(A, G, b, h, z);
+        }
         __syncthreads();  // the last piece's results have been read
         const float unit = A.scale * 1.44269504088896341f;  // scores in powers of two
-        for (uint32_t s = wave; s < C; s += kWaves) {
-            u32x4 w[3] = {};
-            if (n < rows) {
-                const float* q = A.q + b * A.q_stride + (uint64_t)(h * group + z * kHeads + n) * D + k_column<FMT, C>(s, g);
-                const f32x4 a = *reinterpret_cast<const f32x4*>(q) * unit, c = *reinterpret_cast<const f32x4*>(q + 4) * unit;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Parts p = e < 2 ? split2(a[2 * e], a[2 * e + 1]) : split2(c[2 * e - 4], c[2 * e - 3]);
+        for (int i = 0; i < kTurns; ++i) {
+            const uint32_t s = i * kWaves + wave;
+            u32x4 w[3];
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) w[i][e] = p.part[i];
-                }
+            for (int e = 0; e < 4; ++e) {
+                const f32x4 x = q[i][e / 2] * unit;
+                const Parts p = split2(x[2 * (e % 2)], x[2 * (e % 2) + 1]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) w[k][e] = p.part[k];
             }
+            if (s < C)
 #pragma unroll
-            for (int i = 0; i < 3; ++i) S.q[i][s][lane] = w[i];
+                for (int k = 0; k < 3; ++k) S.q[k][s][lane] = w[k];
         }
         __syncthreads();
         State<C> st;
@@ -590,7 +694,7 @@ struct Kernel {
         for (int j = 0; j < 2 * C; ++j) st.o[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
         st.m = -INFINITY;
         st.l = 0.0f;
-        blocks(A, S, b, h, first, last, st);
+        blocks(A, S, b, h, begin, A.pages ? (uint32_t)A.lens[b] : len, first, last, st);
         st.l = head_sum(st.l);
         __syncthreads();  // q is no longer read
         if (wave >= 2) give(S, wave - 2, st);
@@ -602,150 +706,117 @@ struct Kernel {
         if (wave != 0) return;
         take(S, 0, st);
         if (n >= rows) return;
-        const float inv = 1.0f / st.l;
-        using R = VRuns<C>;
-        unrolled<R::count>([&](auto r_) {
-            constexpr int r = decltype(r_)::value, wide = R::wide(r), j0 = R::product(r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // `wide` consecutive columns
-                const uint32_t col = R::column(r) + wide * (4 * g + i);
-                if (part) {
-#pragma unroll
-                    for (int j = 0; j < wide; ++j) part[n * D + col + j] = st.o[j0 + j][i];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < wide; ++j) {
-                        const float v = st.l == 0.0f ? 0.0f : st.o[j0 + j][i] * inv;
-                        const uint64_t at = (head0 + n) * D + col + j;
-                        if (G.dtype == kF32)
-                            static_cast<float*>(A.out)[at] = v;
-                        else if (G.dtype == kF16)
-                            static_cast<_Float16*>(A.out)[at] = (_Float16)v;
-                        else
-                            static_cast<__bf16*>(A.out)[at] = (__bf16)v;
-                    }
-                }
-            }
-        });
+        const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;
+        if (part)
+            store<kF32>(part, n * D, g, 1.0f, st);
+        else if (G.dtype == kF32)
+            store<kF32>(A.out, (head0 + n) * D, g, inv, st);
+        else if (G.dtype == kF16)
+            store<kF16>(A.out, (head0 + n) * D, g, inv, st);
+        else
+            store<kBF16>(A.out, (head0 + n) * D, g, inv, st);
         if (g == 0) {
             if (part) {
                 part[G.part_rows * D + n] = st.m;
                 part[G.part_rows * (D + 1) + n] = st.l;
             } else if (A.lse)
-                A.lse[head0 + n] = st.l == 0.0f ? -INFINITY : st.m * 0.693147180559945309f + logf(st.l);
+                A.lse[head0 + n] = lse_of(st.m, st.l);
         }
     }
 };
-
-// Zeros for sequence b's rows of (h, z).
-template <int C>
-__device__ __forceinline__ void empty(const KvAttend& A, const Grid& G, uint32_t b, uint32_t h, uint32_t z) {
-    const uint32_t group = A.q_heads / A.heads, rows = group - z * kHeads < kHeads ? group - z * kHeads : kHeads;
-    const uint64_t head0 = (uint64_t)b * A.q_heads + h * group + z * kHeads;
-    for (uint32_t i = threadIdx.x; i < rows * 32u * C; i += kThreads) {
-        if (G.dtype == kF32)
-            static_cast<float*>(A.out)[head0 * 32u * C + i] = 0.0f;
-        else
-            static_cast<uint16_t*>(A.out)[head0 * 32u * C + i] = 0;
-    }
-    if (A.lse && threadIdx.x < rows) A.lse[head0 + threadIdx.x] = -INFINITY;
-}
 
 template <int FMT, int C>
 __global__ __launch_bounds__(kThreads, C <= 4 ? 2 : 1) void attend_kernel(KvAttend A, Grid G) {
     using K = Kernel<FMT, C>;
     __shared__ typename K::Shared S;
     const uint32_t lanes = A.heads * G.tiles, r = blockIdx.x / lanes, h = blockIdx.x % lanes / G.tiles, z = blockIdx.x % G.tiles;
-    if (G.whole) {
-        for (uint32_t b = r; b < A.seqs; b += G.R) {
-            const uint32_t n = blocks_of(A, b);
-            if (n)
-                K::piece(A, G, S, b, h, z, 0, n, nullptr);
-            else
-                empty<C>(A, G, b, h, z);
-        }
-        return;
-    }
-    for (uint32_t b = r; b < A.seqs; b += G.R)
-        if (blocks_of(A, b) == 0) empty<C>(A, G, b, h, z);
-    const int64_t T = total_blocks(A);
-    const uint32_t R = workers_of(T, G.R);
-    if (r >= R) return;
-    int64_t at = share(T, r, R);
-    const int64_t end = share(T, r + 1, R);
-    Place p = find_block(A, at);
+    uint32_t* info = reinterpret_cast<uint32_t*>(static_cast<float*>(A.ws) + G.info);
     float* part = static_cast<float*>(A.ws) + (uint64_t)blockIdx.x * 2u * part_floats(G.part_rows, K::D);
+    Batch batch;
+    uint32_t R = G.R;
+    int64_t at = r, end = A.seqs;  // whole sequences r, r + R, ..; or blocks
+    if (!G.whole) {
+        for (uint32_t b = r; b < A.seqs; b += G.R)
+            if (blocks_of(A, b) == 0) {
+                empty<C>(A, G, b, h, z);
+                if (threadIdx.x == 0) info[2 * b] = info[2 * b + 1] = 0;
+            }
+        batch.begin(A);
+        R = workers_of(batch.total, G.R);
+        if (r >= R) return;
+        at = share(batch.total, r, R);
+        end = share(batch.total, r + 1, R);
+    }
     while (at < end) {
-        const uint32_t n = blocks_of(A, p.b), first = (uint32_t)(at - p.first);
-        if (n == 0) {
-            ++p.b;
-            continue;
+        uint32_t b = (uint32_t)at, first = 0, last = 0;
+        float* to = nullptr;
+        if (!G.whole) {
+            const Batch::Place p = batch.find(A, at);
+            b = p.b;
+            first = (uint32_t)(at - p.first);
+            last = end - p.first < p.count ? (uint32_t)(end - p.first) : p.count;
+            if (first != 0 || last != p.count) to = part + (first == 0 ? part_floats(G.part_rows, K::D) : 0);
+            if (first == 0 && threadIdx.x == 0) {  // the same from every key head's worker
+                info[2 * b] = r;
+                info[2 * b + 1] = worker_of(batch.total, p.first + p.count - 1, R);
+            }
         }
-        const uint32_t last = end - p.first < n ? (uint32_t)(end - p.first) : n;
-        K::piece(A, G, S, p.b, h, z, first, last, first == 0 && last == n ? nullptr : part + (first == 0 ? part_floats(G.part_rows, K::D) : 0));
-        at += last - first;
-        p.first += n;
-        ++p.b;
+        K::piece(A, G, S, b, h, z, first, last, to);
+        at += G.whole ? R : last - first;
     }
 }
 
-// Joins the parts of sequences that several workers hold: a workgroup a query.
-__global__ __launch_bounds__(kThreads) void join_kernel(KvAttend A, Grid G) {
+// Joins the parts of a sequence that several workers hold: a workgroup a query
+// head.  Four columns a lane, and the parts shared among the rows of lanes,
+// each with a running maximum of its own.
+constexpr int kJoin = 1024;
+__global__ __launch_bounds__(kJoin) void join_kernel(KvAttend A, Grid G) {
     const uint32_t b = blockIdx.x / A.q_heads, qh = blockIdx.x % A.q_heads, group = A.q_heads / A.heads;
     const uint32_t h = qh / group, z = qh % group / kHeads, row = qh % group % kHeads, lanes = A.heads * G.tiles;
-    const uint32_t n = blocks_of(A, b);
-    if (n == 0) return;
-    int64_t T = 0, g0 = 0;
-    for (uint32_t i = threadIdx.x % kWave; i < A.seqs; i += kWave) {
-        const uint32_t k = blocks_of(A, i);
-        T += k;
-        if (i < b) g0 += k;
-    }
-    T = wave_sum(T);
-    g0 = wave_sum(g0);
-    const uint32_t R = workers_of(T, G.R), r0 = worker_of(T, g0, R), r1 = worker_of(T, g0 + n - 1, R);
+    const uint32_t* info = reinterpret_cast<const uint32_t*>(static_cast<const float*>(A.ws) + G.info);
+    const uint32_t r0 = info[2 * b], r1 = info[2 * b + 1];
     if (r0 == r1) return;
     const uint64_t floats = part_floats(G.part_rows, A.dim);
-    // worker r0 began the sequence: its second part; the others hold it from their start: their first
-    auto part = [&](uint32_t r) {
-        const uint32_t block = r * lanes + h * G.tiles + z;
-        return static_cast<const float*>(A.ws) + ((uint64_t)block * 2u + (r == r0 ? 1u : 0u)) * floats;
-    };
-    __shared__ float top_of[kWaves], sum_of[kWaves];
-    float top = -INFINITY;
-    for (uint32_t r = r0 + threadIdx.x; r <= r1; r += kThreads) top = fmaxf(top, part(r)[G.part_rows * A.dim + row]);
-    for (int off = 1; off < kWave; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-    if (threadIdx.x % kWave == 0) top_of[threadIdx.x / kWave] = top;
-    __syncthreads();
-    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, top_of[i]);
-    const float base = base_of(top);
-    float sum = 0.0f;
-    for (uint32_t r = r0 + threadIdx.x; r <= r1; r += kThreads) {
-        const float* p = part(r) + G.part_rows * A.dim + row;
-        sum += p[G.part_rows] * __builtin_amdgcn_exp2f(p[0] - base);
-    }
-    for (int off = 1; off < kWave; off <<= 1) sum += __shfl_xor(sum, off, kWave);
-    if (threadIdx.x % kWave == 0) sum_of[threadIdx.x / kWave] = sum;
-    __syncthreads();
-    sum = 0.0f;
-    for (int i = 0; i < kWaves; ++i) sum += sum_of[i];
-    const float inv = 1.0f / sum;
-    const uint64_t head = (uint64_t)b * A.q_heads + qh;
-    for (uint32_t d = threadIdx.x; d < A.dim; d += kThreads) {
-        float o = 0.0f;
-        for (uint32_t r = r0; r <= r1; ++r) {
-            const float* p = part(r);
-            o += p[row * A.dim + d] * __builtin_amdgcn_exp2f(p[G.part_rows * A.dim + row] - base);
+    const uint32_t cols = A.dim / 4u, ways = kJoin / cols, way = threadIdx.x / cols, col = threadIdx.x % cols * 4u;
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o = {};
+    if (way < ways) {
+#pragma unroll 4
+        for (uint32_t r = r0 + way; r <= r1; r += ways) {
+            // worker r0 began the sequence: its second part; the others hold it from their start: their first
+            const uint32_t block = r * lanes + h * G.tiles + z;
+            const float* p = static_cast<const float*>(A.ws) + ((uint64_t)block * 2u + (r == r0 ? 1u : 0u)) * floats;
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p + row * A.dim + col);
+            const float mp = p[G.part_rows * A.dim + row], lp = p[G.part_rows * (A.dim + 1u) + row];
+            const float top = fmaxf(m, mp), base = base_of(top);
+            const float f = __builtin_amdgcn_exp2f(m - base), e = __builtin_amdgcn_exp2f(mp - base);
+            o = o * f + v * e;
+            l = l * f + lp * e;
+            m = top;
         }
-        const float v = sum == 0.0f ? 0.0f : o * inv;
-        if (G.dtype == kF32)
-            static_cast<float*>(A.out)[head * A.dim + d] = v;
-        else if (G.dtype == kF16)
-            static_cast<_Float16*>(A.out)[head * A.dim + d] = (_Float16)v;
-        else
-            static_cast<__bf16*>(A.out)[head * A.dim + d] = (__bf16)v;
     }
-    if (A.lse && threadIdx.x == 0) A.lse[head] = sum == 0.0f ? -INFINITY : top * 0.693147180559945309f + logf(sum);
+    __shared__ f32x4 o_of[kJoin];
+    __shared__ float m_of[kJoin], l_of[kJoin];
+    o_of[threadIdx.x] = o;
+    m_of[threadIdx.x] = m;
+    l_of[threadIdx.x] = l;
+    __syncthreads();
+    if (way != 0) return;
+    float top = m;
+    for (uint32_t w = 1; w < ways; ++w) top = fmaxf(top, m_of[w * cols + threadIdx.x]);
+    const float base = base_of(top);
+    o = (f32x4){};
+    l = 0.0f;
+    for (uint32_t w = 0; w < ways; ++w) {
+        const float e = __builtin_amdgcn_exp2f(m_of[w * cols + threadIdx.x] - base);
+        o += o_of[w * cols + threadIdx.x] * e;
+        l += l_of[w * cols + threadIdx.x] * e;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const uint64_t head = (uint64_t)b * A.q_heads + qh;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put(A.out, G.dtype, head * A.dim + col + i, l == 0.0f ? 0.0f : o[i] * inv);
+    if (A.lse && threadIdx.x == 0) A.lse[head] = lse_of(top, l);
 }
 
 // Workgroups of a launch: two a compute unit.
@@ -773,11 +844,16 @@ uint32_t split(uint32_t q_heads, uint32_t heads, int cus) {
     return r ? r : 1;
 }
 
+// Floats of all workers' parts.
+uint64_t part_total(uint32_t q_heads, uint32_t heads, uint32_t dim, int cus) {
+    const uint64_t lanes = (uint64_t)heads * ((q_heads / heads + kHeads - 1) / kHeads);
+    return split(q_heads, heads, cus) * lanes * 2u * part_floats(part_rows(q_heads, heads), dim);
+}
+
 }  // namespace
 
-size_t kv_attend_ws_bytes(uint32_t q_heads, uint32_t heads, uint32_t dim, int cus) {
-    const uint64_t lanes = (uint64_t)heads * ((q_heads / heads + kHeads - 1) / kHeads);
-    return split(q_heads, heads, cus) * lanes * 2u * (uint64_t)part_rows(q_heads, heads) * (dim + 2u) * 4u;
+size_t kv_attend_ws_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint32_t dim, int cus) {
+    return (part_total(q_heads, heads, dim, cus) + 2u * (uint64_t)seqs) * 4u;
 }
 
 hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, hipStream_t st) {
@@ -785,9 +861,10 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
     G.tiles = (A.q_heads / A.heads + kHeads - 1) / kHeads;
     G.part_rows = part_rows(A.q_heads, A.heads);
     G.dtype = dtype;
+    G.info = part_total(A.q_heads, A.heads, A.dim, cus);
     // one block a sequence at most: nothing to split
     const uint64_t most = (uint64_t)(A.pages ? A.budget : A.max_pages) * A.page_len;
-    G.whole = !A.ws || most <= kBlock || (uint64_t)A.seqs * A.q_heads >= 0x1000000u;
+    G.whole = !A.ws || most <= kBlock || (uint64_t)A.seqs * A.q_heads >= 0x400000u;
     const uint32_t lanes = A.heads * G.tiles;
     G.R = split(A.q_heads, A.heads, cus);
     if (G.whole) {
@@ -801,7 +878,7 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
         else
             attend_kernel<kKvMXFP4, C><<<G.R * lanes, kThreads, 0, st>>>(A, G);
     });
-    if (!G.whole) join_kernel<<<A.seqs * A.q_heads, kThreads, 0, st>>>(A, G);
+    if (!G.whole) join_kernel<<<A.seqs * A.q_heads, kJoin, 0, st>>>(A, G);
     return hipGetLastError();
 }
 

@@ -190,7 +190,7 @@ struct KvAttend {
     float scale;
     uint32_t q_heads, heads, dim, page_len, seqs, max_pages, budget;
 };
-size_t kv_attend_ws_bytes(uint32_t q_heads, uint32_t heads, uint32_t dim, int cus);
+size_t kv_attend_ws_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint32_t dim, int cus);
 hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, hipStream_t st);
 
 // ---- kvselect.hip
