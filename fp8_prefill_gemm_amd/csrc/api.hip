@@ -855,6 +855,10 @@ int rz_kv_attention(int format, const float* q, uint32_t q_heads, uint64_t q_str
     if (dtype != RZ_F32 && dtype != RZ_F16 && dtype != RZ_BF16) return fail(RZ_ERR_VALUE, "%s: unknown dtype %d", fn, dtype);
     if (scale - scale != 0.0f) return fail(RZ_ERR_VALUE, "%s: scale must be finite", fn);
     if (pages && (uint64_t)budget * page_len > 0x7FFFFFFFu) return fail(RZ_ERR_SHAPE, "%s: budget*page_len exceeds 2^31 - 1", fn);
+    // workgroups share the positions of all sequences in blocks of 128, which count in 31 bits
+    uint64_t most = (uint64_t)(pages ? budget : max_pages) * page_len;
+    most = most < 0x7FFFFFFFu ? most : 0x7FFFFFFFu;
+    if ((most + 127u) / 128u * seqs > 0x7FFFFFFFu) return fail(RZ_ERR_SHAPE, "%s: the sequences' pages hold more than 2^38 positions", fn);
     if (seqs == 0) return RZ_OK;  // nothing to read or write
     if (!q || (num_slots != 0 && (!k_codes || !k_scales || !v_codes || !v_scales)) || (max_pages != 0 && !page_table) || !lens || !out)
         return fail(RZ_ERR_NULL, "%s: null pointer", fn);

@@ -2,11 +2,12 @@
 //   out[b][h] = sum_p w_p v_p,  w = softmax(scale q[b][h] . k_p),
 // one pass over the rows with the running maximum and sum of the softmax.
 //
-// A step reads each cached row once for all the queries of its key head, so
-// it is bound by memory; the products run on the bf16 matrix cores, whose
-// operands hold E4M3 and E2M1 codes exactly.  Both products put positions or
-// columns of the cache in the rows of the result and query heads in its
-// columns (16 of them), so that a lane has the same head throughout:
+// A step reads each cached row once for all the queries of its key head; what
+// bounds it beside memory is the instructions a row takes, so both products
+// run on the fp16 matrix cores, whose operands hold E4M3 and E2M1 codes
+// exactly.  Both put positions or columns of the cache in the rows of the
+// result and query heads in its columns (16 of them), so that a lane has the
+// same head throughout:
 //   scores  S[32 positions][16 heads] = K q^T, a lane reads 8 columns of a row
 //           a step as they lie; which columns those are is the same for both
 //           operands, so 16-byte loads serve two steps (four in MXFP4);
@@ -15,15 +16,23 @@
 //           for head l % 16, which is where S leaves them, and reads V's rows
 //           of these eight positions.  Nothing moves between lanes but the
 //           maximum.
-// q and the weights stay fp32: each is the exact sum of three bf16 parts (8
-// bits each, cut, not rounded), multiplied one after another into fp32.
+// q and the weights count to 22 bits, as two fp16 parts each (the second the
+// first's rounding, rounded: 2^-22 at most).  With up to 8 queries a key head
+// the parts lie side by side in the 16 columns, one product for both.  What
+// fp16's range does not hold is kept outside it: a head's q is scaled to
+// 2^14 <= max |q| < 2^15, a row's scale (MXFP4: its largest block's) multiplies
+// scores and weights in fp32, and weights are taken times 2^14 over the
+// largest scale of the values so far, so that what is lost lies 2^-38 below
+// the largest value times its weight.
 //
 // Workgroups take equal shares of all blocks of 128 positions, whatever the
-// sequences' lengths: worker r of R reads blocks [T r / R, T (r + 1) / R) of
-// the T that the batch has, for one key head (and 16 of its queries); the
-// heads of the same blocks are neighbours in the grid, so a page is read by
-// all of them at a time.  What is not the whole of a sequence goes to the
-// workspace, at most two parts a worker, and a second launch joins them.
+// sequences' lengths: worker r of R reads its run of the blocks that the batch
+// has, for one key head (and 16 of its queries); the heads of the same blocks
+// go to one XCD, so that a page's lines, which hold rows of several heads, are
+// fetched once (24 sequences of 131072 positions in all, MXFP4 rows of 64 bytes: 46 -> 42
+// us).
+// What is not the whole of a sequence goes to the workspace, at most two parts
+// a worker, and a second launch joins them.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -37,96 +46,168 @@ namespace rz {
 namespace {
 using namespace mx;
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr uint32_t kTile = 32;               // positions a wave takes at a time
 constexpr uint32_t kBlock = kTile * kWaves;  // and a workgroup
+constexpr uint32_t kChunk = 8 * kBlock;      // positions whose rows are looked up at a time
 constexpr uint32_t kHeads = 16;              // queries of a key head that a workgroup serves
+constexpr uint32_t kPacked = 8;              // up to so many: both parts of theirs at a time
+
+// A value that all lanes hold, in a scalar register.
+__device__ __forceinline__ uint32_t scalar(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+
+// What the launch adds to its arguments.
+struct Grid {
+    uint32_t R;          // workers a key head (and 16 queries)
+    uint32_t group;      // queries a key head
+    uint32_t tiles;      // and 16 of them at a time
+    uint32_t part_rows;  // queries that a part has room for
+    uint32_t most;       // positions that a sequence's pages hold at most
+    uint32_t magic, shift;  // v / page_len is v * magic >> 31 + shift for v < 2^31
+    bool whole;          // workers take whole sequences
+    bool near;           // a worker's key heads go to one XCD
+    int dtype;
+    uint64_t info;       // floats before the workspace's record of who holds which sequence
+};
 
 // Positions that sequence b attends (those of a choice may hold gaps).
-__device__ __forceinline__ uint32_t length_of(const KvAttend& A, uint32_t b) {
+__device__ __forceinline__ uint32_t length_of(const KvAttend& A, const Grid& G, uint32_t b) {
     const int32_t len = A.lens[b];
     if (len <= 0 || A.num_slots == 0) return 0;
-    if (A.pages) return A.budget * A.page_len;
-    const uint64_t most = (uint64_t)A.max_pages * A.page_len;
-    return (uint32_t)((uint64_t)len < most ? len : most);
+    return A.pages || (uint32_t)len > G.most ? G.most : (uint32_t)len;
 }
-__device__ __forceinline__ uint32_t blocks_of(const KvAttend& A, uint32_t b) { return (length_of(A, b) + kBlock - 1) / kBlock; }
+__device__ __forceinline__ uint32_t blocks_of(const KvAttend& A, const Grid& G, uint32_t b) { return (length_of(A, G, b) + kBlock - 1) / kBlock; }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) v += __shfl_xor(v, off, kWave);
-    return v;
+// Sum and maximum over a wave's lanes, in a scalar register.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F&& f) {
+    auto ror = [](uint32_t x, auto n) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + decltype(n)::value, 0xF, 0xF, true); };
+    v = f(v, ror(v, std::integral_constant<int, 8>{}));
+    v = f(v, ror(v, std::integral_constant<int, 4>{}));
+    v = f(v, ror(v, std::integral_constant<int, 2>{}));
+    v = f(v, ror(v, std::integral_constant<int, 1>{}));
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = f(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return scalar(f(b[0], b[1]));
+}
+__device__ __forceinline__ uint32_t wave_total(uint32_t v) {
+    return wave_reduce(v, [](uint32_t a, uint32_t b) { return a + b; });
 }
 
-// Where the batch's blocks lie, as every wave finds it for itself: sequences
-// are looked at 64 at a time, a lane each.
+// The batch as units of work, as every wave finds it for itself: sequence b of
+// n blocks is ceil(n / per) units of nearly equal size.  Sequences are looked
+// at 64 at a time, a lane each.
+//
+// A unit costs about four blocks' time beside its blocks (its lookups, the
+// first loads, the join of its waves), so a worker should have one, or where
+// there are many sequences two: `per` is the least that makes R units (2 R
+// where more than R / 2 sequences have something), found by halving where one
+// look holds all sequences, and bounded by T / (2 R - S) otherwise.  (A run of
+// equal length for each worker instead, cut where sequences end, took 37 us on
+// 64 sequences of 65536 positions: two or three pieces for the last worker.)
 struct Batch {
-    int64_t total = 0;        // blocks of all sequences
-    uint32_t b0 = 0;          // the 64 that `count` is of
-    uint32_t count = 0, sum = 0;  // a lane's sequence's blocks, and those of the lanes before it and its own
-    int64_t base = 0;         // blocks before b0
+    uint32_t per = 1, units = 0;
+    uint32_t b0 = 0;                      // the 64 that the lanes' values are of
+    uint32_t base = 0, split_base = 0;    // units, and units that are not whole sequences, before b0
+    uint32_t blocks = 0, sum = 0, split = 0;  // a lane's sequence's blocks; units up to and with it; those of them not whole sequences
 
-    __device__ __forceinline__ void look(const KvAttend& A) {
+    __device__ __forceinline__ uint32_t parts(uint32_t n) const { return (n + per - 1) / per; }
+    __device__ __forceinline__ void look(const KvAttend& A, const Grid& G) {
         const uint32_t lane = threadIdx.x % kWave, b = b0 + lane;
-        count = b < A.seqs ? blocks_of(A, b) : 0;
-        sum = count;  // 64 of at most 2^24
+        blocks = b < A.seqs ? blocks_of(A, G, b) : 0;
+    }
+    __device__ __forceinline__ void scan() {
+        const uint32_t lane = threadIdx.x % kWave, n = parts(blocks);
+        sum = n;
+        split = n > 1 ? n : 0;
 #pragma unroll
         for (int off = 1; off < kWave; off <<= 1) {
-            const uint32_t o = __shfl_up(sum, off, kWave);
-            if (lane >= off) sum += o;
+            const uint32_t o = (uint32_t)__shfl_up((int)sum, off, kWave), u = (uint32_t)__shfl_up((int)split, off, kWave);
+            if (lane >= off) {
+                sum += o;
+                split += u;
+            }
         }
     }
-    __device__ __forceinline__ void begin(const KvAttend& A) {
-        look(A);
-        total = (uint32_t)__shfl((int)sum, kWave - 1, kWave);
+    __device__ __forceinline__ void begin(const KvAttend& A, const Grid& G) {
+        look(A, G);
+        uint32_t n = blocks, some = blocks != 0;
+        for (uint32_t b = kWave + threadIdx.x % kWave; b < A.seqs; b += kWave) {
+            const uint32_t k = blocks_of(A, G, b);
+            n += k;
+            some += k != 0;
+        }
+        const uint32_t T = wave_total(n), S = wave_total(some), R = G.R;
+        const uint32_t most = 2u * S > R ? 2u * R : R;
+        uint32_t low = (T + most - 1) / most, high = S < most ? (T + (most - S) - 1) / (most - S) : (T + R - 1) / R;
+        low = low ? low : 1;
+        per = high > low ? high : low;
+        if (A.seqs <= kWave && S <= most) {
+            while (low < per) {  // parts of `per` are few enough
+                const uint32_t was = per, mid = (low + per) / 2;
+                per = mid;
+                if (wave_total(parts(blocks)) > most) {
+                    low = mid + 1;
+                    per = was;
+                }
+            }
+        }
+        per = scalar(per);
+        scan();
+        units = lane_value(sum, kWave - 1);
         if (A.seqs > kWave) {
-            int64_t n = 0;
-            for (uint32_t b = kWave + threadIdx.x % kWave; b < A.seqs; b += kWave) n += blocks_of(A, b);
-            total += wave_sum(n);
+            uint32_t u = 0;
+            for (uint32_t b = kWave + threadIdx.x % kWave; b < A.seqs; b += kWave) u += parts(blocks_of(A, G, b));
+            units += wave_total(u);
         }
     }
-    // A block's sequence, the blocks before that and in it; g < total, not below the last one asked for.
-    struct Place {
-        uint32_t b, count;
-        int64_t first;
+    // The first block of part i of n blocks' `count` parts.
+    static __device__ __forceinline__ uint32_t cut(uint32_t n, uint32_t i, uint32_t count) {
+        const uint32_t each = n / count, more = n - each * count;
+        return each * i + (i < more ? i : more);
+    }
+    // Unit u < units, not below the last one asked for: blocks [first, last) of sequence b, which is all of it or `part` of `count`,
+    // the workspace's `at`.
+    struct Unit {
+        uint32_t b, first, last, part, count, at;
     };
-    __device__ __forceinline__ Place find(const KvAttend& A, int64_t g) {
+    __device__ __forceinline__ Unit find(const KvAttend& A, const Grid& G, uint32_t u) {
         for (;;) {
-            const uint64_t past = __ballot(base + sum > g);
+            const uint64_t past = __ballot(base + sum > u);
             if (past) {
                 const int l = __ffsll((unsigned long long)past) - 1;
-                const uint32_t n = (uint32_t)__shfl((int)count, l, kWave);
-                return {b0 + l, n, base + (uint32_t)__shfl((int)sum, l, kWave) - n};
+                const uint32_t n = lane_value(blocks, l), count = scalar(parts(n)), part = u - (base + lane_value(sum, l) - count);
+                return {b0 + l, scalar(cut(n, part, count)), scalar(cut(n, part + 1, count)), part, count,
+                        split_base + lane_value(split, l) - count + part};
             }
-            base += (uint32_t)__shfl((int)sum, kWave - 1, kWave);
+            base += lane_value(sum, kWave - 1);
+            split_base += lane_value(split, kWave - 1);
             b0 += kWave;
-            look(A);
+            look(A, G);
+            scan();
         }
     }
 };
 
-// Workers that get a block: each of them does.  The share of worker r: blocks [T r / R, T (r + 1) / R); and the worker of block g.
-__device__ __forceinline__ uint32_t workers_of(int64_t T, uint32_t R) { return T < R ? (uint32_t)T : R; }
-__device__ __forceinline__ int64_t share(int64_t T, uint32_t r, uint32_t R) { return T * r / R; }
-__device__ __forceinline__ uint32_t worker_of(int64_t T, int64_t g, uint32_t R) { return (uint32_t)(((g + 1) * R - 1) / T); }
-
 // ---- rows of the cache in registers
 
-__device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ uint32_t bits(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
 
-// Eight consecutive codes as bf16 (times `scale`, a power of two, for MXFP4).
+// Eight consecutive codes as fp16 (times `scale`, a power of two, for MXFP4).
 template <int FMT>
 __device__ __forceinline__ u32x4 widen8(uint32_t w0, uint32_t w1, float scale) {
     if constexpr (FMT == kKvE4M3) {
-        return (u32x4){bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false)), bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true)),
-                       bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false)), bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true))};
+        return (u32x4){bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false)), bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true)),
+                       bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false)), bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true))};
     } else {
-        return (u32x4){bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, scale, 0)), bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, scale, 1)),
-                       bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, scale, 2)), bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w0, scale, 3))};
+        return (u32x4){bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w0, scale, 0)), bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w0, scale, 1)),
+                       bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w0, scale, 2)), bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w0, scale, 3))};
     }
 }
 
@@ -266,48 +347,47 @@ __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -
 // Where a running maximum is -inf nothing has been added: any base will do.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
-// Three bf16 parts of two values, which they sum to exactly (24 bits in all).
+// Two fp16 parts of two values.
 struct Parts {
-    uint32_t part[3];
+    uint32_t part[2];
 };
 __device__ __forceinline__ Parts split2(float a, float b) {
-    Parts s;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        s.part[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-        a -= __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
-        b -= __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
-    }
-    return s;
+    const f16x2 h = {(_Float16)a, (_Float16)b};
+    float minus = -1.0f;
+    asm("" : "+s"(minus));  // kept a factor, so that one instruction widens and subtracts
+    const f16x2 l = {(_Float16)__builtin_fmaf((float)h.x, minus, a), (_Float16)__builtin_fmaf((float)h.y, minus, b)};
+    return {{bits(h), bits(l)}};
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// A wave's running state: o[j][i] is column VRuns' product j, row 4 g + i, of head l % 16.
+// Sum over lanes l and l ^ 8, where the two parts of packed heads lie.
+__device__ __forceinline__ float part_sum(float v) {
+    return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x128, 0xF, 0xF, true));  // row_ror:8
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// A wave's running state: o[j][i] is column VRuns' product j, row 4 g + i, of
+// head l % 16 (or part l / 8 of head l % 8).  m is the largest score as the
+// products give it, and m c = `base` in powers of two; o and l are sums of
+// 2^(score - base + shift).
 template <int C>
 struct State {
     f32x4 o[2 * C];
-    float m, l;
+    float m, base, l;
 };
 
 // Floats of one part in the workspace: [rows][dim], then m [rows], l [rows]; the next begins on 16 bytes.
 __host__ __device__ __forceinline__ uint64_t part_floats(uint32_t rows, uint32_t dim) { return ((uint64_t)rows * (dim + 2u) + 3u) & ~3ull; }
 
-struct Grid {
-    uint32_t R;          // workers a key head (and 16 queries)
-    uint32_t tiles;      // groups of 16 queries a key head
-    uint32_t part_rows;  // queries that a part has room for
-    bool whole;          // workers take whole sequences
-    uint64_t info;       // floats before the workspace's record of who holds which sequence
-    int dtype;
-};
-
 // Zeros for sequence b's rows of (h, z).
 template <int C>
 __device__ __forceinline__ void empty(const KvAttend& A, const Grid& G, uint32_t b, uint32_t h, uint32_t z) {
-    const uint32_t group = A.q_heads / A.heads, rows = group - z * kHeads < kHeads ? group - z * kHeads : kHeads;
+    const uint32_t group = G.group, rows = group - z * kHeads < kHeads ? group - z * kHeads : kHeads;
     const uint64_t head0 = (uint64_t)b * A.q_heads + h * group + z * kHeads;
     for (uint32_t i = threadIdx.x; i < rows * 32u * C; i += kThreads) {
         if (G.dtype == kF32)
@@ -318,41 +398,154 @@ __device__ __forceinline__ void empty(const KvAttend& A, const Grid& G, uint32_t
     if (A.lse && threadIdx.x < rows) A.lse[head0 + threadIdx.x] = -INFINITY;
 }
 
-template <int FMT, int C>
+template <int FMT, int C, bool PACK>
 struct Kernel {
     static constexpr uint32_t D = 32 * C;
+    static constexpr int kParts = PACK ? 1 : 2;              // products for a q or a weight
     static constexpr uint32_t kRow = FMT == kKvE4M3 ? D : D / 2;  // bytes
 
-    struct Shared {
-        union {
-            u32x4 q[3][C][kWave];       // the query's parts as the matrix cores take them
-            float o[2][8 * C][kWave];   // two waves' results
-        };
-        float m[2][kWave], l[2][kWave];
-        // two tiles a wave at a time, twice
-        uint32_t row[kWaves][2][kWave];  // rows of the cache; row 0's stands in for what is none
-        float scale[FMT == kKvE4M3 ? kWaves : 1][2][2][FMT == kKvE4M3 ? kWave : 1];  // keys, values
-        uint8_t byte[FMT == kKvE4M3 ? 1 : kWaves][2][2][FMT == kKvE4M3 ? 1 : C][FMT == kKvE4M3 ? 4 : kWave];
+    struct Chunk {
+        u32x4 q[kParts][C][kWave];  // the queries' parts as the matrix cores take them
+        // a chunk of positions: rows of the cache (row 0's for what is none), which of a tile's count, their scales
+        uint32_t row[kChunk];
+        uint32_t live[kChunk / kTile];
+        float scale[2][kChunk];  // keys, values
+        float largest[kWaves], q_largest[kWaves][16];  // scale of the values, |q| of a head
+        uint8_t byte[FMT == kKvE4M3 ? 1 : 2][FMT == kKvE4M3 ? 1 : C][FMT == kKvE4M3 ? 4 : kChunk];
+    };
+    union Shared {
+        Chunk c;
+        struct {
+            float o[kWaves][8 * C][kWave], m[kWaves][kWave], l[kWaves][kWave];
+        } w;  // the waves' results
     };
 
-    // Where position v of (b, h) lies, as far as the length need not be known: its page's number in the cache (-1: none)
-    // and its place in the sequence.
+    // Where position v lies, as far as the length need not be known: its page's number in the cache (-1: none), its place in it
+    // and in the sequence (no length reaches 2^32 - 1).
     struct Spot {
         int32_t id;
-        uint32_t at;    // in the page
-        uint64_t place;
+        uint32_t at, place;
     };
-    static __device__ __forceinline__ Spot spot(const KvAttend& A, uint32_t b, uint32_t h, uint32_t v) {
-        uint32_t page = v / A.page_len;
-        Spot s = {-1, v - page * A.page_len, 0};
-        if (A.pages) page = page < A.budget ? (uint32_t)A.pages[((uint64_t)b * A.heads + h) * A.budget + page] : ~0u;
-        s.place = (uint64_t)page * A.page_len + s.at;
-        if (page < A.max_pages) s.id = A.page_table[(uint64_t)b * A.max_pages + page];
+    static __device__ __forceinline__ Spot spot(const KvAttend& A, const Grid& G, uint32_t b, uint32_t h, uint32_t v) {
+        uint32_t column = __umulhi(2u * v, G.magic) >> G.shift;
+        Spot s = {-1, v - column * A.page_len, 0};
+        if (A.pages) column = column < A.budget ? (uint32_t)A.pages[((uint64_t)b * A.heads + h) * A.budget + column] : ~0u;
+        const uint64_t place = (uint64_t)column * A.page_len + s.at;
+        s.place = place >> 32 ? ~0u : (uint32_t)place;
+        if (v < G.most && column < A.max_pages) s.id = A.page_table[(uint64_t)b * A.max_pages + column];
         return s;
     }
     static __device__ __forceinline__ int32_t slot_of(const KvAttend& A, const Spot& s, uint32_t len) {
         const uint64_t slot = (uint64_t)(uint32_t)s.id * A.page_len + s.at;
         return s.id >= 0 && s.place < len && slot < A.num_slots ? (int32_t)slot : -1;
+    }
+
+    // A row's scales: fp32 of its key and value; MXFP4: their largest blocks', and the blocks' bytes relative to those.
+    struct Scales2 {
+        float row[2];
+        uint32_t byte[FMT == kKvE4M3 ? 1 : 2 * C];
+    };
+    static __device__ __forceinline__ void load_scales(const KvAttend& A, uint64_t row, Scales2& s) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if constexpr (FMT == kKvE4M3) {
+                s.row[c] = static_cast<const float*>(A.scales[c])[row];
+            } else {
+                const uint8_t* p = static_cast<const uint8_t*>(A.scales[c]) + row * C;
+                uint32_t* x = s.byte + c * C;
+                if constexpr (C % 4 == 0) {
+#pragma unroll
+                    for (int i = 0; i < C / 4; ++i) x[i] = reinterpret_cast<const uint32_t*>(p)[i];
+                } else if constexpr (C % 2 == 0) {
+#pragma unroll
+                    for (int i = 0; i < C / 2; ++i) x[i] = reinterpret_cast<const uint16_t*>(p)[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C; ++i) x[i] = p[i];
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void ready(bool live, Scales2& s) {
+        if constexpr (FMT == kKvMXFP4) {
+            constexpr int per = C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1;  // bytes that were loaded at a time
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t* x = s.byte + c * C;
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = C - 1; i >= 0; --i) {
+                    x[i] = x[i / per] >> (8 * (i % per)) & 255u;
+                    top = x[i] != kNanByte && x[i] > top ? x[i] : top;
+                }
+                s.row[c] = __uint_as_float(top ? top << 23 : 0x00400000u);
+#pragma unroll
+                for (int i = 0; i < C; ++i) x[i] = x[i] == kNanByte ? kNanByte : x[i] + 127u > top ? x[i] + 127u - top : 0u;
+            }
+        }
+        if (!live) {
+            s.row[0] = s.row[1] = 0.0f;
+            if constexpr (FMT == kKvMXFP4)
+#pragma unroll
+                for (int i = 0; i < 2 * C; ++i) s.byte[i] = 0;
+        }
+    }
+
+    // The workgroup's lanes find a chunk's positions, kTurns each; `blocks` of it are used.
+    static constexpr int kTurns = kChunk / kThreads;
+    struct Spots {
+        Spot s[kTurns];
+    };
+    static __device__ __forceinline__ void find(const KvAttend& A, const Grid& G, uint32_t b, uint32_t h, uint32_t block, Spots& x) {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) x.s[i] = spot(A, G, b, h, block * kBlock + i * kThreads + threadIdx.x);
+    }
+    // First the rows, whose scales are then on their way, and once those are here the scales.
+    struct Staged {
+        Scales2 sc[kTurns];
+        uint32_t live;
+    };
+    static __device__ __forceinline__ void stage_rows(const KvAttend& A, Chunk& S, uint32_t h, uint32_t blocks, uint32_t len, const Spots& x, Staged& y) {
+        y.live = 0;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const uint32_t at = i * kThreads + threadIdx.x;
+            const int32_t slot = at < blocks * kBlock ? slot_of(A, x.s[i], len) : -1;
+            const uint32_t row = (uint32_t)(slot < 0 ? 0 : slot) * A.heads + h;  // below 2^31
+            load_scales(A, row, y.sc[i]);
+            const uint64_t on = __ballot(slot >= 0);
+            S.row[at] = row;
+            if (threadIdx.x % kTile == 0) S.live[at / kTile] = (uint32_t)(on >> (threadIdx.x % kWave));
+            y.live |= (slot >= 0 ? 1u : 0u) << i;
+        }
+    }
+    static __device__ __forceinline__ void stage_scales(Chunk& S, Staged& y) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const uint32_t at = i * kThreads + threadIdx.x;
+            ready(y.live >> i & 1, y.sc[i]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                S.scale[c][at] = y.sc[i].row[c];
+                if constexpr (FMT == kKvMXFP4)
+#pragma unroll
+                    for (int k = 0; k < C; ++k) S.byte[c][k][at] = (uint8_t)y.sc[i].byte[c * C + k];
+            }
+            const uint32_t key = __float_as_uint(y.sc[i].row[1]) & 0x7FFFFFFFu;
+            top = key < 0x7F800000u && key > top ? key : top;
+        }
+        top = wave_reduce(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+        if (threadIdx.x % kWave == 0) S.largest[threadIdx.x / kWave] = __uint_as_float(top);
+    }
+    // The exponent of a power of two over the chunk's scales of values, within what the weights' range allows, at least e.
+    static __device__ __forceinline__ int exponent(const Chunk& S, int e) {
+        float top = S.largest[0];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) top = fmaxf(top, S.largest[i]);
+        int x = (int)(__float_as_uint(top) >> 23) - 126;
+        x = x < 110 ? x : 110;
+        return (int)scalar((uint32_t)(x > e ? x : e));
     }
 
     // A tile's rows as they are loaded; `row` its 32 rows of the cache.
@@ -371,77 +564,80 @@ struct Kernel {
         }
     }
 
-    // Scores of a tile, in powers of two: p[4 t + i] of position 16 t + 4 g + i.
-    static __device__ __forceinline__ void scores(const Shared& S, int wave, int buf, int half, const uint32_t (&k)[2][kKWords<FMT, C>], float (&p)[8]) {
+    // Scores of the tile at `at` of the chunk, in units of c powers of two: p[4 t + i] of position 16 t + 4 g + i.
+    static __device__ __forceinline__ void scores(const Chunk& S, uint32_t at, const uint32_t (&k)[2][kKWords<FMT, C>], float (&p)[8]) {
         const uint32_t lane = threadIdx.x % kWave, n = lane % 16, g = lane / 16;
-        f32x4 hi[2] = {}, lo[2] = {};
+        f32x4 sum[2] = {};
 #pragma unroll
         for (int s = 0; s < C; ++s) {
-            const u32x4 q0 = S.q[0][s][lane], q1 = S.q[1][s][lane], q2 = S.q[2][s][lane];
             u32x4 a[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if constexpr (FMT == kKvE4M3)
                     a[t] = widen8<FMT>(k[t][2 * s], k[t][2 * s + 1], 1.0f);
                 else
-                    a[t] = widen8<FMT>(k[t][s], 0u, cvt_scale(S.byte[wave][buf][0][k_column<FMT, C>(s, g) / 32][half * 32 + 16 * t + n]));
+                    a[t] = widen8<FMT>(k[t][s], 0u, cvt_scale(S.byte[0][k_column<FMT, C>(s, g) / 32][at + 16 * t + n]));
             }
 #pragma unroll
-            for (int t = 0; t < 2; ++t) hi[t] = mfma(a[t], q0, hi[t]);
+            for (int i = kParts - 1; i >= 0; --i) {
+                const u32x4 q = S.q[i][s][lane];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) lo[t] = mfma(a[t], q1, lo[t]);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) lo[t] = mfma(a[t], q2, lo[t]);
+                for (int t = 0; t < 2; ++t) sum[t] = mfma(a[t], q, sum[t]);
+            }
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            f32x4 sc = hi[t] + lo[t];
-            if constexpr (FMT == kKvE4M3) sc *= *reinterpret_cast<const f32x4*>(&S.scale[wave][buf][0][half * 32 + 16 * t + 4 * g]);
+            const f32x4 sc = *reinterpret_cast<const f32x4*>(&S.scale[0][at + 16 * t + 4 * g]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[4 * t + i] = sc[i];
+            for (int i = 0; i < 4; ++i) p[4 * t + i] = (PACK ? part_sum(sum[t][i]) : sum[t][i]) * sc[i];
         }
     }
 
-    // Scores into weights relative to the running maximum, `live` the positions that count; E4M3: times the values' scales.
-    static __device__ __forceinline__ void weigh(const Shared& S, int wave, int buf, int half, uint32_t live, float (&p)[8], State<C>& st) {
+    // Scores into weights relative to the running maximum times 2^shift and the values' scales, `live` the positions that count.
+    static __device__ __forceinline__ void weigh(const Chunk& S, uint32_t at, uint32_t live, float c, float shift, float (&p)[8], State<C>& st) {
         const uint32_t g = threadIdx.x % kWave / 16;
         if (live != 0xFFFFFFFFu) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[e] = live >> (16 * (e / 4) + 4 * g + e % 4) & 1 ? p[e] : -INFINITY;
         }
         float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-        top = fmaxf(head_max(top), st.m);
-        const float base = base_of(top);
+        top = head_max(top);
         if (__any(top > st.m)) {  // rarely, after the first tiles
-            const float f = __builtin_amdgcn_exp2f(st.m - base);
+            top = fmaxf(top, st.m);
+            const float base = base_of(top) * c;
+            const float f = st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.base - base);
 #pragma unroll
             for (int j = 0; j < 2 * C; ++j) st.o[j] *= f;
             st.l *= f;
             st.m = top;
+            st.base = base;
         }
+        const float off = shift - st.base;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(p[e] - base);
+        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[e], c, off));
         st.l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-        if constexpr (FMT == kKvE4M3) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const f32x4 sc = *reinterpret_cast<const f32x4*>(&S.scale[wave][buf][1][half * 32 + 16 * t + 4 * g]);
+        for (int t = 0; t < 2; ++t) {
+            const f32x4 sc = *reinterpret_cast<const f32x4*>(&S.scale[1][at + 16 * t + 4 * g]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[4 * t + i] *= sc[i];  // 0 where there is no row
-            }
+            for (int i = 0; i < 4; ++i) p[4 * t + i] *= sc[i];  // 0 where there is no row
         }
     }
 
     // o += the tile's values times its weights.
-    static __device__ __forceinline__ void add_values(const Shared& S, int wave, int buf, int half, uint32_t live, const float (&p)[8],
+    static __device__ __forceinline__ void add_values(const Chunk& S, uint32_t at, uint32_t live, const float (&p)[8],
                                                       uint32_t (&v)[8][kVWords<FMT, C>], State<C>& st) {
         const uint32_t n = threadIdx.x % 16, g = threadIdx.x % kWave / 16;
-        u32x4 w[3];
+        u32x4 w[kParts];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const Parts s = split2(p[2 * e], p[2 * e + 1]);
-#pragma unroll
-            for (int i = 0; i < 3; ++i) w[i][e] = s.part[i];
+            if constexpr (PACK) {
+                w[0][e] = n < kPacked ? s.part[0] : s.part[1];
+            } else {
+                w[0][e] = s.part[0];
+                w[1][e] = s.part[1];
+            }
         }
         if (live != 0xFFFFFFFFu) {  // what lies in no row's place must not meet a weight of 0
 #pragma unroll
@@ -453,11 +649,11 @@ struct Kernel {
         }
         using R = VRuns<C>;
         unrolled<R::count>([&](auto r_) {
-            constexpr int r = decltype(r_)::value, at = R::template word<FMT>(r), wide = R::wide(r), j0 = R::product(r);
+            constexpr int r = decltype(r_)::value, w0 = R::template word<FMT>(r), wide = R::wide(r), j0 = R::product(r);
             constexpr int step = wide < 4 ? wide : 4;  // columns at a time
             [[maybe_unused]] float sc[8];
             if constexpr (FMT == kKvMXFP4) {  // a lane's columns lie in one block of 32
-                const uint8_t* by = S.byte[wave][buf][1][(R::column(r) + wide * n) / 32] + half * 32;
+                const uint8_t* by = S.byte[1][(R::column(r) + wide * n) / 32] + at;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const uint32_t four = *reinterpret_cast<const uint32_t*>(by + 16 * t + 4 * g);
@@ -471,298 +667,259 @@ struct Kernel {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (FMT == kKvE4M3) {
-                        const uint32_t x0 = v[2 * e][at + k], x1 = v[2 * e + 1][at + k];
+                        const uint32_t x0 = v[2 * e][w0 + k], x1 = v[2 * e + 1][w0 + k];
                         const uint32_t y0 = __builtin_amdgcn_perm(x1, x0, 0x05010400u);
-                        a[0][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y0, 1.0f, false));
-                        a[1][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y0, 1.0f, true));
+                        a[0][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y0, 1.0f, false));
+                        a[1][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y0, 1.0f, true));
                         if constexpr (step == 4) {
                             const uint32_t y1 = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
-                            a[2][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y1, 1.0f, false));
-                            a[3][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y1, 1.0f, true));
+                            a[2][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y1, 1.0f, false));
+                            a[3][e] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y1, 1.0f, true));
                         }
                     } else {
                         unrolled<step / 2>([&](auto c_) {
                             constexpr int c = decltype(c_)::value, two = step / 2 * k + c;  // columns 2 two and 2 two + 1
-                            const uint32_t x0 = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[2 * e][at + two / 4], sc[2 * e], two % 4));
-                            const uint32_t x1 = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[2 * e + 1][at + two / 4], sc[2 * e + 1], two % 4));
+                            const uint32_t x0 = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v[2 * e][w0 + two / 4], sc[2 * e], two % 4));
+                            const uint32_t x1 = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v[2 * e + 1][w0 + two / 4], sc[2 * e + 1], two % 4));
                             a[2 * c][e] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
                             a[2 * c + 1][e] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
                         });
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
+                for (int i = 0; i < kParts; ++i)
 #pragma unroll
                     for (int j = 0; j < step; ++j) st.o[j0 + step * k + j] = mfma(a[j], w[i], st.o[j0 + step * k + j]);
             });
         });
     }
 
-    // This lane's row's scales: fp32 of its key and value, or C bytes each.
-    struct Scales2 {
-        uint32_t x[FMT == kKvE4M3 ? 2 : 2 * C];
-    };
-    static __device__ __forceinline__ void load_scales(const KvAttend& A, uint64_t row, bool live, Scales2& s) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if constexpr (FMT == kKvE4M3) {
-                s.x[c] = static_cast<const uint32_t*>(A.scales[c])[row];
-                if (!live) s.x[c] = 0;
-            } else {
-                const uint8_t* p = static_cast<const uint8_t*>(A.scales[c]) + row * C;
-                if constexpr (C % 4 == 0) {
-#pragma unroll
-                    for (int i = 0; i < C / 4; ++i) {
-                        const uint32_t w = reinterpret_cast<const uint32_t*>(p)[i];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s.x[c * C + 4 * i + j] = w >> (8 * j) & 255u;
-                    }
-                } else if constexpr (C % 2 == 0) {
-#pragma unroll
-                    for (int i = 0; i < C / 2; ++i) {
-                        const uint32_t w = reinterpret_cast<const uint16_t*>(p)[i];
-                        s.x[c * C + 2 * i] = w & 255u;
-                        s.x[c * C + 2 * i + 1] = w >> 8;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < C; ++i) s.x[c * C + i] = p[i];
-                }
-                if (!live)
-#pragma unroll
-                    for (int i = 0; i < C; ++i) s.x[c * C + i] = 0;
-            }
-        }
-    }
-    static __device__ __forceinline__ void keep_scales(Shared& S, int wave, int buf, const Scales2& s) {
-        const uint32_t lane = threadIdx.x % kWave;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if constexpr (FMT == kKvE4M3)
-                S.scale[wave][buf][c][lane] = __uint_as_float(s.x[c]);
-            else
-#pragma unroll
-                for (int i = 0; i < C; ++i) S.byte[wave][buf][c][i][lane] = (uint8_t)s.x[c * C + i];
-        }
-    }
-
-    // LDS of one wave, written and read by its own lanes.
-    static __device__ __forceinline__ void wave_sync() {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    }
-
-    // Two blocks at a time: lanes 0..31 take a wave's tile of the first, 32..63 that of the second.
-    static __device__ __forceinline__ Spot spot_in(const KvAttend& A, uint32_t b, uint32_t h, uint32_t block) {
-        const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-        return spot(A, b, h, (block + lane / 32) * kBlock + wave * kTile + lane % 32);
-    }
-
-    // Blocks [first, last) of sequence b, by the workgroup: every wave's own tiles of 32 into `st`.  `begin`: the first ones' spots.
-    static __device__ __forceinline__ void blocks(const KvAttend& A, Shared& S, uint32_t b, uint32_t h, const Spot& begin, uint32_t len, uint32_t first,
-                                                  uint32_t last, State<C>& st) {
-        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-        auto slot_in = [&](const Spot& s, uint32_t block) { return block + lane / 32 < last ? slot_of(A, s, len) : -1; };
-        Scales2 sc;
-        // the rows of two blocks' spots into buffer `buf`, their scales on their way
-        auto rows_of = [&](const Spot& s, uint32_t block, int buf) {
-            const int32_t slot = slot_in(s, block);
-            const uint32_t row = (uint32_t)((slot < 0 ? 0 : slot) * A.heads + h);  // below 2^31
-            S.row[wave][buf][lane] = row;
-            load_scales(A, row, slot >= 0, sc);
-            return __ballot(slot >= 0);
-        };
-        uint64_t live = rows_of(begin, first, 0);
-        wave_sync();
+    struct Rows {
         uint32_t k[2][kKWords<FMT, C>], v[8][kVWords<FMT, C>];
-        load_keys(A, S.row[wave][0], k);
-        load_values(A, S.row[wave][0], v);
-        keep_scales(S, wave, 0, sc);
-        wave_sync();
-        int buf = 0;
-        for (uint32_t at = first; at < last; at += 2) {
-            Spot s = {-1, 0, 0};
-            if (at + 2 < last) s = spot_in(A, b, h, at + 2);
-            uint64_t next = 0;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // the next tile's keys are loaded once this one's are used, its values likewise
-                const uint32_t on = (uint32_t)(live >> (32 * half));
-                const uint32_t* then = half ? S.row[wave][buf ^ 1] : S.row[wave][buf] + 32;
-                float p[8];
-                if (on) scores(S, wave, buf, half, k, p);
-                load_keys(A, then, k);
-                if (on) {
-                    weigh(S, wave, buf, half, on, p, st);
-                    add_values(S, wave, buf, half, on, p, v, st);
-                }
-                load_values(A, then, v);
-                if (half == 0) next = rows_of(s, at + 2, buf ^ 1);
-                if (half == 1) keep_scales(S, wave, buf ^ 1, sc);
-                wave_sync();
+    };
+    static __device__ __forceinline__ void load(const KvAttend& A, const uint32_t* row, Rows& x) {
+        load_keys(A, row, x.k);
+        load_values(A, row, x.v);
+    }
+    static __device__ __forceinline__ void tile(const Chunk& S, uint32_t at, uint32_t live, float c, float shift, Rows& x, State<C>& st) {
+        float p[8];
+        scores(S, at, x.k, p);
+        weigh(S, at, live, c, shift, p, st);
+        add_values(S, at, live, p, x.v, st);
+    }
+
+    // `blocks` blocks of the chunk, by the workgroup: every wave's own tiles of 32 into `st`, the next one's rows on their way;
+    // x0: the first one's.
+    static __device__ __forceinline__ void chunk(const KvAttend& A, const Chunk& S, uint32_t blocks, float c, float shift, Rows& x0, State<C>& st) {
+        Rows x1;
+        uint32_t at = scalar(threadIdx.x / kWave) * kTile;
+#pragma unroll 1
+        for (uint32_t i = 0; i < blocks; i += 2, at += 2 * kBlock) {
+            if (i + 1 < blocks) load(A, S.row + at + kBlock, x1);
+            const uint32_t on = scalar(S.live[at / kTile]);
+            if (on) tile(S, at, on, c, shift, x0, st);
+            if (i + 1 < blocks) {
+                if (i + 2 < blocks) load(A, S.row + at + 2 * kBlock, x0);
+                const uint32_t then = scalar(S.live[(at + kBlock) / kTile]);
+                if (then) tile(S, at + kBlock, then, c, shift, x1, st);
             }
-            live = next;
-            buf ^= 1;
         }
     }
 
-    // Adds the state that lane, by lane, lies in set `c` of the workgroup's LDS.
-    static __device__ __forceinline__ void give(Shared& S, int c, const State<C>& st) {
-        const int lane = threadIdx.x % kWave;
-#pragma unroll
-        for (int j = 0; j < 2 * C; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S.o[c][4 * j + i][lane] = st.o[j][i];
-        S.m[c][lane] = st.m;
-        S.l[c][lane] = st.l;
-    }
-    static __device__ __forceinline__ void take(const Shared& S, int c, State<C>& st) {
-        const int lane = threadIdx.x % kWave;
-        const float m = fmaxf(st.m, S.m[c][lane]), base = base_of(m);
-        const float f = __builtin_amdgcn_exp2f(st.m - base), e = __builtin_amdgcn_exp2f(S.m[c][lane] - base);
-#pragma unroll
-        for (int j = 0; j < 2 * C; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st.o[j][i] = st.o[j][i] * f + S.o[c][4 * j + i][lane] * e;
-        st.l = st.l * f + S.l[c][lane] * e;
-        st.m = m;
-    }
-
-    // A lane's columns of its head, from element `at` on, times f.
+    // A lane's columns in row i of each product, from element `at` on, times f.
     template <int DT>
-    static __device__ __forceinline__ void store(void* out, uint64_t at, uint32_t g, float f, const State<C>& st) {
+    static __device__ __forceinline__ void store(void* out, uint64_t at, uint32_t row, float f, const float (&o)[2 * C]) {
         using T = std::conditional_t<DT == kF32, float, std::conditional_t<DT == kF16, _Float16, __bf16>>;
         using R = VRuns<C>;
         unrolled<R::count>([&](auto r_) {
-            constexpr int r = decltype(r_)::value, wide = R::wide(r), j0 = R::product(r);
-            typedef T vec __attribute__((ext_vector_type(wide < 4 ? wide : 4)));
+            constexpr int r = decltype(r_)::value, wide = R::wide(r), j0 = R::product(r), most = wide < 4 ? wide : 4;
+            typedef T vec __attribute__((ext_vector_type(most)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)  // `wide` consecutive columns
+            for (int j = 0; j < wide; j += most) {  // `wide` consecutive columns
+                vec x;
 #pragma unroll
-                for (int j = 0; j < wide; j += 4) {
-                    vec x;
-#pragma unroll
-                    for (int e = 0; e < (wide < 4 ? wide : 4); ++e) x[e] = (T)(st.o[j0 + j + e][i] * f);
-                    *reinterpret_cast<vec*>(static_cast<T*>(out) + at + R::column(r) + wide * (4 * g + i) + j) = x;
-                }
+                for (int e = 0; e < most; ++e) x[e] = (T)(o[j0 + j + e] * f);
+                *reinterpret_cast<vec*>(static_cast<T*>(out) + at + R::column(r) + wide * row + j) = x;
+            }
         });
     }
 
     // Blocks [first, last) of (b, h, tile z), all of them if `last` is 0; `part`: where they go if they are not the whole of
     // a sequence.  What needs no length is loaded beside it.
-    static __device__ __forceinline__ void piece(const KvAttend& A, const Grid& G, Shared& S, uint32_t b, uint32_t h, uint32_t z, uint32_t first, uint32_t last,
-                                                 float* part) {
-        const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, n = lane % 16, g = lane / 16;
-        const uint32_t group = A.q_heads / A.heads, rows = group - z * kHeads < kHeads ? group - z * kHeads : kHeads;
+    static __device__ __forceinline__ void piece(const KvAttend& A, const Grid& G, Shared& shared, uint32_t b, uint32_t h, uint32_t z, uint32_t first,
+                                                 uint32_t last, float* part) {
+        Chunk& S = shared.c;
+        const uint32_t lane = threadIdx.x % kWave, wave = scalar(threadIdx.x / kWave), n = lane % 16, g = lane / 16;
+        const uint32_t group = G.group, rows = group - z * kHeads < kHeads ? group - z * kHeads : kHeads;
         const uint64_t head0 = (uint64_t)b * A.q_heads + h * group + z * kHeads;
-        const Spot begin = spot_in(A, b, h, first);
-        constexpr int kTurns = (C + kWaves - 1) / kWaves;
-        f32x4 q[kTurns][2] = {};
+        Spots spots;
+        find(A, G, b, h, first, spots);
+        constexpr int kSteps = (C + kWaves - 1) / kWaves;
+        const uint32_t head = PACK ? n % kPacked : n;
+        f32x4 q[kSteps][2] = {};
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
             const uint32_t s = i * kWaves + wave;
-            if (s < C && n < rows) {
-                const float* p = A.q + b * A.q_stride + (uint64_t)(h * group + z * kHeads + n) * D + k_column<FMT, C>(s, g);
+            if (s < C && head < rows) {
+                const float* p = A.q + b * A.q_stride + (uint64_t)(h * group + z * kHeads + head) * D + k_column<FMT, C>(s, g);
                 q[i][0] = *reinterpret_cast<const f32x4*>(p);
                 q[i][1] = *reinterpret_cast<const f32x4*>(p + 4);
             }
         }
-        const uint32_t len = length_of(A, b);
+        const uint32_t len = length_of(A, G, b);
         if (last == 0) {
             last = (len + kBlock - 1) / kBlock;
             if (last == 0) return empty<C>(A, G, b, h, z);
         }
+        const uint32_t until = A.pages ? (uint32_t)A.lens[b] : len;
         __syncthreads();  // the last piece's results have been read
-        const float unit = A.scale * 1.44269504088896341f;  // scores in powers of two
+        Staged staged;
+        stage_rows(A, S, h, last - first, until, spots, staged);
+        float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(q[i][0][e]), fabsf(q[i][1][e])));
+        top = head_max(top);
+        if (g == 0) S.q_largest[wave][n] = top;
+        __syncthreads();
+        Rows x0;
+        load(A, S.row + wave * kTile, x0);
+        stage_scales(S, staged);
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) top = fmaxf(top, S.q_largest[i][n]);
+        // a head's power of two, and what brings its scores back to powers of two
+        int up = 141 - (int)(__float_as_uint(top) >> 23);
+        up = up < -112 ? -112 : up > 126 ? 126 : up;
+        const float c = A.scale == 0.0f ? 1.0f : fmaxf(__builtin_ldexpf(fabsf(A.scale) * 1.44269504088896341f, -up), 0x1p-126f);
+        const float by = A.scale == 0.0f ? 0.0f : A.scale < 0.0f ? -power(up) : power(up);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
             const uint32_t s = i * kWaves + wave;
-            u32x4 w[3];
+            u32x4 w[2];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const f32x4 x = q[i][e / 2] * unit;
+                const f32x4 x = q[i][e / 2] * by;
                 const Parts p = split2(x[2 * (e % 2)], x[2 * (e % 2) + 1]);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) w[k][e] = p.part[k];
+                w[0][e] = p.part[0];
+                w[1][e] = p.part[1];
             }
-            if (s < C)
-#pragma unroll
-                for (int k = 0; k < 3; ++k) S.q[k][s][lane] = w[k];
+            if (s < C) {
+                if constexpr (PACK) {
+                    S.q[0][s][lane] = n < kPacked ? w[0] : w[1];
+                } else {
+                    S.q[0][s][lane] = w[0];
+                    S.q[1][s][lane] = w[1];
+                }
+            }
         }
         __syncthreads();
+        int e = exponent(S, -90);
         State<C> st;
 #pragma unroll
         for (int j = 0; j < 2 * C; ++j) st.o[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
         st.m = -INFINITY;
-        st.l = 0.0f;
-        blocks(A, S, b, h, begin, A.pages ? (uint32_t)A.lens[b] : len, first, last, st);
-        st.l = head_sum(st.l);
-        __syncthreads();  // q is no longer read
-        if (wave >= 2) give(S, wave - 2, st);
+        st.base = st.l = 0.0f;
+        for (uint32_t at = first;;) {
+            const uint32_t count = last - at < kChunk / kBlock ? last - at : kChunk / kBlock;
+            chunk(A, S, count, c, (float)(14 - e), x0, st);
+            at += count;
+            if (at >= last) break;
+            find(A, G, b, h, at, spots);
+            __syncthreads();  // the chunk is no longer read
+            stage_rows(A, S, h, last - at, until, spots, staged);
+            __syncthreads();
+            load(A, S.row + wave * kTile, x0);
+            stage_scales(S, staged);
+            __syncthreads();
+            const int then = exponent(S, e);
+            if (then != e) {  // larger values to come: the sums' unit grows
+                const float f = power(e - then < -126 ? -126 : e - then);
+#pragma unroll
+                for (int j = 0; j < 2 * C; ++j) st.o[j] *= f;
+                st.l *= f;
+            }
+            e = then;
+        }
+        const float unit = power(e - 14);
+        __syncthreads();  // the chunk and q are no longer read
+        auto& W = shared.w;
+#pragma unroll
+        for (int j = 0; j < 2 * C; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) W.o[wave][4 * j + i][lane] = st.o[j][i] * unit;
+        W.m[wave][lane] = st.m == -INFINITY ? -INFINITY : st.base;  // in powers of two
+        W.l[wave][lane] = head_sum(st.l) * unit;
         __syncthreads();
-        if (wave < 2) take(S, wave, st);
-        __syncthreads();
-        if (wave == 1) give(S, 0, st);
-        __syncthreads();
-        if (wave != 0) return;
-        take(S, 0, st);
+        // wave i joins row i of every product
+        float m = W.m[0][lane];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) m = fmaxf(m, W.m[i][lane]);
+        float l = 0.0f, f[kWaves], o[2 * C];
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            f[i] = __builtin_amdgcn_exp2f(W.m[i][lane] - base_of(m));
+            l += W.l[i][lane] * f[i];
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * C; ++j) {
+            o[j] = W.o[0][4 * j + wave][lane] * f[0];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) o[j] += W.o[i][4 * j + wave][lane] * f[i];
+            if constexpr (PACK) o[j] = part_sum(o[j]);
+        }
         if (n >= rows) return;
-        const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const uint32_t row = 4 * g + wave;
         if (part)
-            store<kF32>(part, n * D, g, 1.0f, st);
+            store<kF32>(part, n * D, row, 1.0f, o);
         else if (G.dtype == kF32)
-            store<kF32>(A.out, (head0 + n) * D, g, inv, st);
+            store<kF32>(A.out, (head0 + n) * D, row, inv, o);
         else if (G.dtype == kF16)
-            store<kF16>(A.out, (head0 + n) * D, g, inv, st);
+            store<kF16>(A.out, (head0 + n) * D, row, inv, o);
         else
-            store<kBF16>(A.out, (head0 + n) * D, g, inv, st);
-        if (g == 0) {
+            store<kBF16>(A.out, (head0 + n) * D, row, inv, o);
+        if (g == 0 && wave == 0) {
             if (part) {
-                part[G.part_rows * D + n] = st.m;
-                part[G.part_rows * (D + 1) + n] = st.l;
+                part[G.part_rows * D + n] = m;
+                part[G.part_rows * (D + 1) + n] = l;
             } else if (A.lse)
-                A.lse[head0 + n] = lse_of(st.m, st.l);
+                A.lse[head0 + n] = lse_of(m, l);
         }
     }
 };
 
-template <int FMT, int C>
+template <int FMT, int C, bool PACK>
 __global__ __launch_bounds__(kThreads, C <= 4 ? 2 : 1) void attend_kernel(KvAttend A, Grid G) {
-    using K = Kernel<FMT, C>;
+    using K = Kernel<FMT, C, PACK>;
     __shared__ typename K::Shared S;
-    const uint32_t lanes = A.heads * G.tiles, r = blockIdx.x / lanes, h = blockIdx.x % lanes / G.tiles, z = blockIdx.x % G.tiles;
+    // the heads of a run of blocks on one XCD (workgroups go to the eight in turn): they share the lines of its L2
+    const uint32_t lanes = A.heads * G.tiles, turn = G.near ? blockIdx.x >> 3 : blockIdx.x, run = scalar(turn / lanes);
+    const uint32_t r = G.near ? run * 8u + (blockIdx.x & 7u) : run, hz = turn - run * lanes, h = scalar(hz / G.tiles), z = hz - h * G.tiles;
+    if (r >= G.R) return;
     uint32_t* info = reinterpret_cast<uint32_t*>(static_cast<float*>(A.ws) + G.info);
-    float* part = static_cast<float*>(A.ws) + (uint64_t)blockIdx.x * 2u * part_floats(G.part_rows, K::D);
     Batch batch;
-    uint32_t R = G.R;
-    int64_t at = r, end = A.seqs;  // whole sequences r, r + R, ..; or blocks
+    uint32_t end = A.seqs;  // whole sequences, or units
     if (!G.whole) {
+        batch.begin(A, G);
+        end = batch.units;
         for (uint32_t b = r; b < A.seqs; b += G.R)
-            if (blocks_of(A, b) == 0) {
+            if (blocks_of(A, G, b) == 0) {
                 empty<C>(A, G, b, h, z);
                 if (threadIdx.x == 0) info[2 * b] = info[2 * b + 1] = 0;
             }
-        batch.begin(A);
-        R = workers_of(batch.total, G.R);
-        if (r >= R) return;
-        at = share(batch.total, r, R);
-        end = share(batch.total, r + 1, R);
     }
-    while (at < end) {
-        uint32_t b = (uint32_t)at, first = 0, last = 0;
-        float* to = nullptr;
+    for (uint32_t u = r; u < end; u += G.R) {
+        Batch::Unit x = {u, 0, 0, 0, 1, 0};
         if (!G.whole) {
-            const Batch::Place p = batch.find(A, at);
-            b = p.b;
-            first = (uint32_t)(at - p.first);
-            last = end - p.first < p.count ? (uint32_t)(end - p.first) : p.count;
-            if (first != 0 || last != p.count) to = part + (first == 0 ? part_floats(G.part_rows, K::D) : 0);
-            if (first == 0 && threadIdx.x == 0) {  // the same from every key head's worker
-                info[2 * b] = r;
-                info[2 * b + 1] = worker_of(batch.total, p.first + p.count - 1, R);
+            x = batch.find(A, G, u);
+            if (x.part == 0 && threadIdx.x == 0) {  // the same from every key head's worker
+                info[2 * x.b] = x.count > 1 ? x.at : 0;
+                info[2 * x.b + 1] = x.count > 1 ? x.count : 0;
             }
         }
-        K::piece(A, G, S, b, h, z, first, last, to);
-        at += G.whole ? R : last - first;
+        K::piece(A, G, S, x.b, h, z, x.first, x.last,
+                 x.count > 1 ? static_cast<float*>(A.ws) + (uint64_t)(x.at * lanes + hz) * part_floats(G.part_rows, K::D) : nullptr);
     }
 }
 
@@ -774,18 +931,16 @@ __global__ __launch_bounds__(kJoin) void join_kernel(KvAttend A, Grid G) {
     const uint32_t b = blockIdx.x / A.q_heads, qh = blockIdx.x % A.q_heads, group = A.q_heads / A.heads;
     const uint32_t h = qh / group, z = qh % group / kHeads, row = qh % group % kHeads, lanes = A.heads * G.tiles;
     const uint32_t* info = reinterpret_cast<const uint32_t*>(static_cast<const float*>(A.ws) + G.info);
-    const uint32_t r0 = info[2 * b], r1 = info[2 * b + 1];
-    if (r0 == r1) return;
+    const uint32_t first = info[2 * b], count = info[2 * b + 1];
+    if (count == 0) return;
     const uint64_t floats = part_floats(G.part_rows, A.dim);
     const uint32_t cols = A.dim / 4u, ways = kJoin / cols, way = threadIdx.x / cols, col = threadIdx.x % cols * 4u;
     float m = -INFINITY, l = 0.0f;
     f32x4 o = {};
     if (way < ways) {
 #pragma unroll 4
-        for (uint32_t r = r0 + way; r <= r1; r += ways) {
-            // worker r0 began the sequence: its second part; the others hold it from their start: their first
-            const uint32_t block = r * lanes + h * G.tiles + z;
-            const float* p = static_cast<const float*>(A.ws) + ((uint64_t)block * 2u + (r == r0 ? 1u : 0u)) * floats;
+        for (uint32_t i = way; i < count; i += ways) {
+            const float* p = static_cast<const float*>(A.ws) + (uint64_t)((first + i) * lanes + h * G.tiles + z) * floats;
             const f32x4 v = *reinterpret_cast<const f32x4*>(p + row * A.dim + col);
             const float mp = p[G.part_rows * A.dim + row], lp = p[G.part_rows * (A.dim + 1u) + row];
             const float top = fmaxf(m, mp), base = base_of(top);
@@ -841,13 +996,13 @@ void with_steps(uint32_t c, F&& f) {
 uint32_t split(uint32_t q_heads, uint32_t heads, int cus) {
     const uint32_t lanes = heads * ((q_heads / heads + kHeads - 1) / kHeads);
     const uint32_t r = workers(cus) / lanes;
-    return r ? r : 1;
+    return r >= 8u ? r / 8u * 8u : r ? r : 1;
 }
 
-// Floats of all workers' parts.
+// Floats of all parts: a sequence in more than one has fewer than 2 n / per of them, and per is at least T / (2 R).
 uint64_t part_total(uint32_t q_heads, uint32_t heads, uint32_t dim, int cus) {
     const uint64_t lanes = (uint64_t)heads * ((q_heads / heads + kHeads - 1) / kHeads);
-    return split(q_heads, heads, cus) * lanes * 2u * part_floats(part_rows(q_heads, heads), dim);
+    return split(q_heads, heads, cus) * lanes * 4u * part_floats(part_rows(q_heads, heads), dim);
 }
 
 }  // namespace
@@ -858,12 +1013,16 @@ size_t kv_attend_ws_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint3
 
 hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, hipStream_t st) {
     Grid G;
-    G.tiles = (A.q_heads / A.heads + kHeads - 1) / kHeads;
+    G.group = A.q_heads / A.heads;
+    G.tiles = (G.group + kHeads - 1) / kHeads;
     G.part_rows = part_rows(A.q_heads, A.heads);
     G.dtype = dtype;
     G.info = part_total(A.q_heads, A.heads, A.dim, cus);
     // one block a sequence at most: nothing to split
     const uint64_t most = (uint64_t)(A.pages ? A.budget : A.max_pages) * A.page_len;
+    G.most = (uint32_t)(most < 0x7FFFFFFFu ? most : 0x7FFFFFFFu);
+    G.shift = A.page_len == 1 || A.page_len >= 0x80000000u ? 0 : 32 - (uint32_t)__builtin_clz(A.page_len - 1);  // of 2^shift >= page_len
+    G.magic = A.page_len >= 0x80000000u ? 0 : (uint32_t)((((uint64_t)1 << (31 + G.shift)) + A.page_len - 1) / A.page_len);
     G.whole = !A.ws || most <= kBlock || (uint64_t)A.seqs * A.q_heads >= 0x400000u;
     const uint32_t lanes = A.heads * G.tiles;
     G.R = split(A.q_heads, A.heads, cus);
@@ -871,12 +1030,21 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
         const uint32_t limit = 0x800000u / lanes;  // workgroups of 256 lanes, which are counted in 32 bits
         G.R = A.seqs < limit ? A.seqs : limit ? limit : 1;
     }
+    G.near = G.R >= 8u;
+    const uint32_t grid = (G.near ? (G.R + 7u) / 8u * 8u : G.R) * lanes;
     with_steps(A.dim / 32u, [&](auto c_) {
         constexpr int C = decltype(c_)::value;
-        if (format == kKvE4M3)
-            attend_kernel<kKvE4M3, C><<<G.R * lanes, kThreads, 0, st>>>(A, G);
+        auto launch = [&](auto pack_) {
+            constexpr bool PACK = decltype(pack_)::value;
+            if (format == kKvE4M3)
+                attend_kernel<kKvE4M3, C, PACK><<<grid, kThreads, 0, st>>>(A, G);
+            else
+                attend_kernel<kKvMXFP4, C, PACK><<<grid, kThreads, 0, st>>>(A, G);
+        };
+        if (G.group <= kPacked)
+            launch(std::true_type{});
         else
-            attend_kernel<kKvMXFP4, C><<<G.R * lanes, kThreads, 0, st>>>(A, G);
+            launch(std::false_type{});
     });
     if (!G.whole) join_kernel<<<A.seqs * A.q_heads, kJoin, 0, st>>>(A, G);
     return hipGetLastError();

@@ -642,9 +642,12 @@ int rz_kv_plan(const int32_t* lens, const int32_t* keep, const int32_t* offsets,
  * does anything that the cache holds in them or behind a sequence's end.  A
  * row without a position, or with all its scores -inf, gives zeros and
  * lse -inf.  Otherwise, for n positions and gamma_t = t eps / (1 - t eps), eps = 2^-24,
- *   |out - exact| <= (2.5 e + gamma_{8 n + 64}) sum_p w_p |v_p| + rounding to dtype,
- *   e = max_p (gamma_{8 dim} scale sum_d |q_d k_pd| + (4 |scale q . k_p| + 8) eps)
- * where no sum overflows and q and the rows' scales are at least 2^-100 or 0.
+ *   |out - exact| <= (2.5 e + gamma_{8 n + 64}) sum_p w_p |v_p| + n 2^-38 max |v| + rounding to dtype,
+ *   e = max_p (gamma_{8 dim} scale sum_d |q_d k_pd| + 2^-39 scale max |q| sum_d |k_pd| + (4 |scale q . k_p| + 12) eps)
+ * where no sum overflows, q and the rows' scales are 0 or between 2^-100 and
+ * 2^90 in size, and rows are as rz_kv_cache_write leaves them.  A NaN or an
+ * infinity in q or a key gives a NaN or takes no weight, in a value NaN or an
+ * infinity in its columns (E4M3: an infinite scale, in its row's).
  * Sums have a fixed order for given sizes and workspace.  seqs == 0 is a no-op.
  */
 size_t rz_kv_attention_workspace_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint32_t dim);

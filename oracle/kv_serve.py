@@ -73,15 +73,23 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None):
     """(out [seqs][q_heads][dim], lse [seqs][q_heads], bound of out, bound of
     lse) in float64, for the caches' values k and v (values()).
 
-    The kernels' errors, u = 2^-24.  A score is a sum of dim exact products of
-    q * scale (2 u: the constant's rounding and the product's), held as up to
-    three parts, with a row's scale (2 u: as read, and as multiplied); it
-    passes at most 3 dim additions of 2 u each (truncation): it errs by at most
-    gamma_{8 dim} sum |scale q k|.  The exponential's argument is rounded (u
-    |s|, twice: base change and difference), the exponential errs by 1 ulp: e
-    covers them as a weight's relative error.  Weights and their sum pass at
-    most 3 additions and 1 rescaling (2 u each) a position and 64 in the joins:
-    gamma_{8 n + 64}.  Numerator and denominator each err by (e^e - 1) <= 1.25 e."""
+    The kernels' errors, u = 2^-24.  q and the weights are held as two fp16
+    parts, the second the first's rounding, rounded: 2^-11 of 2^-11, 4 u in all,
+    where neither is subnormal.  Subnormal parts err by 2^-25 at most: q is
+    scaled so that its largest magnitude is at least 2^14, hence 2^-39 of it;
+    a weight w <= 1 is taken times 2^14 times its row's scale over a power of
+    two at most twice the largest scale, hence 2^-38 of the largest value (in a
+    row as it is written the largest code is the format's).  A score is a sum
+    of 2 dim exact products and as many additions of 2 u each (truncation),
+    with a row's scale (2 u: as read, and as multiplied) and the rounded
+    constant (u): it errs by at most gamma_{4 dim + 10}, and so gamma_{8 dim},
+    times sum |scale q k|.  The exponential's argument is rounded (u |s|,
+    twice: the product with the constant and the difference; twice more in a
+    join), the exponential errs by 1 ulp, and a weight's scale and parts by
+    6 u: e covers them as a weight's relative error.  Weights and their sum
+    pass at most 3 additions and 1 rescaling (2 u each) a position and 64 in
+    the joins: gamma_{8 n + 64}.  Numerator and denominator each err by
+    (e^e - 1) <= 1.25 e."""
     seqs, heads_q, dim = q.shape
     heads = k.shape[1]
     group = heads_q // heads
@@ -106,8 +114,8 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None):
                     w /= w.sum()
                     out[b, g] = w @ vv
                     far = np.max(np.abs(s)[np.isfinite(s)], initial=0.0)
-                    e = gamma(8 * dim) * (np.abs(kk) @ np.abs(x)).max() + (4 * far + 8) * U
-                    tol[b, g] = (2.5 * e + gamma(8 * len(at) + 64)) * (w @ np.abs(vv)) + 1e-37
+                    e = gamma(8 * dim) * (np.abs(kk) @ np.abs(x)).max() + 2.0 ** -39 * np.abs(x).max() * np.abs(kk).sum(1).max() + (4 * far + 12) * U
+                    tol[b, g] = (2.5 * e + gamma(8 * len(at) + 64)) * (w @ np.abs(vv)) + len(at) * 2.0 ** -38 * np.abs(vv).max() + 1e-37
                     ltol[b, g] = 1.25 * e + gamma(8 * len(at) + 64) + 4 * U * abs(lse[b, g])
     return out, lse, tol, ltol
 
