@@ -100,6 +100,18 @@ __device__ __forceinline__ uint32_t wave_total(uint32_t v) {
     return wave_reduce(v, [](uint32_t a, uint32_t b) { return a + b; });
 }
 
+// Sum of the values of the lanes up to and with this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    // lanes 1, 2, 4, 8 before in a row of 16, then the last lane of the row and of the half before
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
+    return v;
+}
+
 // The batch as units of work, as every wave finds it for itself: sequence b of
 // n blocks is ceil(n / per) units of nearly equal size.  Sequences are looked
 // at 64 at a time, a lane each.
@@ -123,17 +135,9 @@ struct Batch {
         blocks = b < A.seqs ? blocks_of(A, G, b) : 0;
     }
     __device__ __forceinline__ void scan() {
-        const uint32_t lane = threadIdx.x % kWave, n = parts(blocks);
-        sum = n;
-        split = n > 1 ? n : 0;
-#pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) {
-            const uint32_t o = (uint32_t)__shfl_up((int)sum, off, kWave), u = (uint32_t)__shfl_up((int)split, off, kWave);
-            if (lane >= off) {
-                sum += o;
-                split += u;
-            }
-        }
+        const uint32_t n = parts(blocks);
+        sum = wave_scan(n);
+        split = wave_scan(n > 1 ? n : 0);
     }
     __device__ __forceinline__ void begin(const KvAttend& A, const Grid& G) {
         look(A, G);
@@ -548,11 +552,18 @@ struct Kernel {
         return (int)scalar((uint32_t)(x > e ? x : e));
     }
 
+    // kRow as a factor that the compiler does not know: one multiply-add an address, not a shift and two additions.
+    static __device__ __forceinline__ uint32_t row_bytes() {
+        uint32_t x = kRow;
+        asm("" : "+s"(x));
+        return x;
+    }
+
     // A tile's rows as they are loaded; `row` its 32 rows of the cache.
     static __device__ __forceinline__ void load_keys(const KvAttend& A, const uint32_t* row, uint32_t (&k)[2][kKWords<FMT, C>]) {
         const uint32_t n = threadIdx.x % 16, g = threadIdx.x % kWave / 16;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) load_k<FMT, C>(A.codes[0] + (uint64_t)row[16 * t + n] * kRow, g, k[t]);
+        for (int t = 0; t < 2; ++t) load_k<FMT, C>(A.codes[0] + (uint64_t)row[16 * t + n] * row_bytes(), g, k[t]);
     }
     static __device__ __forceinline__ void load_values(const KvAttend& A, const uint32_t* row, uint32_t (&v)[8][kVWords<FMT, C>]) {
         const uint32_t n = threadIdx.x % 16, g = threadIdx.x % kWave / 16;
@@ -560,7 +571,7 @@ struct Kernel {
         for (int t = 0; t < 2; ++t) {
             const u32x4 at = *reinterpret_cast<const u32x4*>(row + 16 * t + 4 * g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_v<FMT, C>(A.codes[1] + (uint64_t)at[i] * kRow, n, v[4 * t + i]);
+            for (int i = 0; i < 4; ++i) load_v<FMT, C>(A.codes[1] + (uint64_t)at[i] * row_bytes(), n, v[4 * t + i]);
         }
     }
 
@@ -903,11 +914,6 @@ __global__ __launch_bounds__(kThreads, C <= 4 ? 2 : 1) void attend_kernel(KvAtte
     if (!G.whole) {
         batch.begin(A, G);
         end = batch.units;
-        for (uint32_t b = r; b < A.seqs; b += G.R)
-            if (blocks_of(A, G, b) == 0) {
-                empty<C>(A, G, b, h, z);
-                if (threadIdx.x == 0) info[2 * b] = info[2 * b + 1] = 0;
-            }
     }
     for (uint32_t u = r; u < end; u += G.R) {
         Batch::Unit x = {u, 0, 0, 0, 1, 0};
@@ -921,12 +927,18 @@ __global__ __launch_bounds__(kThreads, C <= 4 ? 2 : 1) void attend_kernel(KvAtte
         K::piece(A, G, S, x.b, h, z, x.first, x.last,
                  x.count > 1 ? static_cast<float*>(A.ws) + (uint64_t)(x.at * lanes + hz) * part_floats(G.part_rows, K::D) : nullptr);
     }
+    if (!G.whole)
+        for (uint32_t b = r; b < A.seqs; b += G.R)
+            if (blocks_of(A, G, b) == 0) {
+                empty<C>(A, G, b, h, z);
+                if (threadIdx.x == 0) info[2 * b] = info[2 * b + 1] = 0;
+            }
 }
 
 // Joins the parts of a sequence that several workers hold: a workgroup a query
 // head.  Four columns a lane, and the parts shared among the rows of lanes,
 // each with a running maximum of its own.
-constexpr int kJoin = 1024;
+template <int kJoin>
 __global__ __launch_bounds__(kJoin) void join_kernel(KvAttend A, Grid G) {
     const uint32_t b = blockIdx.x / A.q_heads, qh = blockIdx.x % A.q_heads, group = A.q_heads / A.heads;
     const uint32_t h = qh / group, z = qh % group / kHeads, row = qh % group % kHeads, lanes = A.heads * G.tiles;
@@ -958,10 +970,12 @@ __global__ __launch_bounds__(kJoin) void join_kernel(KvAttend A, Grid G) {
     __syncthreads();
     if (way != 0) return;
     float top = m;
+#pragma unroll 8
     for (uint32_t w = 1; w < ways; ++w) top = fmaxf(top, m_of[w * cols + threadIdx.x]);
     const float base = base_of(top);
     o = (f32x4){};
     l = 0.0f;
+#pragma unroll 8
     for (uint32_t w = 0; w < ways; ++w) {
         const float e = __builtin_amdgcn_exp2f(m_of[w * cols + threadIdx.x] - base);
         o += o_of[w * cols + threadIdx.x] * e;
@@ -1046,7 +1060,13 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
         else
             launch(std::false_type{});
     });
-    if (!G.whole) join_kernel<<<A.seqs * A.q_heads, kJoin, 0, st>>>(A, G);
+    if (!G.whole) {
+        // few sequences are in many parts each
+        if (A.seqs < 8u)
+            join_kernel<1024><<<A.seqs * A.q_heads, 1024, 0, st>>>(A, G);
+        else
+            join_kernel<256><<<A.seqs * A.q_heads, 256, 0, st>>>(A, G);
+    }
     return hipGetLastError();
 }
 
