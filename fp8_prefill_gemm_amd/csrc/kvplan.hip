@@ -7,8 +7,11 @@
 // stack[count + given - 1 - i], so two prefix sums over the sequences say
 // where every page goes, in any order of execution.
 //
-// One workgroup does the sums and moves the pages; where a step has more
-// tokens than it serves well, a second launch gives every token its slot.
+// A few hundred bytes are read and written, so what counts is the chain of
+// loads and barriers.  One workgroup does the sums, a lane a sequence, and for
+// a decoding step everything else; where a step has more tokens than its
+// lanes serve in four turns, a second launch gives every token its slot and
+// writes the new pages' numbers as it meets their first tokens.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -19,44 +22,51 @@ namespace rz {
 namespace {
 
 constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / kWave;
+constexpr uint32_t kOneLaunch = 4u * kThreads;  // tokens
 
-// What a sequence does in this step.
+// What the second launch (and the slots of the first) know of a sequence.
 struct Row {
-    int64_t first;  // position of its first new token
-    int64_t held, need;
-    bool ok;
-    __device__ __forceinline__ Row(const KvPlan& A, uint32_t b) {
-        const int64_t len = A.lens[b], keep = A.keep ? A.keep[b] : len;
-        const int64_t fresh = (int64_t)A.offsets[b + 1] - A.offsets[b];
-        first = keep;
-        ok = keep >= 0 && keep <= len && fresh >= 0 && keep + fresh <= INT32_MAX;
-        held = ok ? (len + A.page_len - 1) / A.page_len : 0;
-        need = ok ? (keep + fresh + A.page_len - 1) / A.page_len : 0;
-        ok = ok && held <= A.max_pages && need <= A.max_pages;
-    }
-    __device__ __forceinline__ int64_t give() const { return ok && held > need ? held - need : 0; }
-    __device__ __forceinline__ int64_t take() const { return ok && need > held ? need - held : 0; }
+    int32_t first;  // position of its first new token, -1: refused
+    uint32_t held;  // pages
+    uint32_t top;   // place of its first new page in the stack; the next ones lie below
 };
 
-// Sum of v over the threads before this one, and over all of them.
+// Saturating sums: page counts of any input stay in order, and none wraps.
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// Sums over the lanes before this one, and over all of them, of two values.
 struct Scan {
-    int64_t before, all;
+    uint32_t before[2], all[2];
 };
-__device__ __forceinline__ Scan scan(int64_t v, int64_t* smem) {
+__device__ __forceinline__ Scan scan(uint32_t x, uint32_t y, uint32_t (*smem)[2]) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    int64_t sum = v;
+    uint32_t v[2] = {x, y};
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const int64_t o = __shfl_up(sum, off, kWave);
-        if (lane >= off) sum += o;
+    for (int c = 0; c < 2; ++c) {  // lanes 1, 2, 4, 8 before in a row of 16, then the last lane of the row and of the half before
+        v[c] = add(v[c], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[c], 0x111, 0xF, 0xF, true));
+        v[c] = add(v[c], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[c], 0x112, 0xF, 0xF, true));
+        v[c] = add(v[c], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[c], 0x114, 0xF, 0xF, true));
+        v[c] = add(v[c], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[c], 0x118, 0xF, 0xF, true));
+        v[c] = add(v[c], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[c], 0x142, 0xA, 0xF, false));
+        v[c] = add(v[c], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[c], 0x143, 0xC, 0xF, false));
     }
-    if (lane == kWave - 1) smem[wave] = sum;
+    Scan s = {{0, 0}, {0, 0}};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t up = (uint32_t)__shfl_up((int)v[c], 1, kWave);
+        s.before[c] = lane ? up : 0;
+        if (lane == kWave - 1) smem[wave][c] = v[c];
+    }
     __syncthreads();
-    Scan s = {sum - v, 0};
-    for (int i = 0; i < kThreads / kWave; ++i) {
-        if (i < wave) s.before += smem[i];
-        s.all += smem[i];
-    }
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t n = smem[i][c];
+            if (i < wave) s.before[c] = add(s.before[c], n);
+            s.all[c] = add(s.all[c], n);
+        }
     __syncthreads();
     return s;
 }
@@ -64,107 +74,130 @@ __device__ __forceinline__ Scan scan(int64_t v, int64_t* smem) {
 // Calls f(lane, n of that lane) for each lane whose n is not 0, with the whole
 // wave: f may shuffle before it loops.
 template <typename F>
-__device__ __forceinline__ void each(int64_t n, F&& f) {
+__device__ __forceinline__ void each(uint32_t n, F&& f) {
     for (uint64_t todo = __ballot(n > 0); todo; todo &= todo - 1) {
         const int l = __ffsll((unsigned long long)todo) - 1;
-        f(l, __shfl(n, l, kWave));
+        f(l, (uint32_t)__shfl((int)n, l, kWave));
     }
 }
 
-// The slot of token t: `first` holds each sequence's first new position (-1: refused).
-__device__ __forceinline__ int64_t slot_of(const KvPlan& A, const int32_t* first, uint32_t t) {
+// A step's demand of sequence b.
+struct Step {
+    int32_t len = 0;
+    int64_t first = 0, then = 0;  // tokens kept, and with the new ones
+    uint32_t held = 0, need = 0;
+    bool ok = false;
+    __device__ __forceinline__ Step(const KvPlan& A, uint32_t b) {
+        if (b >= A.seqs) return;
+        len = A.lens[b];
+        first = A.keep ? A.keep[b] : len;
+        const int64_t fresh = (int64_t)A.offsets[b + 1] - A.offsets[b];
+        then = first + fresh;
+        ok = first >= 0 && first <= len && fresh >= 0 && then <= INT32_MAX;
+        held = ok ? ((uint32_t)len + (A.page_len - 1ull)) / A.page_len : 0;
+        need = ok ? ((uint32_t)then + (A.page_len - 1ull)) / A.page_len : 0;
+        ok = ok && held <= A.max_pages && need <= A.max_pages;
+    }
+    __device__ __forceinline__ uint32_t give() const { return ok && held > need ? held - need : 0; }
+    __device__ __forceinline__ uint32_t take() const { return ok && need > held ? need - held : 0; }
+};
+
+// The slot of token t, by its sequence's row; FILL: a new page's number is
+// taken from the stack and, at the page's first token, written to the table.
+template <bool FILL, typename R>
+__device__ __forceinline__ int64_t slot_of(const KvPlan& A, const R* rows, uint32_t t) {
     if (A.seqs == 0 || (int64_t)t < A.offsets[0] || (int64_t)t >= A.offsets[A.seqs]) return -1;
     uint32_t lo = 0, hi = A.seqs;  // offsets[lo] <= t < offsets[hi]
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) >> 1;
         if ((int64_t)t >= A.offsets[mid]) lo = mid; else hi = mid;
     }
-    if (first[lo] < 0) return -1;
-    const uint64_t pos = (uint64_t)first[lo] + (t - (uint32_t)A.offsets[lo]);
-    if (pos / A.page_len >= A.max_pages) return -1;  // offsets that decrease
-    const int64_t page = A.page_table[(uint64_t)lo * A.max_pages + pos / A.page_len];
-    return page < 0 ? -1 : page * A.page_len + (int64_t)(pos % A.page_len);
+    const Row row = rows[lo];
+    if (row.first < 0) return -1;
+    const uint64_t pos = (uint64_t)(uint32_t)row.first + (t - (uint32_t)A.offsets[lo]), page = pos / A.page_len;
+    if (page >= A.max_pages) return -1;  // offsets that decrease
+    const uint32_t at = (uint32_t)(pos - page * A.page_len);
+    int32_t* entry = A.page_table + (uint64_t)lo * A.max_pages + page;
+    int64_t id;
+    if (FILL && page >= row.held) {
+        const uint64_t below = page - row.held;
+        if (below > row.top || row.top - below >= A.num_pages) return -1;  // offsets that decrease
+        id = A.free_pages[row.top - below];
+        if (at == 0) *entry = (int32_t)id;
+    } else {
+        id = *entry;
+    }
+    return id < 0 ? -1 : id * A.page_len + at;
 }
 
-__global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, int32_t* first, bool with_slots) {
-    __shared__ int64_t smem[kThreads / kWave];
+__global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, bool one) {
+    __shared__ uint32_t smem[kWaves][2];
+    __shared__ uint32_t used_of;
     const int lane = threadIdx.x & (kWave - 1);
     const uint32_t rounds = (A.seqs + kThreads - 1) / kThreads;
-    int64_t have = A.free_count[0];
-    have = have < 0 ? 0 : have > A.num_pages ? A.num_pages : have;
-    for (uint32_t r = 0; r < rounds; ++r) {
-        const uint32_t b = r * kThreads + threadIdx.x, wave0 = b & ~(kWave - 1u);
-        int64_t give = 0, need = 0;
-        if (b < A.seqs) {
-            const Row row(A, b);
-            give = row.give();
-            need = row.need;
-        }
-        const Scan s = scan(give, smem);
-        const int64_t at = have + s.before;
-        each(give, [&](int l, int64_t n) {
-            const int64_t to = __shfl(at, l, kWave);
-            const int32_t* from = A.page_table + (uint64_t)(wave0 + l) * A.max_pages + __shfl(need, l, kWave);
-            for (int64_t i = lane; i < n; i += kWave)
-                if (to + i < A.num_pages) A.free_pages[to + i] = from[i];
+    // pages are moved here unless every new token is the second launch's (tokens that it does not know have pages too)
+    const bool fill = one || (A.seqs != 0 && A.offsets[A.seqs] > (int64_t)A.tokens);
+    const int32_t count = A.free_count[0];
+    uint32_t have = count < 0 ? 0 : (uint32_t)count > A.num_pages ? A.num_pages : (uint32_t)count;
+    if (threadIdx.x == 0) used_of = 0;
+    Step step(A, threadIdx.x);
+    uint32_t before_take = 0, taken = 0;
+    for (uint32_t r = 0; r < rounds; ++r) {  // one for up to 1024 sequences
+        if (rounds > 1) step = Step(A, r * kThreads + threadIdx.x);
+        const uint32_t give = step.give(), wave0 = (r * kThreads + threadIdx.x) & ~(kWave - 1u);
+        const Scan s = scan(give, rounds > 1 ? 0 : step.take(), smem);
+        before_take = s.before[1];
+        const uint32_t at = add(have, s.before[0]);
+        each(give, [&](int l, uint32_t n) {
+            const uint32_t to = (uint32_t)__shfl((int)at, l, kWave);
+            const int32_t* from = A.page_table + (uint64_t)(wave0 + l) * A.max_pages + (uint32_t)__shfl((int)step.need, l, kWave);
+            for (uint32_t i = lane; i < n && add(to, i) < A.num_pages; i += kWave) A.free_pages[to + i] = from[i];
         });
-        have += s.all;
+        have = add(have, s.all[0]);
     }
     have = have > A.num_pages ? A.num_pages : have;
     __syncthreads();  // what was given may be taken below
-    int64_t taken = 0, used = 0;
     for (uint32_t r = 0; r < rounds; ++r) {
         const uint32_t b = r * kThreads + threadIdx.x, wave0 = b & ~(kWave - 1u);
-        int64_t take = 0, held = 0;
-        bool ok = false;
-        int64_t len = 0, then = 0, pos = 0;
-        if (b < A.seqs) {
-            const Row row(A, b);
-            take = row.take();
-            held = row.held;
-            ok = row.ok;
-            pos = row.first;
-            len = A.lens[b];
-            then = row.first + A.offsets[b + 1] - A.offsets[b];
+        if (rounds > 1) {
+            step = Step(A, b);
+            const Scan s = scan(step.take(), 0, smem);
+            before_take = add(taken, s.before[0]);
+            taken = add(taken, s.all[0]);
         }
-        const Scan s = scan(take, smem);
-        const int64_t before = taken + s.before;
-        const bool fits = ok && (take == 0 || before + take <= have);
+        const uint32_t take = step.take(), after = add(before_take, take);
+        const bool fits = step.ok && (take == 0 || after <= have);
         if (b < A.seqs) {
-            first[b] = fits ? (int32_t)pos : -1;
-            A.lens_out[b] = (int32_t)(fits ? then : len);
+            rows[b] = {fits ? (int32_t)step.first : -1, step.held, have - 1 - before_take};
+            A.lens_out[b] = (int32_t)(fits ? step.then : step.len);
         }
-        each(fits ? take : 0, [&](int l, int64_t n) {
-            const int32_t* from = A.free_pages + (have - 1 - __shfl(before, l, kWave));
-            int32_t* to = A.page_table + (uint64_t)(wave0 + l) * A.max_pages + __shfl(held, l, kWave);
-            for (int64_t i = lane; i < n; i += kWave) to[i] = from[-i];
+        if (fits && take) atomicMax(&used_of, after);
+        each(fits && fill ? take : 0, [&](int l, uint32_t n) {
+            const int32_t* from = A.free_pages + (have - 1 - (uint32_t)__shfl((int)before_take, l, kWave));
+            int32_t* to = A.page_table + (uint64_t)(wave0 + l) * A.max_pages + (uint32_t)__shfl((int)step.held, l, kWave);
+            for (uint32_t i = lane; i < n; i += kWave) to[i] = from[-(int64_t)i];
         });
-        const Scan u = scan(fits ? take : 0, smem);
-        taken += s.all;
-        used += u.all;
     }
     __syncthreads();
-    if (threadIdx.x == 0) A.count_out[0] = (int32_t)(have - used);
-    if (with_slots)
-        for (uint32_t t = threadIdx.x; t < A.tokens; t += kThreads) A.slots[t] = slot_of(A, first, t);
+    if (threadIdx.x == 0) A.count_out[0] = (int32_t)(have - used_of);
+    if (one)
+        for (uint32_t t = threadIdx.x; t < A.tokens; t += kThreads) A.slots[t] = slot_of<false>(A, rows, t);
 }
 
-__global__ __launch_bounds__(256) void slots_kernel(KvPlan A, const int32_t* first) {
+__global__ __launch_bounds__(256) void slots_kernel(KvPlan A, const Row* rows) {
     const uint32_t t = blockIdx.x * 256u + threadIdx.x;
-    if (t < A.tokens) A.slots[t] = slot_of(A, first, t);
+    if (t < A.tokens) A.slots[t] = slot_of<true>(A, rows, t);
 }
-
-constexpr uint32_t kOneLaunch = 4096;  // tokens
 
 }  // namespace
 
-size_t kv_plan_ws_bytes(uint32_t seqs, uint32_t) { return (size_t)seqs * 4u; }
+size_t kv_plan_ws_bytes(uint32_t seqs, uint32_t) { return (size_t)seqs * sizeof(Row); }
 
 hipError_t launch_kv_plan(const KvPlan& A, hipStream_t st) {
-    int32_t* first = static_cast<int32_t*>(A.ws);
+    Row* rows = static_cast<Row*>(A.ws);
     const bool one = A.tokens <= kOneLaunch;
-    plan_kernel<<<1, kThreads, 0, st>>>(A, first, one);
-    if (!one) slots_kernel<<<(A.tokens + 255u) / 256u, 256, 0, st>>>(A, first);
+    plan_kernel<<<1, kThreads, 0, st>>>(A, rows, one);
+    if (!one) slots_kernel<<<(A.tokens + 255u) / 256u, 256, 0, st>>>(A, rows);
     return hipGetLastError();
 }
 

@@ -3,13 +3,15 @@
 // A page and head's bounds are the largest and smallest value of each column
 // over the page's filled rows, as int8 multiples of one scale, rounded away
 // from the middle; a query is held as int8 too, so that
-//   sum_d max(n_d hi_d, n_d lo_d)
-// is a sum of whole numbers (below 2^24 for 512 columns: exact in fp32 as
-// well), the same in any order, and the choice by it has no rounding to
-// depend on.  To its roundings it is an upper bound of n . k for every key k
-// of the page.
+//   sum_d max(n_d hi_d, n_d lo_d) = sum_d max(n_d, 0) hi_d + min(n_d, 0) lo_d
+// is a product of whole numbers on the matrix cores (below 2^24 for 512
+// columns: exact in fp32 as well), the same in any order, and the choice by it
+// has no rounding to depend on.  To its roundings it is an upper bound of n . k
+// for every key k of the page.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "mx_device.h"
 #include "rz_device.h"
@@ -19,44 +21,34 @@ namespace rz {
 namespace {
 using namespace mx;
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kThreads = 256;
 constexpr float kTiny = 0x1p-100f;
 
-// a / 127 and 127 / a of a largest magnitude a.
+// What a largest magnitude a stands for: 1 where there is next to nothing.
 __device__ __forceinline__ float sized(float a) { return a >= kTiny ? a : 1.0f; }
 
-// One wave a (token, head): the first token of a page in `slots` takes the
-// page, eight columns a lane.
+// ---- bounds
+
+// Eight fp32 values of a row of keys, as the cache's read gives them.
 template <int FMT>
-__global__ __launch_bounds__(kThreads) void bounds_kernel(KvBounds A) {
-    const uint64_t item = (uint64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
-    const uint32_t lane = threadIdx.x % kWave;
-    if (item >= (uint64_t)A.tokens * A.heads) return;
-    const uint32_t t = (uint32_t)(item / A.heads), h = (uint32_t)(item % A.heads);
-    auto page_of = [&](uint32_t i) -> int64_t {
-        const int64_t s = A.slots[i];
-        return s < 0 || (uint64_t)s >= A.num_slots ? -1 : s / A.page_len;
-    };
-    const int64_t page = page_of(t);
-    if (page < 0 || (uint64_t)page >= A.num_pages || (t > 0 && page_of(t - 1) == page)) return;
-    uint32_t filled = 0;
-    for (uint32_t i = t; i < A.tokens && page_of(i) == page; ++i) {
-        const uint32_t at = (uint32_t)(A.slots[i] % A.page_len) + 1;
-        filled = filled > at ? filled : at;
-    }
-    const bool live = lane * 8u < A.dim;
-    float hi[8], lo[8];
-    bool fine = true;
-    for (int i = 0; i < 8; ++i) {
-        hi[i] = -INFINITY;
-        lo[i] = INFINITY;
-    }
-    for (uint32_t r = 0; r < filled && live; ++r) {
-        const uint64_t row = ((uint64_t)page * A.page_len + r) * A.heads + h;
-        float x[8];
+struct Eight {
+    u32x2 w;
+    uint32_t sc;  // the row's fp32 scale, or the block's byte
+    __device__ __forceinline__ void load(const KvBounds& A, uint64_t row, uint32_t part) {
         if constexpr (FMT == kKvE4M3) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(A.codes + row * A.dim + lane * 8u);
-            const float s = static_cast<const float*>(A.scales)[row];
+            w = *reinterpret_cast<const u32x2*>(A.codes + row * A.dim + part * 8u);
+            sc = static_cast<const uint32_t*>(A.scales)[row];
+        } else {
+            w.x = *reinterpret_cast<const uint32_t*>(A.codes + row * (A.dim / 2u) + part * 4u);
+            sc = static_cast<const uint8_t*>(A.scales)[row * (A.dim / 32u) + part / 4u];
+        }
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        if constexpr (FMT == kKvE4M3) {
+            const float s = __uint_as_float(sc);
+#pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
                 const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
@@ -66,40 +58,133 @@ __global__ __launch_bounds__(kThreads) void bounds_kernel(KvBounds A) {
                 x[4 * j + 3] = b.y * s;
             }
         } else {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(A.codes + row * (A.dim / 2u) + lane * 4u);
-            decode8(w, x, cvt_scale(static_cast<const uint8_t*>(A.scales)[row * (A.dim / 32u) + lane / 4u]));
-        }
-        for (int i = 0; i < 8; ++i) {
-            fine = fine && fabsf(x[i]) < INFINITY;
-            hi[i] = fmaxf(hi[i], x[i]);
-            lo[i] = fminf(lo[i], x[i]);
+            decode8(w.x, x, cvt_scale(sc));
         }
     }
-    float a = 0.0f;
-    if (live)
-        for (int i = 0; i < 8; ++i) a = fmaxf(a, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
-    for (int off = 1; off < kWave; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));
-    fine = __ballot(!fine) == 0;
-    a = sized(a);
-    const float inv = 127.0f / a;
-    const uint64_t dst = (uint64_t)page * A.heads + h;
-    if (live) {
-        u32x2 up, down;
-        for (int j = 0; j < 2; ++j) {
-            uint32_t u = 0, d = 0;
-            for (int i = 0; i < 4; ++i) {
-                const float p = fine ? ceilf(hi[4 * j + i] * inv) : 127.0f, n = fine ? floorf(lo[4 * j + i] * inv) : -127.0f;
-                u |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(p, -127.0f, 127.0f) & 255u) << (8 * i);
-                d |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(n, -127.0f, 127.0f) & 255u) << (8 * i);
+};
+
+// A workgroup takes `per` consecutive tokens and `wide` heads: a token whose
+// predecessor lies in another page leads, and its page's rows (up to the last
+// token of the page in `slots`) are shared among the rows of lanes, eight
+// columns of a head a lane (L lanes a head), kTurn rows a lane in flight.
+constexpr int kTurn = 4;
+constexpr uint32_t kMaxPer = 64;
+
+template <int FMT, int L>
+__global__ __launch_bounds__(kThreads) void bounds_kernel(KvBounds A, uint32_t per, uint32_t wide, uint32_t groups) {
+    __shared__ int64_t slot_of[kMaxPer + 1];  // of the token before, then of these
+    __shared__ float hi_of[kThreads][9], lo_of[kThreads][9];
+    __shared__ uint32_t filled_of;
+    const uint32_t t0 = blockIdx.x / groups * per, head0 = blockIdx.x % groups * wide, lane = threadIdx.x % kWave;
+    const uint32_t width = wide * L, sub = threadIdx.x % width, way = threadIdx.x / width, ways = kThreads / width;
+    const uint32_t head = head0 + sub / L, part = sub % L;
+    const bool live = way < ways && head < A.heads && part * 8u < A.dim;
+    if (threadIdx.x <= per) {
+        const int64_t t = (int64_t)t0 + threadIdx.x - 1;
+        const int64_t s = t >= 0 && t < A.tokens ? A.slots[t] : -1;
+        slot_of[threadIdx.x] = s < 0 || (uint64_t)s >= A.num_slots ? -1 : s;
+    }
+    __syncthreads();
+    for (uint32_t i = 0; i < per; ++i) {  // uniform: every lane sees the same slots
+        const int64_t s = slot_of[i + 1], before = slot_of[i];
+        if (s < 0) continue;
+        const uint64_t page = (uint64_t)s / A.page_len;
+        if (page >= A.num_pages || (before >= 0 && (uint64_t)before / A.page_len == page)) continue;
+        // how far the page is filled: the largest of the tokens that follow each other in it
+        __syncthreads();
+        if (threadIdx.x < kWave) {
+            uint32_t top = 0;
+            for (uint64_t t = (uint64_t)t0 + i;; t += kWave) {
+                const int64_t x = t + lane < A.tokens ? A.slots[t + lane] : -1;
+                const bool in = x >= 0 && (uint64_t)x < A.num_slots && (uint64_t)x / A.page_len == page;
+                const uint64_t out = ~__ballot(in);
+                const uint32_t n = out ? (uint32_t)__ffsll((unsigned long long)out) - 1 : kWave;  // lanes that follow on
+                const uint32_t at = lane < n ? (uint32_t)((uint64_t)x - page * A.page_len) + 1 : 0;
+                top = top > at ? top : at;
+                if (n < kWave) break;
             }
-            up[j] = u;
-            down[j] = d;
+            top = wave_max_u32(top);
+            if (lane == 0) filled_of = top;
         }
-        *reinterpret_cast<u32x2*>(A.bounds + dst * 2u * A.dim + lane * 8u) = up;
-        *reinterpret_cast<u32x2*>(A.bounds + (dst * 2u + 1u) * A.dim + lane * 8u) = down;
+        __syncthreads();
+        const uint32_t filled = filled_of;
+        float hi[8], lo[8], bad = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            hi[j] = -INFINITY;
+            lo[j] = INFINITY;
+        }
+        if (live) {
+            for (uint32_t r0 = way; r0 < filled; r0 += kTurn * ways) {
+                Eight<FMT> x[kTurn];
+#pragma unroll
+                for (int u = 0; u < kTurn; ++u) {
+                    const uint32_t r = r0 + u * ways < filled ? r0 + u * ways : r0;  // a row twice changes nothing
+                    x[u].load(A, (page * A.page_len + r) * A.heads + head, part);
+                }
+#pragma unroll
+                for (int u = 0; u < kTurn; ++u) {
+                    float v[8];
+                    x[u].values(v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        bad = fabsf(v[j]) < INFINITY ? bad : 1.0f;
+                        hi[j] = fmaxf(hi[j], v[j]);
+                        lo[j] = fminf(lo[j], v[j]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            hi_of[threadIdx.x][j] = hi[j];
+            lo_of[threadIdx.x][j] = lo[j];
+        }
+        hi_of[threadIdx.x][8] = bad;
+        __syncthreads();
+        if (way == 0) {
+            for (uint32_t w = 1; w < ways; ++w) {
+                const uint32_t o = w * width + sub;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    hi[j] = fmaxf(hi[j], hi_of[o][j]);
+                    lo[j] = fminf(lo[j], lo_of[o][j]);
+                }
+                bad = fmaxf(bad, hi_of[o][8]);
+            }
+            float a = bad != 0.0f ? INFINITY : 0.0f;
+            if (live)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a = fmaxf(a, fmaxf(fabsf(hi[j]), fabsf(lo[j])));
+#pragma unroll
+            for (int off = 1; off < L; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));  // of the head's lanes
+            const bool fine = a < INFINITY;
+            a = sized(a);
+            const float inv = 127.0f / a;
+            const uint64_t dst = page * A.heads + head;
+            if (live) {
+                u32x2 up, down;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t u = 0, d = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = fine ? ceilf(hi[4 * j + e] * inv) : 127.0f, n = fine ? floorf(lo[4 * j + e] * inv) : -127.0f;
+                        u |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(p, -127.0f, 127.0f) & 255u) << (8 * e);
+                        d |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(n, -127.0f, 127.0f) & 255u) << (8 * e);
+                    }
+                    up[j] = u;
+                    down[j] = d;
+                }
+                *reinterpret_cast<u32x2*>(A.bounds + dst * 2u * A.dim + part * 8u) = up;
+                *reinterpret_cast<u32x2*>(A.bounds + (dst * 2u + 1u) * A.dim + part * 8u) = down;
+                if (part == 0) A.bound_scales[dst] = fine ? a / 127.0f : INFINITY;
+            }
+        }
     }
-    if (lane == 0) A.bound_scales[dst] = fine ? a / 127.0f : INFINITY;
 }
+
+// ---- scores
 
 // Scores as ordered integers: 0 for a page that cannot be taken.
 __device__ __forceinline__ uint32_t order_key(float s) {
@@ -113,119 +198,321 @@ __device__ __forceinline__ uint32_t used_pages(const KvSelect& A, uint32_t b) {
     return (uint32_t)(n < A.max_pages ? n : A.max_pages);
 }
 
-// keys[b][h][page]; a workgroup takes 4 pages of (b, h), one a wave.
-__global__ __launch_bounds__(kThreads) void score_kernel(KvSelect A, uint32_t* keys, uint32_t groups) {
-    const uint64_t bh = blockIdx.x / groups;
-    const uint32_t b = (uint32_t)(bh / A.heads), h = (uint32_t)(bh % A.heads), lane = threadIdx.x % kWave;
-    const uint32_t page = (blockIdx.x % groups) * (kThreads / kWave) + threadIdx.x / kWave, used = used_pages(A, b);
-    if (page >= A.max_pages) return;
-    uint32_t key = 0;
-    const int32_t id = page < used ? A.page_table[(uint64_t)b * A.max_pages + page] : -1;
-    if (id >= 0 && (uint32_t)id < A.num_pages) {
-        const uint64_t at = (uint64_t)id * A.heads + h;
-        const uint32_t group = A.q_heads / A.heads;
-        for (uint32_t g = 0; g < group; ++g) {
-            const float* q = A.q + b * A.q_stride + (uint64_t)(h * group + g) * A.dim;
-            uint32_t top = 0;
-            for (uint32_t d = lane; d < A.dim; d += kWave) {
-                const uint32_t k = abs_key(q[d]);
+// 16 queries of a key head at a time, as the matrix cores take them: lane 16 g
+// + m holds bytes 64 s + 16 g .. + 15 of query m's 2 dim bytes max(n, 0), min(n,
+// 0).  C steps of 64 bytes cover them, as they do a page's hi, lo.
+constexpr uint32_t kQueries = 16;
+constexpr uint32_t kMaxSteps = 16;
+struct Queries {
+    i32x4 n[kMaxSteps][kWave];
+    float scale[kQueries];
+    uint32_t top[kQueries];
+};
+
+// Fills `Q` with the queries from q0 on (`rows` of them; zeros behind), by a workgroup of T lanes; barriers at both ends.
+template <int T>
+__device__ __forceinline__ void hold_queries(const float* q0, uint32_t rows, uint32_t dim, Queries& Q) {
+    constexpr uint32_t kLanes = T / kQueries;  // a query
+    const uint32_t m = threadIdx.x / kLanes, part = threadIdx.x % kLanes;
+    static_assert(kLanes >= 16 && kWave % 16 == 0);
+    __syncthreads();
+    const float* q = q0 + (uint64_t)m * dim;
+    uint32_t top = 0;
+    if (m < rows)
+        for (uint32_t d = part * 4u; d < dim; d += kLanes * 4u) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(q + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t k = abs_key(x[i]);
                 top = top > k ? top : k;
             }
-            const float a = sized(__uint_as_float(wave_max_u32(top))), inv = 127.0f / a, qs = a / 127.0f;
-            int sum = 0;
-            for (uint32_t d = lane; d < A.dim; d += kWave) {
-                const float x = q[d] * inv;
-                const int n = x != x ? 0 : (int)__builtin_amdgcn_fmed3f(rintf(x), -127.0f, 127.0f);
-                const int u = n * A.bounds[at * 2 * A.dim + d], l = n * A.bounds[(at * 2 + 1) * A.dim + d];
-                sum += u > l ? u : l;
-            }
-            for (int off = 1; off < kWave; off <<= 1) sum += __shfl_xor(sum, off, kWave);
-            const uint32_t k = order_key((float)sum * A.bound_scales[at] * qs);
-            key = key > k ? key : k;
         }
-        if (page == 0 || page == used - 1) key = order_key(INFINITY);
+    constexpr uint32_t kIn = kLanes < (uint32_t)kWave ? kLanes : kWave;  // of them in a wave
+#pragma unroll
+    for (uint32_t off = 1; off < kIn; off <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)top, (int)off, kWave);
+        top = top > o ? top : o;
     }
-    if (lane == 0) keys[bh * A.max_pages + page] = key;
+    const float a = sized(__uint_as_float(top)), inv = 127.0f / a;
+    if (part == 0) Q.scale[m] = a / 127.0f;
+    for (uint32_t d = part * 4u; d < dim; d += kLanes * 4u) {
+        uint32_t plus = 0, minus = 0;
+        if (m < rows) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(q + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float y = x[i] * inv;
+                const int n = y != y ? 0 : (int)__builtin_amdgcn_fmed3f(rintf(y), -127.0f, 127.0f);
+                plus |= (uint32_t)(n > 0 ? n : 0) << (8 * i);
+                minus |= ((uint32_t)(n < 0 ? n : 0) & 255u) << (8 * i);
+            }
+        }
+        // byte k of the 2 dim: step k / 64, lane group k / 16 % 4, byte k % 16
+        uint32_t* out = reinterpret_cast<uint32_t*>(Q.n);
+        const uint32_t k0 = d, k1 = dim + d;
+        out[(k0 / 64u * kWave + k0 / 16u % 4u * 16u + m) * 4u + k0 / 4u % 4u] = plus;
+        out[(k1 / 64u * kWave + k1 / 16u % 4u * 16u + m) * 4u + k1 / 4u % 4u] = minus;
+    }
+    __syncthreads();
 }
 
-// The `budget` largest keys of each row, ascending by page: the key of the
-// last one taken is found 8 bits at a time from counts.
+// The largest key of 16 pages' scores with the queries held in Q: every lane
+// 16 g + n gets that of page n, whose bounds lie at `bounds` for it.
+template <int C>
+__device__ __forceinline__ uint32_t score16(const Queries& Q, uint32_t rows, const int8_t* bounds, float scale) {
+    const uint32_t lane = threadIdx.x % kWave, g = lane / 16;
+    i32x4 b[C];
+#pragma unroll
+    for (int s = 0; s < C; ++s) b[s] = *reinterpret_cast<const i32x4*>(bounds + 64 * s + 16 * g);
+    i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < C; ++s) sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(Q.n[s][lane], b[s], sum, 0, 0, 0);
+    uint32_t key = 0;  // of queries 4 g + i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t k = 4 * g + i < rows ? order_key((float)sum[i] * scale * Q.scale[4 * g + i]) : 0u;
+        key = key > k ? key : k;
+    }
+    const auto x = __builtin_amdgcn_permlane16_swap(key, key, false, false);
+    key = x[0] > x[1] ? x[0] : x[1];
+    const auto y = __builtin_amdgcn_permlane32_swap(key, key, false, false);
+    return y[0] > y[1] ? y[0] : y[1];
+}
+
+// Keys of pages [first, last) of (b, h), by a workgroup of T lanes, to out[0 .. last - first).
+template <int C, int T>
+__device__ __forceinline__ void score_pages(const KvSelect& A, Queries& Q, uint32_t b, uint32_t h, uint32_t first, uint32_t last, uint32_t used, uint32_t* out) {
+    const uint32_t group = A.q_heads / A.heads, lane = threadIdx.x % kWave, n = lane % 16;
+    for (uint32_t q0 = 0; q0 < group; q0 += kQueries) {
+        const uint32_t rows = group - q0 < kQueries ? group - q0 : kQueries;
+        hold_queries<T>(A.q + b * A.q_stride + (uint64_t)(h * group + q0) * A.dim, rows, A.dim, Q);
+        for (uint32_t p0 = first + threadIdx.x / kWave * 16u; p0 < last; p0 += T / kWave * 16u) {
+            const uint32_t page = p0 + n;
+            int32_t id = page < last && page < used ? A.page_table[(uint64_t)b * A.max_pages + page] : -1;
+            if ((uint32_t)id >= A.num_pages) id = -1;
+            const uint64_t at = (uint64_t)(id < 0 ? 0 : id) * A.heads + h;
+            uint32_t key = score16<C>(Q, rows, A.bounds + at * (64u * C), A.bound_scales[at]);
+            if (page == 0 || page == used - 1) key = order_key(INFINITY);
+            if (id < 0) key = 0;
+            if (lane < 16 && page < last) out[page - first] = q0 && out[page - first] > key ? out[page - first] : key;
+        }
+    }
+}
+
+// ---- the choice
+
 constexpr int kPick = 1024;
-__global__ __launch_bounds__(kPick) void pick_kernel(KvSelect A, const uint32_t* keys) {
-    __shared__ uint32_t count[256], part[kPick / kWave], found[2];
-    const uint64_t bh = blockIdx.x;
-    const uint32_t used = used_pages(A, (uint32_t)(bh / A.heads)), lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    keys += bh * A.max_pages;
-    int32_t* out = A.pages + bh * A.budget;
-    uint32_t prefix = 0, left = A.budget;  // the threshold's upper bits so far; how many of those that share them are taken
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (threadIdx.x < 256) count[threadIdx.x] = 0;
-        if (threadIdx.x == 0) found[0] = 0, found[1] = left;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-        for (uint32_t i = threadIdx.x; i < used; i += kPick)
-            if ((keys[i] & mask) == prefix) atomicAdd(&count[keys[i] >> shift & 255u], 1u);
-        __syncthreads();
-        if (threadIdx.x < 256) {
-            uint32_t above = 0;
-            for (uint32_t i = threadIdx.x + 1; i < 256; ++i) above += count[i];
-            if (above < left && above + count[threadIdx.x] >= left) {
-                found[0] = threadIdx.x;
-                found[1] = left - above;
+constexpr int kPickWaves = kPick / kWave;
+constexpr uint32_t kBins = 2048;
+
+struct Pick {
+    uint32_t count[kBins];
+    uint32_t part[2][kPickWaves];
+    uint32_t bin, above, low, high;
+};
+
+// Sum of v over the lanes of the workgroup before this one, and over all.
+__device__ __forceinline__ uint32_t before(uint32_t v, uint32_t* part, uint32_t& all) {
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    uint32_t sum = v;
+    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x111, 0xF, 0xF, true);
+    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x112, 0xF, 0xF, true);
+    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x114, 0xF, 0xF, true);
+    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x118, 0xF, 0xF, true);
+    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x142, 0xA, 0xF, false);
+    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x143, 0xC, 0xF, false);
+    if (lane == kWave - 1) part[wave] = sum;
+    __syncthreads();
+    uint32_t x = sum - v;
+    all = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kPickWaves; ++i) {
+        const uint32_t n = part[i];
+        x += i < wave ? n : 0;
+        all += n;
+    }
+    __syncthreads();
+    return x;
+}
+
+// The `budget` largest of keys[0 .. n), ascending by place, ties to the lower
+// one; then -1.  The key of the last one taken is found from counts of 2048
+// equal bins between the smallest and the largest key that can be it, then
+// between that bin's ends, and so on: two or three rounds, whose counts fall on
+// many bins (counts by a key's upper bits fall on a few, as scores are alike).
+__device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, uint32_t budget, int32_t* out) {
+    uint32_t low = 0xFFFFFFFFu, high = 0, some = 0;  // of those that can be taken
+    for (uint32_t i = threadIdx.x; i < n; i += kPick) {
+        const uint32_t k = keys[i];
+        if (k) {
+            low = low < k ? low : k;
+            high = high > k ? high : k;
+            ++some;
+        }
+    }
+    if (threadIdx.x == 0) P.low = 0xFFFFFFFFu, P.high = 0, P.above = 0;
+    __syncthreads();
+    high = wave_max_u32(high);
+    low = ~wave_max_u32(~low);
+    if (threadIdx.x % kWave == 0 && high) {
+        atomicMin(&P.low, low);
+        atomicMax(&P.high, high);
+    }
+    uint32_t total;
+    before(some, P.part[0], total);  // barriers
+    low = P.low;
+    high = P.high;
+    // the threshold: every key above it is taken, and `left` of those equal to it
+    uint32_t threshold = 0, left = 0;
+    if (total > budget) {
+        left = budget;
+        for (;;) {
+            const uint32_t span = high - low, shift = span < kBins ? 0 : 21 - (uint32_t)__builtin_clz(span);  // span >> shift < 2048
+            for (uint32_t i = threadIdx.x; i < kBins; i += kPick) P.count[i] = 0;
+            __syncthreads();
+            for (uint32_t i = threadIdx.x; i < n; i += kPick) {
+                const uint32_t k = keys[i];
+                if (k >= low && k <= high) atomicAdd(&P.count[(k - low) >> shift], 1u);
             }
+            __syncthreads();
+            // lane t holds the bins 2047 - 2 t and 2046 - 2 t: sums run from the largest keys down
+            const uint32_t x = P.count[kBins - 1 - 2 * threadIdx.x], y = P.count[kBins - 2 - 2 * threadIdx.x];
+            uint32_t all, above = before(x + y, P.part[0], all);
+            if (above < left && above + x >= left) {
+                P.bin = kBins - 1 - 2 * threadIdx.x;
+                P.above = above;
+            } else if (above + x < left && above + x + y >= left) {
+                P.bin = kBins - 2 - 2 * threadIdx.x;
+                P.above = above + x;
+            }
+            __syncthreads();
+            left -= P.above;
+            low += P.bin << shift;
+            if (shift == 0) break;
+            const uint32_t end = low + (1u << shift) - 1;
+            high = end < high ? end : high;
         }
-        __syncthreads();
-        prefix |= found[0] << shift;
-        left = found[1];
-        __syncthreads();
+        threshold = low;
     }
-    // fewer than `budget` pages: the threshold is 0, and every key above it is taken
     uint32_t taken = 0, same = 0;
-    for (uint32_t i0 = 0; i0 < used; i0 += kPick) {
-        const uint32_t i = i0 + threadIdx.x, key = i < used ? keys[i] : 0;
-        const uint64_t eq = __ballot(key == prefix && key != 0);
-        if (lane == 0) part[wave] = (uint32_t)__popcll(eq);
-        __syncthreads();
-        uint32_t before = same + (uint32_t)__popcll(eq & ((1ull << lane) - 1));
-        for (uint32_t w = 0; w < kPick / kWave; ++w) {
-            if (w < wave) before += part[w];
-            same += part[w];
-        }
-        __syncthreads();
-        const bool take = key != 0 && (key > prefix || (key == prefix && before < left));
-        const uint64_t all = __ballot(take);
-        if (lane == 0) part[wave] = (uint32_t)__popcll(all);
-        __syncthreads();
-        uint32_t at = taken + (uint32_t)__popcll(all & ((1ull << lane) - 1));
-        for (uint32_t w = 0; w < kPick / kWave; ++w) {
-            if (w < wave) at += part[w];
-            taken += part[w];
-        }
-        __syncthreads();
+    for (uint32_t i0 = 0; i0 < n; i0 += kPick) {
+        const uint32_t i = i0 + threadIdx.x, key = i < n ? keys[i] : 0;
+        const bool eq = key != 0 && key == threshold;
+        uint32_t all_eq, all;
+        const uint32_t rank = same + before(eq, P.part[0], all_eq);
+        const bool take = key > threshold || (eq && rank < left);
+        const uint32_t at = taken + before(take, P.part[1], all);
         if (take) out[at] = (int32_t)i;
+        same += all_eq;
+        taken += all;
     }
-    for (uint32_t i = taken + threadIdx.x; i < A.budget; i += kPick) out[i] = -1;
+    for (uint32_t i = taken + threadIdx.x; i < budget; i += kPick) out[i] = -1;
+}
+
+// Few pages a sequence, or many sequences: a workgroup scores all pages of its
+// (sequence, key head) into its LDS and picks from there.
+template <int C>
+__global__ __launch_bounds__(kPick) void select_kernel(KvSelect A) {
+    extern __shared__ uint32_t keys[];
+    __shared__ union {
+        Queries q;
+        Pick p;
+    } S;
+    const uint32_t b = blockIdx.x / A.heads, h = blockIdx.x % A.heads, used = used_pages(A, b);
+    score_pages<C, kPick>(A, S.q, b, h, 0, used, used, keys);
+    __syncthreads();
+    pick(S.p, keys, used, A.budget, A.pages + (uint64_t)blockIdx.x * A.budget);
+}
+
+// Otherwise workgroups of their own score kSpan pages each, and a second launch picks.
+constexpr uint32_t kSpan = 256;
+template <int C>
+__global__ __launch_bounds__(kThreads) void score_kernel(KvSelect A, uint32_t* keys, uint32_t spans) {
+    __shared__ Queries Q;
+    const uint32_t bh = blockIdx.x / spans, b = bh / A.heads, h = bh % A.heads, first = blockIdx.x % spans * kSpan, used = used_pages(A, b);
+    if (first >= used) return;
+    const uint32_t last = used - first < kSpan ? used : first + kSpan;
+    score_pages<C, kThreads>(A, Q, b, h, first, last, used, keys + (uint64_t)bh * A.max_pages + first);
+}
+
+constexpr uint32_t kHeld = 32768;  // keys that the picking workgroup copies to its LDS
+__global__ __launch_bounds__(kPick) void pick_kernel(KvSelect A, const uint32_t* keys, bool held) {
+    extern __shared__ uint32_t copy[];
+    __shared__ Pick P;
+    const uint32_t used = used_pages(A, blockIdx.x / A.heads);
+    keys += (uint64_t)blockIdx.x * A.max_pages;
+    int32_t* out = A.pages + (uint64_t)blockIdx.x * A.budget;
+    if (held) {
+        for (uint32_t i = threadIdx.x; i < used; i += kPick) copy[i] = keys[i];
+        __syncthreads();
+        pick(P, copy, used, A.budget, out);
+    } else {
+        pick(P, keys, used, A.budget, out);
+    }
+}
+
+template <typename F>
+void with_steps(uint32_t c, F&& f) {
+    switch (c) {
+#define RZ_C(n) case n: f(std::integral_constant<int, n>{}); break;
+        RZ_C(1) RZ_C(2) RZ_C(3) RZ_C(4) RZ_C(5) RZ_C(6) RZ_C(7) RZ_C(8)
+        RZ_C(9) RZ_C(10) RZ_C(11) RZ_C(12) RZ_C(13) RZ_C(14) RZ_C(15) RZ_C(16)
+#undef RZ_C
+    }
+}
+
+// One launch where a workgroup's pages are few, or the workgroups many: 2048
+// pages of 128 columns are 512 KB of bounds for one of them.
+bool one_launch(uint32_t seqs, uint32_t heads, uint32_t max_pages) {
+    return max_pages <= 1024u || (max_pages <= 4096u && (uint64_t)seqs * heads >= 128u);
 }
 
 }  // namespace
 
 hipError_t launch_kv_bounds(int format, const KvBounds& A, hipStream_t st) {
-    const uint64_t items = (uint64_t)A.tokens * A.heads;
-    const uint32_t grid = (uint32_t)((items + kThreads / kWave - 1) / (kThreads / kWave));
-    if (format == kKvE4M3)
-        bounds_kernel<kKvE4M3><<<grid, kThreads, 0, st>>>(A);
+    const uint32_t lanes = A.dim <= 64 ? 8 : A.dim <= 128 ? 16 : A.dim <= 256 ? 32 : 64;
+    // single tokens: a workgroup a page and head; prompts: 64 tokens and as many heads as its lanes hold
+    uint32_t per = 1, wide = 1;
+    while (per < kMaxPer && (uint64_t)A.tokens * A.heads / per > 2048u) per <<= 1;
+    while (per > 1 && wide * 2u * lanes <= (uint32_t)kThreads && wide < A.heads && (uint64_t)A.tokens * A.heads / (per * wide) > 1024u) wide <<= 1;
+    const uint32_t groups = (A.heads + wide - 1) / wide;
+    const uint32_t grid = (A.tokens + per - 1) / per * groups;
+    auto launch = [&](auto l_) {
+        constexpr int L = decltype(l_)::value;
+        if (format == kKvE4M3)
+            bounds_kernel<kKvE4M3, L><<<grid, kThreads, 0, st>>>(A, per, wide, groups);
+        else
+            bounds_kernel<kKvMXFP4, L><<<grid, kThreads, 0, st>>>(A, per, wide, groups);
+    };
+    if (lanes == 8)
+        launch(std::integral_constant<int, 8>{});
+    else if (lanes == 16)
+        launch(std::integral_constant<int, 16>{});
+    else if (lanes == 32)
+        launch(std::integral_constant<int, 32>{});
     else
-        bounds_kernel<kKvMXFP4><<<grid, kThreads, 0, st>>>(A);
+        launch(std::integral_constant<int, 64>{});
     return hipGetLastError();
 }
 
-size_t kv_select_ws_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages) { return (size_t)seqs * heads * max_pages * 4u; }
+size_t kv_select_ws_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages) {
+    return one_launch(seqs, heads, max_pages) ? 0 : (size_t)seqs * heads * max_pages * 4u;
+}
 
 hipError_t launch_kv_select(const KvSelect& A, hipStream_t st) {
-    uint32_t* keys = static_cast<uint32_t*>(A.ws);
-    const uint32_t groups = (A.max_pages + kThreads / kWave - 1) / (kThreads / kWave);
-    if (groups) score_kernel<<<A.seqs * A.heads * groups, kThreads, 0, st>>>(A, keys, groups);
-    pick_kernel<<<A.seqs * A.heads, kPick, 0, st>>>(A, keys);
+    const uint32_t pairs = A.seqs * A.heads;
+    with_steps(A.dim / 32u, [&](auto c_) {
+        constexpr int C = decltype(c_)::value;
+        if (one_launch(A.seqs, A.heads, A.max_pages)) {
+            select_kernel<C><<<pairs, kPick, A.max_pages * 4u, st>>>(A);
+            return;
+        }
+        uint32_t* keys = static_cast<uint32_t*>(A.ws);
+        const uint32_t spans = (A.max_pages + kSpan - 1) / kSpan;
+        score_kernel<C><<<pairs * spans, kThreads, 0, st>>>(A, keys, spans);
+        const bool held = A.max_pages <= kHeld;
+        pick_kernel<<<pairs, kPick, held ? A.max_pages * 4u : 0u, st>>>(A, keys, held);
+    });
     return hipGetLastError();
 }
 

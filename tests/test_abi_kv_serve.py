@@ -70,7 +70,9 @@ def test_bounds(L):
 def test_select(L):
     #       q q_heads stride bounds scales pages heads dim page table seqs width lens budget out ws stream
     good = [P, 6, 6 * 64, P, P, 20, 2, 64, 16, P, 3, 4, P, 2, P, P, None]
-    refuses_each(L.rz_kv_select, good, (0, 3, 4, 9, 12, 14, 15))
+    refuses_each(L.rz_kv_select, good, (0, 3, 4, 9, 12, 14))
+    long = changed(changed(good, 11, 100000), 15, None)  # too many pages for one launch
+    assert L.rz_kv_select_workspace_bytes(3, 2, 100000) == 3 * 2 * 100000 * 4 and L.rz_kv_select(*long) == NULL
     refuses_each(L.rz_kv_select, good, (0, 3, 4, 15), ALIGN, BAD)
     refuses_each(L.rz_kv_select, good, (9, 12, 14), ALIGN, ODD)
     for at, v in ((1, 0), (1, 5), (2, 380), (2, 386), (6, 0), (7, 48), (8, 0), (13, 0), (11, 1 << 25), (10, 1 << 21)):

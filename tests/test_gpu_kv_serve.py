@@ -185,7 +185,7 @@ def ranked(pages, heads, dim, seed, kinds=0):
 @pytest.mark.parametrize("page,lens,heads,group,dim,budget,kinds", [
     (16, [37], 4, 7, 128, 2, 0), (16, [1, 0, 160, 161], 1, 1, 32, 4, 0), (64, [64 * 300, 64 * 299 + 1, 5], 2, 16, 64, 20, 0), (1, [1500, 1024, 1025], 3, 2, 96, 256, 0),
     (16, [16 * 700, 999], 2, 3, 256, 1, 0), (16, [16 * 900], 2, 17, 160, 300, 5), (32, [32 * 64] * 9, 2, 5, 512, 63, 3), (128, [50000, 130, 128], 1, 40, 192, 64, 0),
-    (1, [9000], 1, 2, 64, 4000, 7), (16, [300, 300], 8, 1, 128, 1000, 0)])
+    (1, [9000], 1, 2, 64, 4000, 7), (16, [300, 300], 8, 1, 128, 1000, 0), (1, [30000, 7], 1, 3, 32, 900, 0), (1, [40000], 2, 1, 32, 37, 0), (1, [4096] * 9, 16, 1, 32, 129, 50)])
 def test_select(rz, page, lens, heads, group, dim, budget, kinds):
     """One page to thousands, budgets below and above them, many equal scores, more queries than a tile holds."""
     print(f"select page={page} lens={lens} heads={heads} group={group} dim={dim} budget={budget}", flush=True)
