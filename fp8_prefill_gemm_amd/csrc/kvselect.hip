@@ -63,123 +63,166 @@ struct Eight {
     }
 };
 
-// A workgroup takes `per` consecutive tokens and `wide` heads: a token whose
-// predecessor lies in another page leads, and its page's rows (up to the last
-// token of the page in `slots`) are shared among the rows of lanes, eight
-// columns of a head a lane (L lanes a head), kTurn rows a lane in flight.
-constexpr int kTurn = 4;
-constexpr uint32_t kMaxPer = 64;
-
-template <int FMT, int L>
-__global__ __launch_bounds__(kThreads) void bounds_kernel(KvBounds A, uint32_t per, uint32_t wide, uint32_t groups) {
-    __shared__ int64_t slot_of[kMaxPer + 1];  // of the token before, then of these
-    __shared__ float hi_of[kThreads][9], lo_of[kThreads][9];
-    __shared__ uint32_t filled_of;
-    const uint32_t t0 = blockIdx.x / groups * per, head0 = blockIdx.x % groups * wide, lane = threadIdx.x % kWave;
-    const uint32_t width = wide * L, sub = threadIdx.x % width, way = threadIdx.x / width, ways = kThreads / width;
-    const uint32_t head = head0 + sub / L, part = sub % L;
-    const bool live = way < ways && head < A.heads && part * 8u < A.dim;
-    if (threadIdx.x <= per) {
-        const int64_t t = (int64_t)t0 + threadIdx.x - 1;
-        const int64_t s = t >= 0 && t < A.tokens ? A.slots[t] : -1;
-        slot_of[threadIdx.x] = s < 0 || (uint64_t)s >= A.num_slots ? -1 : s;
-    }
-    __syncthreads();
-    for (uint32_t i = 0; i < per; ++i) {  // uniform: every lane sees the same slots
-        const int64_t s = slot_of[i + 1], before = slot_of[i];
-        if (s < 0) continue;
-        const uint64_t page = (uint64_t)s / A.page_len;
-        if (page >= A.num_pages || (before >= 0 && (uint64_t)before / A.page_len == page)) continue;
-        // how far the page is filled: the largest of the tokens that follow each other in it
-        __syncthreads();
-        if (threadIdx.x < kWave) {
-            uint32_t top = 0;
-            for (uint64_t t = (uint64_t)t0 + i;; t += kWave) {
-                const int64_t x = t + lane < A.tokens ? A.slots[t + lane] : -1;
-                const bool in = x >= 0 && (uint64_t)x < A.num_slots && (uint64_t)x / A.page_len == page;
-                const uint64_t out = ~__ballot(in);
-                const uint32_t n = out ? (uint32_t)__ffsll((unsigned long long)out) - 1 : kWave;  // lanes that follow on
-                const uint32_t at = lane < n ? (uint32_t)((uint64_t)x - page * A.page_len) + 1 : 0;
-                top = top > at ? top : at;
-                if (n < kWave) break;
-            }
-            top = wave_max_u32(top);
-            if (lane == 0) filled_of = top;
-        }
-        __syncthreads();
-        const uint32_t filled = filled_of;
-        float hi[8], lo[8], bad = 0.0f;
+// Largest and smallest values of eight columns over some rows.
+struct Ends {
+    float hi[8], lo[8], bad;  // bad: not 0 where a value is none
+    __device__ __forceinline__ Ends() : bad(0.0f) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             hi[j] = -INFINITY;
             lo[j] = INFINITY;
         }
-        if (live) {
-            for (uint32_t r0 = way; r0 < filled; r0 += kTurn * ways) {
-                Eight<FMT> x[kTurn];
+    }
+    // rows `way`, way + ways, .. below `filled` of a page whose first row (of `head`) is row0; kTurn of them in flight
+    template <int FMT, int kTurn>
+    __device__ __forceinline__ void rows(const KvBounds& A, uint64_t row0, uint32_t part, uint32_t way, uint32_t ways, uint32_t filled) {
+        for (uint32_t r0 = way; r0 < filled; r0 += kTurn * ways) {
+            Eight<FMT> x[kTurn];
 #pragma unroll
-                for (int u = 0; u < kTurn; ++u) {
-                    const uint32_t r = r0 + u * ways < filled ? r0 + u * ways : r0;  // a row twice changes nothing
-                    x[u].load(A, (page * A.page_len + r) * A.heads + head, part);
-                }
-#pragma unroll
-                for (int u = 0; u < kTurn; ++u) {
-                    float v[8];
-                    x[u].values(v);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        bad = fabsf(v[j]) < INFINITY ? bad : 1.0f;
-                        hi[j] = fmaxf(hi[j], v[j]);
-                        lo[j] = fminf(lo[j], v[j]);
-                    }
-                }
+            for (int u = 0; u < kTurn; ++u) {
+                const uint32_t r = r0 + u * ways < filled ? r0 + u * ways : r0;  // a row twice changes nothing
+                x[u].load(A, row0 + (uint64_t)r * A.heads, part);
             }
-        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            hi_of[threadIdx.x][j] = hi[j];
-            lo_of[threadIdx.x][j] = lo[j];
-        }
-        hi_of[threadIdx.x][8] = bad;
-        __syncthreads();
-        if (way == 0) {
-            for (uint32_t w = 1; w < ways; ++w) {
-                const uint32_t o = w * width + sub;
+            for (int u = 0; u < kTurn; ++u) {
+                float v[8];
+                x[u].values(v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    hi[j] = fmaxf(hi[j], hi_of[o][j]);
-                    lo[j] = fminf(lo[j], lo_of[o][j]);
+                    bad = fabsf(v[j]) < INFINITY ? bad : 1.0f;
+                    hi[j] = fmaxf(hi[j], v[j]);
+                    lo[j] = fminf(lo[j], v[j]);
                 }
-                bad = fmaxf(bad, hi_of[o][8]);
             }
-            float a = bad != 0.0f ? INFINITY : 0.0f;
-            if (live)
+        }
+    }
+    __device__ __forceinline__ float largest() const {
+        float a = bad != 0.0f ? INFINITY : 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a = fmaxf(a, fmaxf(fabsf(hi[j]), fabsf(lo[j])));
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, fmaxf(fabsf(hi[j]), fabsf(lo[j])));
+        return a;
+    }
+    // This lane's columns of (page, head) `dst`, a the largest magnitude of all of them (infinite: a value is none).
+    __device__ __forceinline__ void write(const KvBounds& A, uint64_t dst, uint32_t part, float a) const {
+        const bool fine = a < INFINITY;
+        a = sized(a);
+        const float inv = 127.0f / a;
+        u32x2 up, down;
 #pragma unroll
-            for (int off = 1; off < L; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));  // of the head's lanes
-            const bool fine = a < INFINITY;
-            a = sized(a);
-            const float inv = 127.0f / a;
-            const uint64_t dst = page * A.heads + head;
-            if (live) {
-                u32x2 up, down;
+        for (int j = 0; j < 2; ++j) {
+            uint32_t u = 0, d = 0;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t u = 0, d = 0;
+            for (int e = 0; e < 4; ++e) {
+                const float p = fine ? ceilf(hi[4 * j + e] * inv) : 127.0f, n = fine ? floorf(lo[4 * j + e] * inv) : -127.0f;
+                u |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(p, -127.0f, 127.0f) & 255u) << (8 * e);
+                d |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(n, -127.0f, 127.0f) & 255u) << (8 * e);
+            }
+            up[j] = u;
+            down[j] = d;
+        }
+        *reinterpret_cast<u32x2*>(A.bounds + dst * 2u * A.dim + part * 8u) = up;
+        *reinterpret_cast<u32x2*>(A.bounds + (dst * 2u + 1u) * A.dim + part * 8u) = down;
+        if (part == 0) A.bound_scales[dst] = fine ? a / 127.0f : INFINITY;
+    }
+};
+
+// Slots and pages count below 2^31 (a cache holds at most 2^36 values, 32 a
+// row): a token's slot, or none.
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t slot_at(const KvBounds& A, uint64_t t) {
+    const int64_t s = t < A.tokens ? A.slots[t] : -1;
+    return s < 0 || (uint64_t)s >= A.num_slots ? kNone : (uint32_t)s;
+}
+
+// How far `page` is filled by the tokens from t on that follow each other in
+// it: the largest of them counts.  By a wave.
+__device__ __forceinline__ uint32_t filled_from(const KvBounds& A, uint64_t t, uint32_t page) {
+    const uint32_t lane = threadIdx.x % kWave;
+    uint32_t top = 0;
+    for (;; t += kWave) {
+        const uint32_t s = slot_at(A, t + lane);
+        const uint64_t out = ~__ballot(s != kNone && s / A.page_len == page);
+        const uint32_t n = out ? (uint32_t)__ffsll((unsigned long long)out) - 1 : kWave;  // lanes that follow on
+        const uint32_t at = lane < n ? s - page * A.page_len + 1 : 0;
+        top = top > at ? top : at;
+        if (n < kWave) break;
+    }
+    return wave_max_u32(top);
+}
+
+// A decoding step: a workgroup a (token, head).  A token whose predecessor lies
+// in another page leads; the page's rows are shared among the rows of lanes,
+// eight columns a lane (L lanes a row).
+template <int FMT, int L>
+__global__ __launch_bounds__(kThreads) void bounds_step_kernel(KvBounds A) {
+    constexpr uint32_t ways = kThreads / L;
+    __shared__ float of[17][kThreads];  // column first: no two lanes in a bank
+    const uint32_t t = blockIdx.x / A.heads, head = blockIdx.x % A.heads, part = threadIdx.x % L, way = threadIdx.x / L;
+    const uint32_t s = slot_at(A, t), prior = t ? slot_at(A, t - 1) : kNone;
+    if (s == kNone) return;
+    const uint32_t page = s / A.page_len;
+    if (page >= A.num_pages || (prior != kNone && prior / A.page_len == page)) return;
+    const uint32_t filled = filled_from(A, t, page);
+    Ends x;
+    const bool live = part * 8u < A.dim;
+    if (live) x.template rows<FMT, 4>(A, (uint64_t)page * A.page_len * A.heads + head, part, way, ways, filled);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p = fine ? ceilf(hi[4 * j + e] * inv) : 127.0f, n = fine ? floorf(lo[4 * j + e] * inv) : -127.0f;
-                        u |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(p, -127.0f, 127.0f) & 255u) << (8 * e);
-                        d |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(n, -127.0f, 127.0f) & 255u) << (8 * e);
-                    }
-                    up[j] = u;
-                    down[j] = d;
+    for (int j = 0; j < 8; ++j) {
+        of[j][threadIdx.x] = x.hi[j];
+        of[8 + j][threadIdx.x] = x.lo[j];
+    }
+    of[16][threadIdx.x] = x.bad;
+    __syncthreads();
+    if (way != 0) return;
+#pragma unroll 4
+    for (uint32_t w = 1; w < ways; ++w) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x.hi[j] = fmaxf(x.hi[j], of[j][w * L + part]);
+            x.lo[j] = fminf(x.lo[j], of[8 + j][w * L + part]);
+        }
+        x.bad = fmaxf(x.bad, of[16][w * L + part]);
+    }
+    float a = live ? x.largest() : 0.0f;
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));
+    if (live) x.write(A, (uint64_t)page * A.heads + head, part, a);
+}
+
+// Prompts: a workgroup looks `per` tokens over for those that lead, and its
+// waves take the (page, head) pairs in turn, each by itself.
+template <int FMT, int L>
+__global__ __launch_bounds__(kThreads) void bounds_prompt_kernel(KvBounds A, uint32_t per) {
+    constexpr uint32_t ways = kWave / L;
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, part = lane % L, way = lane / L;
+    const uint64_t t0 = (uint64_t)blockIdx.x * per;
+    const uint32_t s = lane < per ? slot_at(A, t0 + lane) : kNone, prior = lane < per && t0 + lane ? slot_at(A, t0 + lane - 1) : kNone;
+    const uint32_t mine = s == kNone ? kNone : s / A.page_len;
+    const bool leads = mine < A.num_pages && !(prior != kNone && prior / A.page_len == mine);
+    const bool live = part * 8u < A.dim;
+    uint32_t turn = 0;
+    for (uint64_t todo = __ballot(leads); todo; todo &= todo - 1) {
+        const int l = __ffsll((unsigned long long)todo) - 1;
+        const uint32_t page = (uint32_t)__builtin_amdgcn_readlane((int)mine, l);
+        uint32_t filled = 0;
+        for (uint32_t head = 0; head < A.heads; ++head, ++turn) {
+            if (turn % (kThreads / kWave) != wave) continue;
+            if (filled == 0) filled = filled_from(A, t0 + l, page);
+            Ends x;
+            if (live) x.template rows<FMT, 8>(A, (uint64_t)page * A.page_len * A.heads + head, part, way, ways, filled);
+#pragma unroll
+            for (int off = L; off < kWave; off <<= 1) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x.hi[j] = fmaxf(x.hi[j], __shfl_xor(x.hi[j], off, kWave));
+                    x.lo[j] = fminf(x.lo[j], __shfl_xor(x.lo[j], off, kWave));
                 }
-                *reinterpret_cast<u32x2*>(A.bounds + dst * 2u * A.dim + part * 8u) = up;
-                *reinterpret_cast<u32x2*>(A.bounds + (dst * 2u + 1u) * A.dim + part * 8u) = down;
-                if (part == 0) A.bound_scales[dst] = fine ? a / 127.0f : INFINITY;
+                x.bad = fmaxf(x.bad, __shfl_xor(x.bad, off, kWave));
             }
+            float a = live ? x.largest() : 0.0f;
+#pragma unroll
+            for (int off = 1; off < L; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));
+            if (live && way == 0) x.write(A, (uint64_t)page * A.heads + head, part, a);
         }
     }
 }
@@ -471,18 +514,24 @@ bool one_launch(uint32_t seqs, uint32_t heads, uint32_t max_pages) {
 
 hipError_t launch_kv_bounds(int format, const KvBounds& A, hipStream_t st) {
     const uint32_t lanes = A.dim <= 64 ? 8 : A.dim <= 128 ? 16 : A.dim <= 256 ? 32 : 64;
-    // single tokens: a workgroup a page and head; prompts: 64 tokens and as many heads as its lanes hold
-    uint32_t per = 1, wide = 1;
-    while (per < kMaxPer && (uint64_t)A.tokens * A.heads / per > 2048u) per <<= 1;
-    while (per > 1 && wide * 2u * lanes <= (uint32_t)kThreads && wide < A.heads && (uint64_t)A.tokens * A.heads / (per * wide) > 1024u) wide <<= 1;
-    const uint32_t groups = (A.heads + wide - 1) / wide;
-    const uint32_t grid = (A.tokens + per - 1) / per * groups;
+    // up to 2048 (token, head) pairs a workgroup each; more: 16 tokens a workgroup, fewer where those would not fill the CUs
+    // (each token of a step leads)
+    const bool step = (uint64_t)A.tokens * A.heads <= 2048u;
+    const uint32_t per = A.tokens / 1024u < 1u ? 1u : A.tokens / 1024u < 16u ? A.tokens / 1024u : 16u;
+    const uint32_t grid = step ? A.tokens * A.heads : (A.tokens + per - 1) / per;
     auto launch = [&](auto l_) {
         constexpr int L = decltype(l_)::value;
+        auto go = [&](auto f_) {
+            constexpr int FMT = decltype(f_)::value;
+            if (step)
+                bounds_step_kernel<FMT, L><<<grid, kThreads, 0, st>>>(A);
+            else
+                bounds_prompt_kernel<FMT, L><<<grid, kThreads, 0, st>>>(A, per);
+        };
         if (format == kKvE4M3)
-            bounds_kernel<kKvE4M3, L><<<grid, kThreads, 0, st>>>(A, per, wide, groups);
+            go(std::integral_constant<int, kKvE4M3>{});
         else
-            bounds_kernel<kKvMXFP4, L><<<grid, kThreads, 0, st>>>(A, per, wide, groups);
+            go(std::integral_constant<int, kKvMXFP4>{});
     };
     if (lanes == 8)
         launch(std::integral_constant<int, 8>{});
