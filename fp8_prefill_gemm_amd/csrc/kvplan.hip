@@ -102,22 +102,24 @@ struct Step {
     __device__ __forceinline__ uint32_t take() const { return ok && need > held ? need - held : 0; }
 };
 
-// The slot of token t, by its sequence's row; FILL: a new page's number is
-// taken from the stack and, at the page's first token, written to the table.
-template <bool FILL, typename R>
-__device__ __forceinline__ int64_t slot_of(const KvPlan& A, const R* rows, uint32_t t) {
-    if (A.seqs == 0 || (int64_t)t < A.offsets[0] || (int64_t)t >= A.offsets[A.seqs]) return -1;
-    uint32_t lo = 0, hi = A.seqs;  // offsets[lo] <= t < offsets[hi]
+// The sequence among [lo, hi) that token t belongs to, offsets[lo] <= t < offsets[hi].
+__device__ __forceinline__ uint32_t sequence_of(const int32_t* offsets, uint32_t lo, uint32_t hi, uint32_t t) {
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) >> 1;
-        if ((int64_t)t >= A.offsets[mid]) lo = mid; else hi = mid;
+        if ((int64_t)t >= offsets[mid]) lo = mid; else hi = mid;
     }
-    const Row row = rows[lo];
+    return lo;
+}
+
+// The slot of token t of sequence b; FILL: a new page's number is taken from
+// the stack and, at the page's first token, written to the table.
+template <bool FILL>
+__device__ __forceinline__ int64_t slot_of(const KvPlan& A, const Row& row, uint32_t b, uint32_t t, int32_t offset) {
     if (row.first < 0) return -1;
-    const uint64_t pos = (uint64_t)(uint32_t)row.first + (t - (uint32_t)A.offsets[lo]), page = pos / A.page_len;
+    const uint64_t pos = (uint64_t)(uint32_t)row.first + (t - (uint32_t)offset), page = pos / A.page_len;
     if (page >= A.max_pages) return -1;  // offsets that decrease
     const uint32_t at = (uint32_t)(pos - page * A.page_len);
-    int32_t* entry = A.page_table + (uint64_t)lo * A.max_pages + page;
+    int32_t* entry = A.page_table + (uint64_t)b * A.max_pages + page;
     int64_t id;
     if (FILL && page >= row.held) {
         const uint64_t below = page - row.held;
@@ -133,6 +135,8 @@ __device__ __forceinline__ int64_t slot_of(const KvPlan& A, const R* rows, uint3
 __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, bool one) {
     __shared__ uint32_t smem[kWaves][2];
     __shared__ uint32_t used_of;
+    __shared__ Row row_of[kThreads];  // of up to 1024 sequences
+    __shared__ int32_t offset_of[kThreads + 1];
     const int lane = threadIdx.x & (kWave - 1);
     const uint32_t rounds = (A.seqs + kThreads - 1) / kThreads;
     // pages are moved here unless every new token is the second launch's (tokens that it does not know have pages too)
@@ -141,6 +145,8 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
     uint32_t have = count < 0 ? 0 : (uint32_t)count > A.num_pages ? A.num_pages : (uint32_t)count;
     if (threadIdx.x == 0) used_of = 0;
     Step step(A, threadIdx.x);
+    if (rounds == 1)
+        for (uint32_t i = threadIdx.x; i <= A.seqs; i += kThreads) offset_of[i] = A.offsets[i];
     uint32_t before_take = 0, taken = 0;
     for (uint32_t r = 0; r < rounds; ++r) {  // one for up to 1024 sequences
         if (rounds > 1) step = Step(A, r * kThreads + threadIdx.x);
@@ -168,7 +174,8 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
         const uint32_t take = step.take(), after = add(before_take, take);
         const bool fits = step.ok && (take == 0 || after <= have);
         if (b < A.seqs) {
-            rows[b] = {fits ? (int32_t)step.first : -1, step.held, have - 1 - before_take};
+            const Row row = {fits ? (int32_t)step.first : -1, step.held, have - 1 - before_take};
+            if (one && rounds == 1) row_of[b] = row; else rows[b] = row;
             A.lens_out[b] = (int32_t)(fits ? step.then : step.len);
         }
         if (fits && take) atomicMax(&used_of, after);
@@ -180,13 +187,32 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
     }
     __syncthreads();
     if (threadIdx.x == 0) A.count_out[0] = (int32_t)(have - used_of);
-    if (one)
-        for (uint32_t t = threadIdx.x; t < A.tokens; t += kThreads) A.slots[t] = slot_of<false>(A, rows, t);
+    if (!one) return;
+    const int32_t* offsets = rounds == 1 ? offset_of : A.offsets;
+    const int64_t begin = A.seqs ? offsets[0] : 0, end = A.seqs ? offsets[A.seqs] : 0;
+    for (uint32_t t = threadIdx.x; t < A.tokens; t += kThreads) {
+        int64_t slot = -1;
+        if (t >= begin && t < end) {
+            const uint32_t b = sequence_of(offsets, 0, A.seqs, t);
+            slot = slot_of<false>(A, rounds == 1 ? row_of[b] : rows[b], b, t, offsets[b]);
+        }
+        A.slots[t] = slot;
+    }
 }
 
+// The sequences of a workgroup's first and last token narrow down those of the others.
 __global__ __launch_bounds__(256) void slots_kernel(KvPlan A, const Row* rows) {
     const uint32_t t = blockIdx.x * 256u + threadIdx.x;
-    if (t < A.tokens) A.slots[t] = slot_of<true>(A, rows, t);
+    if (t >= A.tokens) return;
+    int64_t slot = -1;
+    if (A.seqs != 0 && (int64_t)t >= A.offsets[0] && (int64_t)t < A.offsets[A.seqs]) {
+        const int64_t begin = A.offsets[0], end = A.offsets[A.seqs], first = blockIdx.x * 256ll, last = first + 255;
+        const uint32_t lo = sequence_of(A.offsets, 0, A.seqs, (uint32_t)(first < begin ? begin : first));
+        const uint32_t hi = sequence_of(A.offsets, lo, A.seqs, (uint32_t)(last < end ? last : end - 1)) + 1;
+        const uint32_t b = sequence_of(A.offsets, lo, hi, t);
+        slot = slot_of<true>(A, rows[b], b, t, A.offsets[b]);
+    }
+    A.slots[t] = slot;
 }
 
 }  // namespace

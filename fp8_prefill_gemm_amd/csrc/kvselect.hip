@@ -236,6 +236,8 @@ __device__ __forceinline__ uint32_t order_key(float s) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr uint32_t kForced = 0xFF800000u;  // that of +inf, the largest there is
+
 __device__ __forceinline__ uint32_t used_pages(const KvSelect& A, uint32_t b) {
     const int64_t len = A.lens[b] > 0 ? A.lens[b] : 0, n = (len + A.page_len - 1) / A.page_len;
     return (uint32_t)(n < A.max_pages ? n : A.max_pages);
@@ -299,45 +301,62 @@ __device__ __forceinline__ void hold_queries(const float* q0, uint32_t rows, uin
     __syncthreads();
 }
 
-// The largest key of 16 pages' scores with the queries held in Q: every lane
-// 16 g + n gets that of page n, whose bounds lie at `bounds` for it.
+// 16 pages' bounds as the matrix cores take them, lane 16 g + n those of page n.
 template <int C>
-__device__ __forceinline__ uint32_t score16(const Queries& Q, uint32_t rows, const int8_t* bounds, float scale) {
-    const uint32_t lane = threadIdx.x % kWave, g = lane / 16;
+struct Pages {
     i32x4 b[C];
-#pragma unroll
-    for (int s = 0; s < C; ++s) b[s] = *reinterpret_cast<const i32x4*>(bounds + 64 * s + 16 * g);
-    i32x4 sum = {0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < C; ++s) sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(Q.n[s][lane], b[s], sum, 0, 0, 0);
-    uint32_t key = 0;  // of queries 4 g + i
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t k = 4 * g + i < rows ? order_key((float)sum[i] * scale * Q.scale[4 * g + i]) : 0u;
-        key = key > k ? key : k;
-    }
-    const auto x = __builtin_amdgcn_permlane16_swap(key, key, false, false);
-    key = x[0] > x[1] ? x[0] : x[1];
-    const auto y = __builtin_amdgcn_permlane32_swap(key, key, false, false);
-    return y[0] > y[1] ? y[0] : y[1];
-}
+    float scale;
+    int32_t id;  // -1: not a page
 
-// Keys of pages [first, last) of (b, h), by a workgroup of T lanes, to out[0 .. last - first).
+    __device__ __forceinline__ void load(const KvSelect& A, uint32_t b0, uint32_t h, uint32_t page, uint32_t last) {
+        const uint32_t g = threadIdx.x % kWave / 16;
+        id = page < last ? A.page_table[(uint64_t)b0 * A.max_pages + page] : -1;
+        if ((uint32_t)id >= A.num_pages) id = -1;
+        if (A.num_pages == 0) return;
+        const uint64_t at = (uint64_t)(id < 0 ? 0 : id) * A.heads + h;
+        scale = A.bound_scales[at];
+#pragma unroll
+        for (int s = 0; s < C; ++s) b[s] = *reinterpret_cast<const i32x4*>(A.bounds + at * (64u * C) + 64 * s + 16 * g);
+    }
+    // The largest key of their scores with the queries held in Q: every lane 16 g + n gets that of page n.
+    __device__ __forceinline__ uint32_t key(const Queries& Q, uint32_t rows) const {
+        const uint32_t lane = threadIdx.x % kWave, g = lane / 16;
+        i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < C; ++s) sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(Q.n[s][lane], b[s], sum, 0, 0, 0);
+        uint32_t key = 0;  // of queries 4 g + i
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t k = 4 * g + i < rows ? order_key((float)sum[i] * scale * Q.scale[4 * g + i]) : 0u;
+            key = key > k ? key : k;
+        }
+        const auto x = __builtin_amdgcn_permlane16_swap(key, key, false, false);
+        key = x[0] > x[1] ? x[0] : x[1];
+        const auto y = __builtin_amdgcn_permlane32_swap(key, key, false, false);
+        return y[0] > y[1] ? y[0] : y[1];
+    }
+};
+
+// Keys of pages [first, last) of (b, h), by a workgroup of T lanes, to out[0 ..
+// last - first); the first pages' bounds are loaded before the queries are
+// held, the next ones' before a tile is scored.
 template <int C, int T>
 __device__ __forceinline__ void score_pages(const KvSelect& A, Queries& Q, uint32_t b, uint32_t h, uint32_t first, uint32_t last, uint32_t used, uint32_t* out) {
     const uint32_t group = A.q_heads / A.heads, lane = threadIdx.x % kWave, n = lane % 16;
+    const uint32_t begin = first + threadIdx.x / kWave * 16u;
     for (uint32_t q0 = 0; q0 < group; q0 += kQueries) {
         const uint32_t rows = group - q0 < kQueries ? group - q0 : kQueries;
+        Pages<C> x, next;
+        x.load(A, b, h, begin + n, last);
         hold_queries<T>(A.q + b * A.q_stride + (uint64_t)(h * group + q0) * A.dim, rows, A.dim, Q);
-        for (uint32_t p0 = first + threadIdx.x / kWave * 16u; p0 < last; p0 += T / kWave * 16u) {
+        for (uint32_t p0 = begin; p0 < last; p0 += T / kWave * 16u) {
             const uint32_t page = p0 + n;
-            int32_t id = page < last && page < used ? A.page_table[(uint64_t)b * A.max_pages + page] : -1;
-            if ((uint32_t)id >= A.num_pages) id = -1;
-            const uint64_t at = (uint64_t)(id < 0 ? 0 : id) * A.heads + h;
-            uint32_t key = score16<C>(Q, rows, A.bounds + at * (64u * C), A.bound_scales[at]);
-            if (page == 0 || page == used - 1) key = order_key(INFINITY);
-            if (id < 0) key = 0;
+            if (p0 + T / kWave * 16u < last) next.load(A, b, h, page + T / kWave * 16u, last);
+            uint32_t key = x.key(Q, rows);
+            if (page == 0 || page == used - 1) key = kForced;
+            if (x.id < 0) key = 0;
             if (lane < 16 && page < last) out[page - first] = q0 && out[page - first] > key ? out[page - first] : key;
+            x = next;
         }
     }
 }
@@ -351,7 +370,7 @@ constexpr uint32_t kBins = 2048;
 struct Pick {
     uint32_t count[kBins];
     uint32_t part[2][kPickWaves];
-    uint32_t bin, above, low, high;
+    uint32_t bin, above, in, low, high;
 };
 
 // Sum of v over the lanes of the workgroup before this one, and over all.
@@ -383,17 +402,21 @@ __device__ __forceinline__ uint32_t before(uint32_t v, uint32_t* part, uint32_t&
 // equal bins between the smallest and the largest key that can be it, then
 // between that bin's ends, and so on: two or three rounds, whose counts fall on
 // many bins (counts by a key's upper bits fall on a few, as scores are alike).
+// Infinite scores, the forced ones, are counted apart: they would stretch the
+// bins.
 __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, uint32_t budget, int32_t* out) {
-    uint32_t low = 0xFFFFFFFFu, high = 0, some = 0;  // of those that can be taken
+    uint32_t low = 0xFFFFFFFFu, high = 0, some = 0, forced = 0;  // of those that can be taken
     for (uint32_t i = threadIdx.x; i < n; i += kPick) {
         const uint32_t k = keys[i];
-        if (k) {
+        if (k == kForced) {
+            ++forced;
+        } else if (k) {
             low = low < k ? low : k;
             high = high > k ? high : k;
             ++some;
         }
     }
-    if (threadIdx.x == 0) P.low = 0xFFFFFFFFu, P.high = 0, P.above = 0;
+    if (threadIdx.x == 0) P.low = 0xFFFFFFFFu, P.high = 0;
     __syncthreads();
     high = wave_max_u32(high);
     low = ~wave_max_u32(~low);
@@ -401,14 +424,18 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
         atomicMin(&P.low, low);
         atomicMax(&P.high, high);
     }
-    uint32_t total;
+    uint32_t total, always;
     before(some, P.part[0], total);  // barriers
+    before(forced, P.part[1], always);
     low = P.low;
     high = P.high;
     // the threshold: every key above it is taken, and `left` of those equal to it
     uint32_t threshold = 0, left = 0;
-    if (total > budget) {
+    if (always >= budget) {
+        threshold = kForced;
         left = budget;
+    } else if (total > budget - always) {
+        left = budget - always;
         for (;;) {
             const uint32_t span = high - low, shift = span < kBins ? 0 : 21 - (uint32_t)__builtin_clz(span);  // span >> shift < 2048
             for (uint32_t i = threadIdx.x; i < kBins; i += kPick) P.count[i] = 0;
@@ -424,30 +451,40 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
             if (above < left && above + x >= left) {
                 P.bin = kBins - 1 - 2 * threadIdx.x;
                 P.above = above;
+                P.in = x;
             } else if (above + x < left && above + x + y >= left) {
                 P.bin = kBins - 2 - 2 * threadIdx.x;
                 P.above = above + x;
+                P.in = y;
             }
             __syncthreads();
             left -= P.above;
             low += P.bin << shift;
             if (shift == 0) break;
+            if (P.in == left) {  // the whole bin is taken: its lower end will do, and nothing equals what lies below that
+                left = 0;
+                low -= 1;
+                break;
+            }
             const uint32_t end = low + (1u << shift) - 1;
             high = end < high ? end : high;
         }
         threshold = low;
     }
-    uint32_t taken = 0, same = 0;
-    for (uint32_t i0 = 0; i0 < n; i0 += kPick) {
-        const uint32_t i = i0 + threadIdx.x, key = i < n ? keys[i] : 0;
-        const bool eq = key != 0 && key == threshold;
-        uint32_t all_eq, all;
-        const uint32_t rank = same + before(eq, P.part[0], all_eq);
-        const bool take = key > threshold || (eq && rank < left);
-        const uint32_t at = taken + before(take, P.part[1], all);
-        if (take) out[at] = (int32_t)i;
-        same += all_eq;
-        taken += all;
+    // a lane a run of consecutive places, so that two sums over the lanes say where each goes
+    const uint32_t per = (n + kPick - 1) / kPick, i0 = threadIdx.x * per < n ? threadIdx.x * per : n, i1 = i0 + per < n ? i0 + per : n;
+    uint32_t equal = 0, over = 0, all;
+    for (uint32_t i = i0; i < i1; ++i) {
+        const uint32_t k = keys[i];
+        equal += k != 0 && k == threshold;
+        over += k > threshold;
+    }
+    uint32_t rank = before(equal, P.part[0], all);
+    const uint32_t mine = rank < left ? (left - rank < equal ? left - rank : equal) : 0;
+    uint32_t taken, at = before(over + mine, P.part[1], taken);
+    for (uint32_t i = i0; i < i1; ++i) {
+        const uint32_t k = keys[i];
+        if (k > threshold || (k != 0 && k == threshold && rank++ < left)) out[at++] = (int32_t)i;
     }
     for (uint32_t i = taken + threadIdx.x; i < budget; i += kPick) out[i] = -1;
 }
@@ -468,7 +505,7 @@ __global__ __launch_bounds__(kPick) void select_kernel(KvSelect A) {
 }
 
 // Otherwise workgroups of their own score kSpan pages each, and a second launch picks.
-constexpr uint32_t kSpan = 256;
+constexpr uint32_t kSpan = 64;
 template <int C>
 __global__ __launch_bounds__(kThreads) void score_kernel(KvSelect A, uint32_t* keys, uint32_t spans) {
     __shared__ Queries Q;
