@@ -111,9 +111,8 @@ __device__ __forceinline__ uint32_t sequence_of(const int32_t* offsets, uint32_t
     return lo;
 }
 
-// The slot of token t of sequence b; FILL: a new page's number is taken from
+// The slot of token t of sequence b.  A new page's number is taken from
 // the stack and, at the page's first token, written to the table.
-template <bool FILL>
 __device__ __forceinline__ int64_t slot_of(const KvPlan& A, const Row& row, uint32_t b, uint32_t t, int32_t offset) {
     if (row.first < 0) return -1;
     const uint64_t pos = (uint64_t)(uint32_t)row.first + (t - (uint32_t)offset), page = pos / A.page_len;
@@ -121,7 +120,7 @@ __device__ __forceinline__ int64_t slot_of(const KvPlan& A, const Row& row, uint
     const uint32_t at = (uint32_t)(pos - page * A.page_len);
     int32_t* entry = A.page_table + (uint64_t)b * A.max_pages + page;
     int64_t id;
-    if (FILL && page >= row.held) {
+    if (page >= row.held) {
         const uint64_t below = page - row.held;
         if (below > row.top || row.top - below >= A.num_pages) return -1;  // offsets that decrease
         id = A.free_pages[row.top - below];
@@ -132,27 +131,53 @@ __device__ __forceinline__ int64_t slot_of(const KvPlan& A, const Row& row, uint
     return id < 0 ? -1 : id * A.page_len + at;
 }
 
+// The row whose run of a prefix sum place i lies in: sums[b] <= i < sums[b + 1].
+__device__ __forceinline__ uint32_t row_of_place(const uint32_t* sums, uint32_t rows, uint32_t i) {
+    uint32_t lo = 0, hi = rows;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (i >= sums[mid]) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// `few`: up to 1024 sequences, a lane each, whose pages the lanes move one a
+// lane; otherwise rounds of 1024, whose waves move a sequence's at a time.
 __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, bool one) {
     __shared__ uint32_t smem[kWaves][2];
     __shared__ uint32_t used_of;
-    __shared__ Row row_of[kThreads];  // of up to 1024 sequences
+    __shared__ Row row_of[kThreads];
     __shared__ int32_t offset_of[kThreads + 1];
+    __shared__ uint32_t sums[kThreads], need_of[kThreads];
     const int lane = threadIdx.x & (kWave - 1);
     const uint32_t rounds = (A.seqs + kThreads - 1) / kThreads;
-    // pages are moved here unless every new token is the second launch's (tokens that it does not know have pages too)
-    const bool fill = one || (A.seqs != 0 && A.offsets[A.seqs] > (int64_t)A.tokens);
+    const bool few = rounds <= 1;
     const int32_t count = A.free_count[0];
     uint32_t have = count < 0 ? 0 : (uint32_t)count > A.num_pages ? A.num_pages : (uint32_t)count;
     if (threadIdx.x == 0) used_of = 0;
     Step step(A, threadIdx.x);
-    if (rounds == 1)
+    if (few && A.seqs)
         for (uint32_t i = threadIdx.x; i <= A.seqs; i += kThreads) offset_of[i] = A.offsets[i];
+    // new pages are written here unless their tokens do that (those that `tokens` leaves out have pages too)
+    const bool fill = A.seqs != 0 && A.offsets[A.seqs] > (int64_t)A.tokens;
     uint32_t before_take = 0, taken = 0;
-    for (uint32_t r = 0; r < rounds; ++r) {  // one for up to 1024 sequences
-        if (rounds > 1) step = Step(A, r * kThreads + threadIdx.x);
-        const uint32_t give = step.give(), wave0 = (r * kThreads + threadIdx.x) & ~(kWave - 1u);
-        const Scan s = scan(give, rounds > 1 ? 0 : step.take(), smem);
+    if (few) {
+        const uint32_t give = step.give();
+        const Scan s = scan(give, step.take(), smem);
         before_take = s.before[1];
+        sums[threadIdx.x] = s.before[0];
+        need_of[threadIdx.x] = step.need;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < s.all[0] && add(have, i) < A.num_pages; i += kThreads) {
+            const uint32_t b = row_of_place(sums, A.seqs, i);
+            A.free_pages[have + i] = A.page_table[(uint64_t)b * A.max_pages + need_of[b] + (i - sums[b])];
+        }
+        have = add(have, s.all[0]);
+    }
+    for (uint32_t r = 0; r < rounds && !few; ++r) {
+        step = Step(A, r * kThreads + threadIdx.x);
+        const uint32_t give = step.give(), wave0 = (r * kThreads + threadIdx.x) & ~(kWave - 1u);
+        const Scan s = scan(give, 0, smem);
         const uint32_t at = add(have, s.before[0]);
         each(give, [&](int l, uint32_t n) {
             const uint32_t to = (uint32_t)__shfl((int)at, l, kWave);
@@ -165,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
     __syncthreads();  // what was given may be taken below
     for (uint32_t r = 0; r < rounds; ++r) {
         const uint32_t b = r * kThreads + threadIdx.x, wave0 = b & ~(kWave - 1u);
-        if (rounds > 1) {
+        if (!few) {
             step = Step(A, b);
             const Scan s = scan(step.take(), 0, smem);
             before_take = add(taken, s.before[0]);
@@ -175,7 +200,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
         const bool fits = step.ok && (take == 0 || after <= have);
         if (b < A.seqs) {
             const Row row = {fits ? (int32_t)step.first : -1, step.held, have - 1 - before_take};
-            if (one && rounds == 1) row_of[b] = row; else rows[b] = row;
+            if (one && few) row_of[b] = row; else rows[b] = row;
             A.lens_out[b] = (int32_t)(fits ? step.then : step.len);
         }
         if (fits && take) atomicMax(&used_of, after);
@@ -188,13 +213,13 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
     __syncthreads();
     if (threadIdx.x == 0) A.count_out[0] = (int32_t)(have - used_of);
     if (!one) return;
-    const int32_t* offsets = rounds == 1 ? offset_of : A.offsets;
+    const int32_t* offsets = few ? offset_of : A.offsets;
     const int64_t begin = A.seqs ? offsets[0] : 0, end = A.seqs ? offsets[A.seqs] : 0;
     for (uint32_t t = threadIdx.x; t < A.tokens; t += kThreads) {
         int64_t slot = -1;
         if (t >= begin && t < end) {
             const uint32_t b = sequence_of(offsets, 0, A.seqs, t);
-            slot = slot_of<false>(A, rounds == 1 ? row_of[b] : rows[b], b, t, offsets[b]);
+            slot = slot_of(A, few ? row_of[b] : rows[b], b, t, offsets[b]);
         }
         A.slots[t] = slot;
     }
@@ -210,7 +235,7 @@ __global__ __launch_bounds__(256) void slots_kernel(KvPlan A, const Row* rows) {
         const uint32_t lo = sequence_of(A.offsets, 0, A.seqs, (uint32_t)(first < begin ? begin : first));
         const uint32_t hi = sequence_of(A.offsets, lo, A.seqs, (uint32_t)(last < end ? last : end - 1)) + 1;
         const uint32_t b = sequence_of(A.offsets, lo, hi, t);
-        slot = slot_of<true>(A, rows[b], b, t, A.offsets[b]);
+        slot = slot_of(A, rows[b], b, t, A.offsets[b]);
     }
     A.slots[t] = slot;
 }
