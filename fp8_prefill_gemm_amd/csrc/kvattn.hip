@@ -935,57 +935,73 @@ __global__ __launch_bounds__(kThreads, C <= 4 ? 2 : 1) void attend_kernel(KvAtte
             }
 }
 
-// Joins the parts of a sequence that several workers hold: a workgroup a query
-// head.  Four columns a lane, and the parts shared among the rows of lanes,
-// each with a running maximum of its own.
-template <int kJoin>
-__global__ __launch_bounds__(kJoin) void join_kernel(KvAttend A, Grid G) {
-    const uint32_t b = blockIdx.x / A.q_heads, qh = blockIdx.x % A.q_heads, group = A.q_heads / A.heads;
-    const uint32_t h = qh / group, z = qh % group / kHeads, row = qh % group % kHeads, lanes = A.heads * G.tiles;
+// A part's, or several parts', sums of 2^(score - m), four columns of them.
+struct Sums {
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o = {};
+    __device__ __forceinline__ void add(float m1, float l1, f32x4 o1) {
+        const float top = fmaxf(m, m1), base = base_of(top);
+        const float f = __builtin_amdgcn_exp2f(m - base), e = __builtin_amdgcn_exp2f(m1 - base);
+        o = o * f + o1 * e;
+        l = l * f + l1 * e;
+        m = top;
+    }
+    // Those of the lanes whose numbers differ in the bits from `off` on.
+    __device__ __forceinline__ void across(uint32_t off) {
+        for (; off < (uint32_t)kWave; off <<= 1) {
+            f32x4 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __shfl_xor(o[i], (int)off, kWave);
+            add(__shfl_xor(m, (int)off, kWave), __shfl_xor(l, (int)off, kWave), x);
+        }
+    }
+};
+
+// Joins the parts of a sequence that several workers hold: kWays waves a query
+// head and run of 32 columns, four columns a lane and eight parts a wave at a
+// time, a running maximum each.  Few sequences are in many parts each (131072
+// positions of one: 16 waves 4.3 us, a workgroup of 16 a head 6.9 us).
+constexpr uint32_t kManyWays = 16;
+template <uint32_t kWays>
+__global__ __launch_bounds__(kWays == 1 ? kThreads : kWays* kWave) void join_kernel(KvAttend A, Grid G) {
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const uint32_t runs = A.dim / 32u, job = kWays == 1 ? scalar(blockIdx.x * kWaves + wave) : blockIdx.x;
+    const uint32_t bh = job / runs, run = job % runs, b = bh / A.q_heads, qh = bh % A.q_heads;
+    if (b >= A.seqs) return;
+    const uint32_t h = qh / G.group, z = qh % G.group / kHeads, row = qh % G.group % kHeads, lanes = A.heads * G.tiles;
     const uint32_t* info = reinterpret_cast<const uint32_t*>(static_cast<const float*>(A.ws) + G.info);
     const uint32_t first = info[2 * b], count = info[2 * b + 1];
     if (count == 0) return;
     const uint64_t floats = part_floats(G.part_rows, A.dim);
-    const uint32_t cols = A.dim / 4u, ways = kJoin / cols, way = threadIdx.x / cols, col = threadIdx.x % cols * 4u;
-    float m = -INFINITY, l = 0.0f;
-    f32x4 o = {};
-    if (way < ways) {
-#pragma unroll 4
-        for (uint32_t i = way; i < count; i += ways) {
-            const float* p = static_cast<const float*>(A.ws) + (uint64_t)((first + i) * lanes + h * G.tiles + z) * floats;
-            const f32x4 v = *reinterpret_cast<const f32x4*>(p + row * A.dim + col);
-            const float mp = p[G.part_rows * A.dim + row], lp = p[G.part_rows * (A.dim + 1u) + row];
-            const float top = fmaxf(m, mp), base = base_of(top);
-            const float f = __builtin_amdgcn_exp2f(m - base), e = __builtin_amdgcn_exp2f(mp - base);
-            o = o * f + v * e;
-            l = l * f + lp * e;
-            m = top;
+    const uint32_t col = 32u * run + lane % 8u * 4u;
+    Sums x;
+#pragma unroll 2
+    for (uint32_t i = kWays == 1 ? lane / 8u : threadIdx.x / 8u; i < count; i += 8u * kWays) {
+        const float* p = static_cast<const float*>(A.ws) + (uint64_t)((first + i) * lanes + h * G.tiles + z) * floats;
+        x.add(p[G.part_rows * A.dim + row], p[G.part_rows * (A.dim + 1u) + row], *reinterpret_cast<const f32x4*>(p + row * A.dim + col));
+    }
+    x.across(8);
+    if constexpr (kWays > 1) {
+        __shared__ f32x4 o_of[kWays][8];
+        __shared__ float m_of[kWays][8], l_of[kWays][8];
+        if (lane < 8) {
+            o_of[wave][lane] = x.o;
+            m_of[wave][lane] = x.m;
+            l_of[wave][lane] = x.l;
         }
+        __syncthreads();
+        if (wave != 0) return;
+        x = Sums();
+#pragma unroll
+        for (uint32_t w = lane / 8; w < kWays; w += 8) x.add(m_of[w][lane % 8], l_of[w][lane % 8], o_of[w][lane % 8]);
+        x.across(8);
     }
-    __shared__ f32x4 o_of[kJoin];
-    __shared__ float m_of[kJoin], l_of[kJoin];
-    o_of[threadIdx.x] = o;
-    m_of[threadIdx.x] = m;
-    l_of[threadIdx.x] = l;
-    __syncthreads();
-    if (way != 0) return;
-    float top = m;
-#pragma unroll 8
-    for (uint32_t w = 1; w < ways; ++w) top = fmaxf(top, m_of[w * cols + threadIdx.x]);
-    const float base = base_of(top);
-    o = (f32x4){};
-    l = 0.0f;
-#pragma unroll 8
-    for (uint32_t w = 0; w < ways; ++w) {
-        const float e = __builtin_amdgcn_exp2f(m_of[w * cols + threadIdx.x] - base);
-        o += o_of[w * cols + threadIdx.x] * e;
-        l += l_of[w * cols + threadIdx.x] * e;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (lane >= 8) return;
+    const float inv = x.l == 0.0f ? 0.0f : 1.0f / x.l;
     const uint64_t head = (uint64_t)b * A.q_heads + qh;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put(A.out, G.dtype, head * A.dim + col + i, l == 0.0f ? 0.0f : o[i] * inv);
-    if (A.lse && threadIdx.x == 0) A.lse[head] = lse_of(top, l);
+    for (int i = 0; i < 4; ++i) put(A.out, G.dtype, head * A.dim + col + i, x.l == 0.0f ? 0.0f : x.o[i] * inv);
+    if (A.lse && lane == 0 && run == 0) A.lse[head] = lse_of(x.m, x.l);
 }
 
 // Workgroups of a launch: two a compute unit.
@@ -1061,11 +1077,11 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
             launch(std::false_type{});
     });
     if (!G.whole) {
-        // few sequences are in many parts each
+        const uint32_t jobs = A.seqs * A.q_heads * (A.dim / 32u);
         if (A.seqs < 8u)
-            join_kernel<1024><<<A.seqs * A.q_heads, 1024, 0, st>>>(A, G);
+            join_kernel<kManyWays><<<jobs, kManyWays * kWave, 0, st>>>(A, G);
         else
-            join_kernel<256><<<A.seqs * A.q_heads, 256, 0, st>>>(A, G);
+            join_kernel<1><<<(jobs + kWaves - 1) / kWaves, kThreads, 0, st>>>(A, G);
     }
     return hipGetLastError();
 }

@@ -369,32 +369,31 @@ constexpr uint32_t kBins = 2048;
 
 struct Pick {
     uint32_t count[kBins];
-    uint32_t part[2][kPickWaves];
-    uint32_t bin, above, in, low, high;
+    uint32_t part[2][2][kPickWaves];
+    uint32_t bin, above, in, low, high, some, forced;
 };
 
-// Sum of v over the lanes of the workgroup before this one, and over all.
-__device__ __forceinline__ uint32_t before(uint32_t v, uint32_t* part, uint32_t& all) {
-    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    uint32_t sum = v;
-    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x111, 0xF, 0xF, true);
-    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x112, 0xF, 0xF, true);
-    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x114, 0xF, 0xF, true);
-    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x118, 0xF, 0xF, true);
-    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x142, 0xA, 0xF, false);
-    sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x143, 0xC, 0xF, false);
-    if (lane == kWave - 1) part[wave] = sum;
-    __syncthreads();
-    uint32_t x = sum - v;
-    all = 0;
+// Sum of v over the wave's lanes up to and with this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
+    return v;
+}
+
+// Of each wave's value, the sum of those before this wave's and of all.
+__device__ __forceinline__ void wave_sums(const uint32_t* part, uint32_t& before, uint32_t& all) {
+    const uint32_t wave = threadIdx.x / kWave;
+    before = all = 0;
 #pragma unroll
     for (uint32_t i = 0; i < kPickWaves; ++i) {
         const uint32_t n = part[i];
-        x += i < wave ? n : 0;
+        before += i < wave ? n : 0;
         all += n;
     }
-    __syncthreads();
-    return x;
 }
 
 // The `budget` largest of keys[0 .. n), ascending by place, ties to the lower
@@ -403,32 +402,56 @@ __device__ __forceinline__ uint32_t before(uint32_t v, uint32_t* part, uint32_t&
 // between that bin's ends, and so on: two or three rounds, whose counts fall on
 // many bins (counts by a key's upper bits fall on a few, as scores are alike).
 // Infinite scores, the forced ones, are counted apart: they would stretch the
-// bins.
+// bins.  A wave has a run of 64 HELD places at most in its registers (HELD 0: of
+// any length, where they lie).
+template <int HELD>
 __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, uint32_t budget, int32_t* out) {
-    uint32_t low = 0xFFFFFFFFu, high = 0, some = 0, forced = 0;  // of those that can be taken
-    for (uint32_t i = threadIdx.x; i < n; i += kPick) {
-        const uint32_t k = keys[i];
-        if (k == kForced) {
-            ++forced;
-        } else if (k) {
-            low = low < k ? low : k;
-            high = high > k ? high : k;
-            ++some;
-        }
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const uint32_t turns = (n + kPick - 1) / kPick, first = wave * turns * kWave + lane;
+    uint32_t held[HELD ? HELD : 1];
+    if constexpr (HELD != 0) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) held[j] = (uint32_t)j < turns && first + j * kWave < n ? keys[first + j * kWave] : 0u;
     }
-    if (threadIdx.x == 0) P.low = 0xFFFFFFFFu, P.high = 0;
+    auto each = [&](auto&& f) {  // f(place, key) of all of the lane's places, 0 for the keys behind the last; whole waves
+        if constexpr (HELD != 0) {
+#pragma unroll
+            for (int j = 0; j < HELD; ++j)
+                if ((uint32_t)j < turns) f(first + j * kWave, held[j]);
+        } else {
+            for (uint32_t j = 0; j < turns; ++j) f(first + j * kWave, first + j * kWave < n ? keys[first + j * kWave] : 0u);
+        }
+    };
+    for (uint32_t i = threadIdx.x; i < kBins; i += kPick) P.count[i] = 0;
+    if (threadIdx.x == 0) {
+        P.low = 0xFFFFFFFFu;
+        P.high = P.some = P.forced = 0;
+    }
     __syncthreads();
+    // key - 1 and key + 2^23 put those that cannot be taken behind the smallest, the forced ones before the largest
+    static_assert((uint32_t)(kForced + 0x00800000u) == 0u);
+    uint32_t low = 0xFFFFFFFFu, high = 0, some = 0, forced = 0;  // the counts are the wave's
+    each([&](uint32_t, uint32_t k) {
+        forced += (uint32_t)__popcll(__ballot(k == kForced));
+        some += (uint32_t)__popcll(__ballot(k != 0));
+        low = k - 1u < low ? k - 1u : low;
+        high = k + 0x00800000u > high ? k + 0x00800000u : high;
+    });
+    some -= forced;
     high = wave_max_u32(high);
     low = ~wave_max_u32(~low);
-    if (threadIdx.x % kWave == 0 && high) {
-        atomicMin(&P.low, low);
-        atomicMax(&P.high, high);
+    if (lane == 0) {
+        if (some) {
+            atomicMin(&P.low, low + 1u);
+            atomicMax(&P.high, high - 0x00800000u);
+            atomicAdd(&P.some, some);
+        }
+        if (forced) atomicAdd(&P.forced, forced);
     }
-    uint32_t total, always;
-    before(some, P.part[0], total);  // barriers
-    before(forced, P.part[1], always);
+    __syncthreads();
     low = P.low;
     high = P.high;
+    const uint32_t total = P.some, always = P.forced;
     // the threshold: every key above it is taken, and `left` of those equal to it
     uint32_t threshold = 0, left = 0;
     if (always >= budget) {
@@ -436,18 +459,22 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
         left = budget;
     } else if (total > budget - always) {
         left = budget - always;
-        for (;;) {
+        for (uint32_t round = 0;; ++round) {
             const uint32_t span = high - low, shift = span < kBins ? 0 : 21 - (uint32_t)__builtin_clz(span);  // span >> shift < 2048
-            for (uint32_t i = threadIdx.x; i < kBins; i += kPick) P.count[i] = 0;
-            __syncthreads();
-            for (uint32_t i = threadIdx.x; i < n; i += kPick) {
-                const uint32_t k = keys[i];
+            each([&](uint32_t, uint32_t k) {
                 if (k >= low && k <= high) atomicAdd(&P.count[(k - low) >> shift], 1u);
-            }
+            });
             __syncthreads();
             // lane t holds the bins 2047 - 2 t and 2046 - 2 t: sums run from the largest keys down
-            const uint32_t x = P.count[kBins - 1 - 2 * threadIdx.x], y = P.count[kBins - 2 - 2 * threadIdx.x];
-            uint32_t all, above = before(x + y, P.part[0], all);
+            uint32_t* bins = &P.count[kBins - 2 - 2 * threadIdx.x];
+            const uint32_t x = bins[1], y = bins[0], sum = wave_scan(x + y);
+            bins[0] = bins[1] = 0;  // for the next round
+            uint32_t* part = P.part[round & 1][0];
+            if (lane == kWave - 1) part[wave] = sum;
+            __syncthreads();
+            uint32_t above, all;
+            wave_sums(part, above, all);
+            above += sum - (x + y);
             if (above < left && above + x >= left) {
                 P.bin = kBins - 1 - 2 * threadIdx.x;
                 P.above = above;
@@ -471,29 +498,42 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
         }
         threshold = low;
     }
-    // a lane a run of consecutive places, so that two sums over the lanes say where each goes
-    const uint32_t per = (n + kPick - 1) / kPick, i0 = threadIdx.x * per < n ? threadIdx.x * per : n, i1 = i0 + per < n ? i0 + per : n;
-    uint32_t equal = 0, over = 0, all;
-    for (uint32_t i = i0; i < i1; ++i) {
-        const uint32_t k = keys[i];
-        equal += k != 0 && k == threshold;
-        over += k > threshold;
+    // where each wave's taken ones go
+    uint32_t over = 0, equal = 0;
+    each([&](uint32_t, uint32_t k) {
+        over += (uint32_t)__popcll(__ballot(k > threshold));
+        equal += (uint32_t)__popcll(__ballot(k != 0 && k == threshold));
+    });
+    __syncthreads();
+    if (lane == 0) {
+        P.part[0][0][wave] = over;
+        P.part[0][1][wave] = equal;
     }
-    uint32_t rank = before(equal, P.part[0], all);
-    const uint32_t mine = rank < left ? (left - rank < equal ? left - rank : equal) : 0;
-    uint32_t taken, at = before(over + mine, P.part[1], taken);
-    for (uint32_t i = i0; i < i1; ++i) {
-        const uint32_t k = keys[i];
-        if (k > threshold || (k != 0 && k == threshold && rank++ < left)) out[at++] = (int32_t)i;
-    }
+    __syncthreads();
+    uint32_t at, rank, overs, equals;
+    wave_sums(P.part[0][0], at, overs);
+    wave_sums(P.part[0][1], rank, equals);
+    at += rank < left ? rank : left;
+    const uint32_t taken = overs + (equals < left ? equals : left);
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    each([&](uint32_t place, uint32_t k) {
+        const bool same = k != 0 && k == threshold;
+        const uint64_t sames = __ballot(same);
+        const bool mine = k > threshold || (same && rank + (uint32_t)__popcll(sames & below) < left);
+        const uint64_t all = __ballot(mine);
+        if (mine) out[at + (uint32_t)__popcll(all & below)] = (int32_t)place;
+        rank += (uint32_t)__popcll(sames);
+        at += (uint32_t)__popcll(all);
+    });
     for (uint32_t i = taken + threadIdx.x; i < budget; i += kPick) out[i] = -1;
 }
 
-// Few pages a sequence, or many sequences: a workgroup scores all pages of its
-// (sequence, key head) into its LDS and picks from there.
+// Few pages a sequence: a workgroup scores all pages of its (sequence, key
+// head) into its LDS and picks from there.
+constexpr uint32_t kOnePages = 512;
 template <int C>
 __global__ __launch_bounds__(kPick) void select_kernel(KvSelect A) {
-    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t keys[kOnePages];
     __shared__ union {
         Queries q;
         Pick p;
@@ -501,34 +541,24 @@ __global__ __launch_bounds__(kPick) void select_kernel(KvSelect A) {
     const uint32_t b = blockIdx.x / A.heads, h = blockIdx.x % A.heads, used = used_pages(A, b);
     score_pages<C, kPick>(A, S.q, b, h, 0, used, used, keys);
     __syncthreads();
-    pick(S.p, keys, used, A.budget, A.pages + (uint64_t)blockIdx.x * A.budget);
+    pick<1>(S.p, keys, used, A.budget, A.pages + (uint64_t)blockIdx.x * A.budget);
 }
 
-// Otherwise workgroups of their own score kSpan pages each, and a second launch picks.
-constexpr uint32_t kSpan = 64;
+// Otherwise workgroups of their own score `span` pages each, and a second launch picks.
 template <int C>
-__global__ __launch_bounds__(kThreads) void score_kernel(KvSelect A, uint32_t* keys, uint32_t spans) {
+__global__ __launch_bounds__(kThreads) void score_kernel(KvSelect A, uint32_t* keys, uint32_t span, uint32_t spans) {
     __shared__ Queries Q;
-    const uint32_t bh = blockIdx.x / spans, b = bh / A.heads, h = bh % A.heads, first = blockIdx.x % spans * kSpan, used = used_pages(A, b);
+    const uint32_t bh = blockIdx.x / spans, b = bh / A.heads, h = bh % A.heads, first = blockIdx.x % spans * span, used = used_pages(A, b);
     if (first >= used) return;
-    const uint32_t last = used - first < kSpan ? used : first + kSpan;
+    const uint32_t last = used - first < span ? used : first + span;
     score_pages<C, kThreads>(A, Q, b, h, first, last, used, keys + (uint64_t)bh * A.max_pages + first);
 }
 
-constexpr uint32_t kHeld = 32768;  // keys that the picking workgroup copies to its LDS
-__global__ __launch_bounds__(kPick) void pick_kernel(KvSelect A, const uint32_t* keys, bool held) {
-    extern __shared__ uint32_t copy[];
+template <int HELD>
+__global__ __launch_bounds__(kPick) void pick_kernel(KvSelect A, const uint32_t* keys) {
     __shared__ Pick P;
     const uint32_t used = used_pages(A, blockIdx.x / A.heads);
-    keys += (uint64_t)blockIdx.x * A.max_pages;
-    int32_t* out = A.pages + (uint64_t)blockIdx.x * A.budget;
-    if (held) {
-        for (uint32_t i = threadIdx.x; i < used; i += kPick) copy[i] = keys[i];
-        __syncthreads();
-        pick(P, copy, used, A.budget, out);
-    } else {
-        pick(P, keys, used, A.budget, out);
-    }
+    pick<HELD>(P, keys + (uint64_t)blockIdx.x * A.max_pages, used, A.budget, A.pages + (uint64_t)blockIdx.x * A.budget);
 }
 
 template <typename F>
@@ -541,11 +571,13 @@ void with_steps(uint32_t c, F&& f) {
     }
 }
 
-// One launch where a workgroup's pages are few, or the workgroups many: 2048
-// pages of 128 columns are 512 KB of bounds for one of them.
-bool one_launch(uint32_t seqs, uint32_t heads, uint32_t max_pages) {
-    return max_pages <= 1024u || (max_pages <= 4096u && (uint64_t)seqs * heads >= 128u);
-}
+// Scoring workgroups are more only where a tile a wave is not: each holds the queries once (2048 instead: 25.6 and 23.4 us).
+constexpr uint32_t kScorers = 1024;
+
+// 4 key heads, 7 queries each, 128 columns, us in one launch and in two: 16
+// sequences of 256 pages 9.6, 10.4; of 512 12.0, 11.2; of 1024 16.3, 12.9; 64 of
+// 512 13.8, 16.9; 32 of 2048 26.3, 23.4; one of 4096 39.9, 11.7.
+bool one_launch(uint32_t max_pages) { return max_pages <= kOnePages; }
 
 }  // namespace
 
@@ -582,22 +614,28 @@ hipError_t launch_kv_bounds(int format, const KvBounds& A, hipStream_t st) {
 }
 
 size_t kv_select_ws_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages) {
-    return one_launch(seqs, heads, max_pages) ? 0 : (size_t)seqs * heads * max_pages * 4u;
+    return one_launch(max_pages) ? 0 : (size_t)seqs * heads * max_pages * 4u;
 }
 
 hipError_t launch_kv_select(const KvSelect& A, hipStream_t st) {
     const uint32_t pairs = A.seqs * A.heads;
     with_steps(A.dim / 32u, [&](auto c_) {
         constexpr int C = decltype(c_)::value;
-        if (one_launch(A.seqs, A.heads, A.max_pages)) {
-            select_kernel<C><<<pairs, kPick, A.max_pages * 4u, st>>>(A);
+        if (one_launch(A.max_pages)) {
+            select_kernel<C><<<pairs, kPick, 0, st>>>(A);
             return;
         }
         uint32_t* keys = static_cast<uint32_t*>(A.ws);
-        const uint32_t spans = (A.max_pages + kSpan - 1) / kSpan;
-        score_kernel<C><<<pairs * spans, kThreads, 0, st>>>(A, keys, spans);
-        const bool held = A.max_pages <= kHeld;
-        pick_kernel<<<pairs, kPick, held ? A.max_pages * 4u : 0u, st>>>(A, keys, held);
+        // a tile a wave, or more where that is more than eight workgroups a compute unit: each holds the queries once
+        const uint64_t tiles = (uint64_t)pairs * ((A.max_pages + 63u) / 64u) / kScorers;
+        const uint32_t span = 64u * (uint32_t)(tiles < 1 ? 1 : tiles < 16 ? tiles : 16), spans = (A.max_pages + span - 1) / span;
+        score_kernel<C><<<pairs * spans, kThreads, 0, st>>>(A, keys, span, spans);
+        if (A.max_pages <= 8u * kPick)
+            pick_kernel<8><<<pairs, kPick, 0, st>>>(A, keys);
+        else if (A.max_pages <= 32u * kPick)
+            pick_kernel<32><<<pairs, kPick, 0, st>>>(A, keys);
+        else
+            pick_kernel<0><<<pairs, kPick, 0, st>>>(A, keys);
     });
     return hipGetLastError();
 }
