@@ -356,9 +356,12 @@ struct Parts {
     uint32_t part[2];
 };
 __device__ __forceinline__ Parts split2(float a, float b) {
-    const f16x2 h = {(_Float16)a, (_Float16)b};
+    uint32_t first = bits((f16x2){(_Float16)a, (_Float16)b});
     float minus = -1.0f;
-    asm("" : "+s"(minus));  // kept a factor, so that one instruction widens and subtracts
+    // `first` as it is (of a product, the compiler would round it for its own use and, fused, once more for the difference: another
+    // value at a tie); -1 kept a factor, so that one instruction widens and subtracts
+    asm("" : "+v"(first), "+s"(minus));
+    const f16x2 h = __builtin_bit_cast(f16x2, first);
     const f16x2 l = {(_Float16)__builtin_fmaf((float)h.x, minus, a), (_Float16)__builtin_fmaf((float)h.y, minus, b)};
     return {{bits(h), bits(l)}};
 }

@@ -76,9 +76,9 @@ def paged(page, lens, seed, spare=3, width=None):
     return table, np.array(used, dtype=np.int64), pages * page
 
 
-def check(got, lse, want, kind, rows=None):
-    """Every value within the oracle's bound and half a step of its type; the whole within what independent errors of that
-    size make: the bound's sums taken as square roots of their lengths, at least 2^-19."""
+def check(got, lse, want, kind, whole=2.0 ** -19):
+    """Every value within the oracle's bound and half a step of its type; the whole within `whole`, what independent errors
+    of that size make: the bound's sums taken as square roots of their lengths, at least 2^-19."""
     out, lref, tol, ltol = want
     unit = TYPES[kind][1]
     got = got.double().cpu().numpy()
@@ -86,7 +86,7 @@ def check(got, lse, want, kind, rows=None):
     assert (np.abs(got - out) <= tol * (1 + unit) + np.abs(out) * unit + (2.0 ** -25 if kind == "f16" else 0)).all()
     norm = np.linalg.norm(out)
     if norm:
-        assert np.linalg.norm(got - out) <= norm * (2.0 ** -19 + unit * 1.01)
+        assert np.linalg.norm(got - out) <= norm * (whole + unit * 1.01)
     if lse is not None:
         lse = host(lse).astype(np.float64)
         empty = np.isneginf(lref)
@@ -138,6 +138,64 @@ def test_every_dim(rz, fmt, dim):
 def test_long_sequences(rz, fmt, page, lens, heads, group, dim):
     """Sequences that are split over workgroups and joined."""
     case(rz, fmt, page, lens, heads, group, dim)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("seqs,heads,group,dim,page,longest", [(200, 8, 1, 64, 16, 5000), (700, 1, 3, 32, 5, 2000), (1300, 2, 9, 32, 16, 1500), (65, 4, 2, 96, 32, 3000)])
+def test_ragged_batches(rz, fmt, seqs, heads, group, dim, page, longest):
+    """More sequences than a wave looks at at once and than there are workers; many of none or a few positions, the last long."""
+    g = W.rng(seqs)
+    lens = [int(n) for n in g.integers(0, 40, seqs) * (g.random(seqs) < 0.7)]
+    lens[seqs // 3], lens[-1] = longest // 2, longest
+    case(rz, fmt, page, lens, heads, group, dim, seed=seqs)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("growth", [1, -1])
+def test_values_that_grow(rz, fmt, growth):
+    """One workgroup's run of thousands of positions whose values grow, and shrink, by powers of two along it: 500 positions
+    make the result, so its 8 n + 64 roundings of 2^-24 are 4064, sqrt(4064) 2^-24 = 2^-18.0 if they are independent."""
+    n, page, heads, group, dim = 5000, 16, 1, 3, 64
+    table, used, slots = paged(page, [n], 70)
+    cache = raw_cache(fmt, slots, heads, dim, 70)
+    fill(fmt, cache, used, 71)
+    up = np.arange(n) // 500 * 12 * growth
+    if fmt == kv_cache.E4M3:
+        cache[3][used] *= np.exp2(up)[:, None].astype(np.float32)
+    else:
+        cache[3][used] = (cache[3][used].astype(np.int64) + (up - (108 if growth > 0 else 0))[:, None, None]).clip(0, 254).astype(np.uint8)
+    q = W.act_normal(72, 1, heads * group * dim).reshape(1, heads * group, dim)
+    k, v = (kv_serve.values(fmt, *c) for c in (cache[:2], cache[2:]))
+    d = [dev(c) for c in cache] + [dev(table), dev(np.array([n], dtype=np.int32)), dev(q)]
+    p = [ctypes.c_void_p(t.data_ptr()) for t in d]
+    for lens in ([n], [1025], [1024], [2049]):
+        want = kv_serve.attention(k, v, q, page, table, lens, 0.1)
+        d[5].copy_(torch.tensor(lens, dtype=torch.int32))
+        out = torch.empty((1, heads * group, dim), device="cuda")
+        torch.cuda.synchronize()
+        assert rz.lib().rz_kv_attention(fmt, p[6], heads * group, heads * group * dim, *p[:4], slots, heads, dim, page, p[4], 1,
+                                        table.shape[1], p[5], None, 0, 0.1, 0, ctypes.c_void_p(out.data_ptr()), None, None, None) == 0
+        check(out, None, want, "f32", 2.0 ** -18)
+        check(run(rz, fmt, cache, d[6], page, table, lens, 0.1)[0], None, want, "f32", 2.0 ** -18)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_two_calls_at_once(rz, fmt):
+    """Two batches on two streams, many times over, each with a workspace of its own: the bits of one after the other."""
+    page, heads, group, dim = 16, 2, 4, 64
+    sets = []
+    for i, lens in enumerate(([3000, 5, 0, 700], [1500] * 3)):
+        table, used, slots = paged(page, lens, 73 + i)
+        cache = raw_cache(fmt, slots, heads, dim, 73 + i)
+        fill(fmt, cache, used, 75 + i)
+        q = dev(W.act_normal(77 + i, len(lens), heads * group * dim).reshape(len(lens), heads * group, dim))
+        sets.append((q, *[dev(c) for c in cache], page, dev(table), dev(np.array(lens, dtype=np.int32)), 0.1))
+    want = [rz.rz_kv_attention(fmt, *a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [rz.rz_kv_attention(fmt, *sets[i % 2], stream=streams[i % 2]) for i in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(got))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

@@ -144,6 +144,21 @@ def test_bounds(rz, fmt, page, lens, before, heads, dim):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+def test_bounds_of_many_pages(rz, fmt):
+    """A prompt's pages by more tokens than a workgroup looks over, the same slot named twice, each page's last filled in part."""
+    page, heads, dim, lens = 3, 5, 32, [4001, 2, 5003]
+    table, used, slots = paged(page, lens, 46)
+    cache = raw_cache(fmt, slots, heads, dim, 47)
+    fill(fmt, cache, used, 48)
+    named = np.repeat(used, 2)
+    codes, scales = np.zeros((slots // page, heads, 2, dim), dtype=np.int8), np.zeros((slots // page, heads), dtype=np.float32)
+    dc, ds = dev(codes), dev(scales)
+    rz.rz_kv_bounds(fmt, dev(cache[0]), dev(cache[1]), dev(named), page, dc, ds)
+    kv_serve.bounds(kv_serve.values(fmt, *cache[:2]), named, page, codes, scales)
+    assert np.array_equal(host(dc), codes) and np.array_equal(host(ds), scales)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_bounds_of_special_rows(rz, fmt):
     """NaN and infinite rows, zeros, tiny and huge ones; slots that are none; a cache that ends inside a page."""
     page, heads, dim, slots = 4, 2, 64, 30
@@ -185,7 +200,8 @@ def ranked(pages, heads, dim, seed, kinds=0):
 @pytest.mark.parametrize("page,lens,heads,group,dim,budget,kinds", [
     (16, [37], 4, 7, 128, 2, 0), (16, [1, 0, 160, 161], 1, 1, 32, 4, 0), (64, [64 * 300, 64 * 299 + 1, 5], 2, 16, 64, 20, 0), (1, [1500, 1024, 1025], 3, 2, 96, 256, 0),
     (16, [16 * 700, 999], 2, 3, 256, 1, 0), (16, [16 * 900], 2, 17, 160, 300, 5), (32, [32 * 64] * 9, 2, 5, 512, 63, 3), (128, [50000, 130, 128], 1, 40, 192, 64, 0),
-    (1, [9000], 1, 2, 64, 4000, 7), (16, [300, 300], 8, 1, 128, 1000, 0), (1, [30000, 7], 1, 3, 32, 900, 0), (1, [40000], 2, 1, 32, 37, 0), (1, [4096] * 9, 16, 1, 32, 129, 50)])
+    (1, [9000], 1, 2, 64, 4000, 7), (16, [300, 300], 8, 1, 128, 1000, 0), (1, [30000, 7], 1, 3, 32, 900, 0), (1, [40000], 2, 1, 32, 37, 0), (1, [4096] * 9, 16, 1, 32, 129, 50),
+    (1, [512, 511, 1], 2, 2, 64, 60, 0), (1, [513, 512, 3], 2, 2, 64, 60, 0), (2, [16384, 7], 1, 2, 96, 500, 9), (2, [16386], 1, 2, 96, 500, 0), (1, [32768], 1, 1, 32, 4097, 3)])
 def test_select(rz, page, lens, heads, group, dim, budget, kinds):
     """One page to thousands, budgets below and above them, many equal scores, more queries than a tile holds."""
     print(f"select page={page} lens={lens} heads={heads} group={group} dim={dim} budget={budget}", flush=True)
