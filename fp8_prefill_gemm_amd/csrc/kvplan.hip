@@ -242,7 +242,9 @@ __global__ __launch_bounds__(256) void slots_kernel(KvPlan A, const Row* rows) {
 
 }  // namespace
 
-size_t kv_plan_ws_bytes(uint32_t seqs, uint32_t) { return (size_t)seqs * sizeof(Row); }
+size_t kv_plan_ws_bytes(uint32_t seqs, uint32_t tokens) {
+    return seqs <= (uint32_t)kThreads && tokens <= kOneLaunch ? 0 : (size_t)seqs * sizeof(Row);  // 0: the rows stay in LDS
+}
 
 hipError_t launch_kv_plan(const KvPlan& A, hipStream_t st) {
     Row* rows = static_cast<Row*>(A.ws);

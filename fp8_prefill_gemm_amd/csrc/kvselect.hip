@@ -134,18 +134,42 @@ __device__ __forceinline__ uint32_t slot_at(const KvBounds& A, uint64_t t) {
     return s < 0 || (uint64_t)s >= A.num_slots ? kNone : (uint32_t)s;
 }
 
-// How far `page` is filled by the tokens from t on that follow each other in
-// it: the largest of them counts.  By a wave.
-__device__ __forceinline__ uint32_t filled_from(const KvBounds& A, uint64_t t, uint32_t page) {
-    const uint32_t lane = threadIdx.x % kWave;
+// f over the lanes whose numbers differ in the bits from kFrom to below kTo.
+template <int kFrom, int kTo, typename F>
+__device__ __forceinline__ float across(float v, F&& f) {
+    auto lane = [&](auto c) { return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), decltype(c)::value, 0xF, 0xF, true)); };
+    if constexpr (kFrom <= 1 && kTo > 1) v = f(v, lane(std::integral_constant<int, 0xB1>{}));  // 1 0 3 2
+    if constexpr (kFrom <= 2 && kTo > 2) v = f(v, lane(std::integral_constant<int, 0x4E>{}));  // 2 3 0 1
+    static_assert(kFrom == 1 || kFrom >= 8);
+    if constexpr (kFrom == 1 && kTo > 4) v = f(v, lane(std::integral_constant<int, 0x141>{}));  // 7 - l, alike in fours
+    if constexpr (kFrom <= 8 && kTo > 8) v = f(v, lane(std::integral_constant<int, 0x128>{}));  // l + 8 of 16
+    if constexpr (kFrom <= 16 && kTo > 16) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    }
+    if constexpr (kFrom <= 32 && kTo > 32) {
+        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    }
+    return v;
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+
+// How far `page` is filled by token t + l and those that follow it there, the
+// lanes holding the slots of tokens t on: the largest of them counts.
+__device__ __forceinline__ uint32_t filled_from(const KvBounds& A, uint64_t t, uint32_t s, int l, uint32_t page) {
+    const uint32_t lane = threadIdx.x % kWave, row0 = page * A.page_len;
     uint32_t top = 0;
-    for (;; t += kWave) {
-        const uint32_t s = slot_at(A, t + lane);
-        const uint64_t out = ~__ballot(s != kNone && s / A.page_len == page);
-        const uint32_t n = out ? (uint32_t)__ffsll((unsigned long long)out) - 1 : kWave;  // lanes that follow on
-        const uint32_t at = lane < n ? s - page * A.page_len + 1 : 0;
+    for (;;) {
+        const uint64_t out = ~__ballot(s - row0 < A.page_len) >> l << l;
+        const uint32_t n = out ? (uint32_t)__ffsll((unsigned long long)out) - 1 : kWave;  // lanes l to n - 1 follow on
+        const uint32_t at = lane >= (uint32_t)l && lane < n ? s - row0 + 1 : 0;
         top = top > at ? top : at;
         if (n < kWave) break;
+        t += kWave;
+        l = 0;
+        s = slot_at(A, t + lane);
     }
     return wave_max_u32(top);
 }
@@ -158,11 +182,12 @@ __global__ __launch_bounds__(kThreads) void bounds_step_kernel(KvBounds A) {
     constexpr uint32_t ways = kThreads / L;
     __shared__ float of[17][kThreads];  // column first: no two lanes in a bank
     const uint32_t t = blockIdx.x / A.heads, head = blockIdx.x % A.heads, part = threadIdx.x % L, way = threadIdx.x / L;
-    const uint32_t s = slot_at(A, t), prior = t ? slot_at(A, t - 1) : kNone;
+    const uint32_t next = slot_at(A, (uint64_t)t + threadIdx.x % kWave), prior = t ? slot_at(A, t - 1) : kNone;
+    const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)next);
     if (s == kNone) return;
     const uint32_t page = s / A.page_len;
     if (page >= A.num_pages || (prior != kNone && prior / A.page_len == page)) return;
-    const uint32_t filled = filled_from(A, t, page);
+    const uint32_t filled = filled_from(A, t, next, 0, page);
     Ends x;
     const bool live = part * 8u < A.dim;
     if (live) x.template rows<FMT, 4>(A, (uint64_t)page * A.page_len * A.heads + head, part, way, ways, filled);
@@ -183,9 +208,7 @@ __global__ __launch_bounds__(kThreads) void bounds_step_kernel(KvBounds A) {
         }
         x.bad = fmaxf(x.bad, of[16][w * L + part]);
     }
-    float a = live ? x.largest() : 0.0f;
-#pragma unroll
-    for (int off = 1; off < L; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));
+    const float a = across<1, L>(live ? x.largest() : 0.0f, larger);
     if (live) x.write(A, (uint64_t)page * A.heads + head, part, a);
 }
 
@@ -196,9 +219,9 @@ __global__ __launch_bounds__(kThreads) void bounds_prompt_kernel(KvBounds A, uin
     constexpr uint32_t ways = kWave / L;
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, part = lane % L, way = lane / L;
     const uint64_t t0 = (uint64_t)blockIdx.x * per;
-    const uint32_t s = lane < per ? slot_at(A, t0 + lane) : kNone, prior = lane < per && t0 + lane ? slot_at(A, t0 + lane - 1) : kNone;
+    const uint32_t s = slot_at(A, t0 + lane), prior = t0 + lane ? slot_at(A, t0 + lane - 1) : kNone;
     const uint32_t mine = s == kNone ? kNone : s / A.page_len;
-    const bool leads = mine < A.num_pages && !(prior != kNone && prior / A.page_len == mine);
+    const bool leads = lane < per && mine < A.num_pages && !(prior != kNone && prior / A.page_len == mine);
     const bool live = part * 8u < A.dim;
     uint32_t turn = 0;
     for (uint64_t todo = __ballot(leads); todo; todo &= todo - 1) {
@@ -207,21 +230,16 @@ __global__ __launch_bounds__(kThreads) void bounds_prompt_kernel(KvBounds A, uin
         uint32_t filled = 0;
         for (uint32_t head = 0; head < A.heads; ++head, ++turn) {
             if (turn % (kThreads / kWave) != wave) continue;
-            if (filled == 0) filled = filled_from(A, t0 + l, page);
+            if (filled == 0) filled = filled_from(A, t0, s, l, page);
             Ends x;
-            if (live) x.template rows<FMT, 8>(A, (uint64_t)page * A.page_len * A.heads + head, part, way, ways, filled);
+            if (live) x.template rows<FMT, 4>(A, (uint64_t)page * A.page_len * A.heads + head, part, way, ways, filled);
 #pragma unroll
-            for (int off = L; off < kWave; off <<= 1) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x.hi[j] = fmaxf(x.hi[j], __shfl_xor(x.hi[j], off, kWave));
-                    x.lo[j] = fminf(x.lo[j], __shfl_xor(x.lo[j], off, kWave));
-                }
-                x.bad = fmaxf(x.bad, __shfl_xor(x.bad, off, kWave));
+            for (int j = 0; j < 8; ++j) {
+                x.hi[j] = across<L, kWave>(x.hi[j], larger);
+                x.lo[j] = across<L, kWave>(x.lo[j], smaller);
             }
-            float a = live ? x.largest() : 0.0f;
-#pragma unroll
-            for (int off = 1; off < L; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));
+            x.bad = across<L, kWave>(x.bad, larger);
+            const float a = across<1, L>(live ? x.largest() : 0.0f, larger);
             if (live && way == 0) x.write(A, (uint64_t)page * A.heads + head, part, a);
         }
     }
@@ -583,10 +601,10 @@ bool one_launch(uint32_t max_pages) { return max_pages <= kOnePages; }
 
 hipError_t launch_kv_bounds(int format, const KvBounds& A, hipStream_t st) {
     const uint32_t lanes = A.dim <= 64 ? 8 : A.dim <= 128 ? 16 : A.dim <= 256 ? 32 : 64;
-    // up to 2048 (token, head) pairs a workgroup each; more: 16 tokens a workgroup, fewer where those would not fill the CUs
-    // (each token of a step leads)
+    // up to 2048 (token, head) pairs a workgroup each; more: as many tokens a workgroup as 1024 of them need, as each costs its
+    // launch (32768 tokens, us: 8 a workgroup 25, 16 16, 32 12.8, 64 14; and 11.7 with 4 rows a lane in flight instead of 8)
     const bool step = (uint64_t)A.tokens * A.heads <= 2048u;
-    const uint32_t per = A.tokens / 1024u < 1u ? 1u : A.tokens / 1024u < 16u ? A.tokens / 1024u : 16u;
+    const uint32_t per = A.tokens / 1024u < 1u ? 1u : A.tokens / 1024u < 64u ? A.tokens / 1024u : 64u;
     const uint32_t grid = step ? A.tokens * A.heads : (A.tokens + per - 1) / per;
     auto launch = [&](auto l_) {
         constexpr int L = decltype(l_)::value;
