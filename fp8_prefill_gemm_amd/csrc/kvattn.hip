@@ -25,14 +25,20 @@
 // largest scale of the values so far, so that what is lost lies 2^-38 below
 // the largest value times its weight.
 //
-// Workgroups take equal shares of all blocks of 128 positions, whatever the
-// sequences' lengths: worker r of R reads its run of the blocks that the batch
-// has, for one key head (and 16 of its queries); the heads of the same blocks
-// go to one XCD, so that a page's lines, which hold rows of several heads, are
-// fetched once (24 sequences of 131072 positions in all, MXFP4 rows of 64 bytes: 46 -> 42
-// us).
-// What is not the whole of a sequence goes to the workspace, at most two parts
-// a worker, and a second launch joins them.
+// Workgroups take nearly equal units of the batch's blocks of 128 positions,
+// whatever the sequences' lengths, one key head (and 16 of its queries) each;
+// the heads of the same blocks go to one XCD, so that a page's lines, which hold
+// rows of several heads, are fetched once (24 sequences of 131072 positions in
+// all, MXFP4 rows of 64 bytes: 46 -> 42 us).  What is not the whole of a sequence
+// goes to the workspace, and a second launch joins it.
+//
+// Measured (4 key heads of 128 columns, 7 queries each; MXFP4 8): 131072
+// positions of one sequence E4M3 34.8 us, 4.0 TB/s of its rows, the loop itself
+// at 7 TB/s; 64 sequences of 65536 in all 20.7; 24 sequences of 131072 in all
+// MXFP4 26.4, 2.7 TB/s.  E4M3 is bound by memory in the loop and by what comes
+// before and after it (lengths, tables, rows and scales are loads that wait for
+// each other, 6 us; the join's launch, 4), MXFP4 by its vector instructions
+// (about 270 a wave and 32 positions, half of them to widen codes).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -962,8 +968,10 @@ struct Sums {
 
 // Joins the parts of a sequence that several workers hold: kWays waves a query
 // head and run of 32 columns, four columns a lane and eight parts a wave at a
-// time, a running maximum each.  Few sequences are in many parts each (131072
-// positions of one: 16 waves 4.3 us, a workgroup of 16 a head 6.9 us).
+// time, a running maximum each.  Few sequences are in many parts each: 16 waves
+// a run (131072 positions of one sequence 4.9 us; 16 waves a head and all its
+// columns 6.9).  Many: one, four a workgroup (64 sequences, with the attention
+// 24.4 us; two waves a run and as many workgroups as runs 25.9).
 constexpr uint32_t kManyWays = 16;
 template <uint32_t kWays>
 __global__ __launch_bounds__(kWays == 1 ? kThreads : kWays* kWave) void join_kernel(KvAttend A, Grid G) {
@@ -1081,7 +1089,7 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
     });
     if (!G.whole) {
         const uint32_t jobs = A.seqs * A.q_heads * (A.dim / 32u);
-        if (A.seqs < 8u)
+        if (A.seqs < 8u && jobs <= 0x10000u)  // lanes of a launch are counted in 32 bits
             join_kernel<kManyWays><<<jobs, kManyWays * kWave, 0, st>>>(A, G);
         else
             join_kernel<1><<<(jobs + kWaves - 1) / kWaves, kThreads, 0, st>>>(A, G);

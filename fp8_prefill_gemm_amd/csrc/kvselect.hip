@@ -8,6 +8,12 @@
 // columns: exact in fp32 as well), the same in any order, and the choice by it
 // has no rounding to depend on.  To its roundings it is an upper bound of n . k
 // for every key k of the page.
+//
+// Few bytes are moved for each launch, so latency counts: the loads that wait for
+// each other (slots, rows; lengths, tables, bounds; keys) and the barriers of
+// the choice.  4 key heads of 128 columns: bounds of 64 pages of 64 rows 6.0 us, of a
+// 32768-token prompt 8.8 (1.2 TB/s); scores of 8192 pages of 32 sequences 7.6
+// and their choice 6.3; of 8192 pages of one 5.8 and 9.2.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -648,7 +648,9 @@ int rz_kv_plan(const int32_t* lens, const int32_t* keep, const int32_t* offsets,
  * 2^90 in size, and rows are as rz_kv_cache_write leaves them.  A NaN or an
  * infinity in q or a key gives a NaN or takes no weight, in a value NaN or an
  * infinity in its columns (E4M3: an infinite scale, in its row's).
- * Sums have a fixed order for given sizes and workspace.  seqs == 0 is a no-op.
+ * Sums have a fixed order for given sizes and workspace.  Refused beside the
+ * cache's limits: budget*page_len past 2^31 - 1, pages of all sequences with
+ * more than 2^38 positions.  seqs == 0 is a no-op.
  */
 size_t rz_kv_attention_workspace_bytes(uint32_t seqs, uint32_t q_heads, uint32_t heads, uint32_t dim);
 int rz_kv_attention(int format, const float* q, uint32_t q_heads, uint64_t q_stride, const uint8_t* k_codes,
@@ -682,10 +684,12 @@ int rz_kv_bounds(int format, const uint8_t* k_codes, const void* k_scales, uint6
 /*
  * The `budget` pages of each sequence and key head with the largest scores.
  *   q, q_heads, q_stride, page_table, lens   as for rz_kv_attention
- *   bounds, bound_scales   of num_pages pages
+ *   bounds, bound_scales   of num_pages pages, as rz_kv_bounds leaves them
+ *                 (bounds[0] >= bounds[1])
  *   pages         device out, int32 [seqs][heads][budget]: columns of
  *                 page_table, ascending, then -1
- *   ws            device workspace of rz_kv_select_workspace_bytes() bytes (any contents)
+ *   ws            device workspace of rz_kv_select_workspace_bytes() bytes (any
+ *                 contents), or NULL if that is 0
  * A query of the group is held as whole numbers n_d = rint(RN(q_d * inv)) (0
  * for a NaN), at most 127 in size, of qs = RN(a / 127), with a = max |q_d|
  * (NaN ignored; 1 where it is under 2^-100) and inv = RN(127 / a).  A page's
