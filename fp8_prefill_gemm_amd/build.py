@@ -35,6 +35,7 @@ HIPCC_FLAGS = [
     "-ffp-contract=off",
     "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    "-parallel-jobs=8",  # one source each
     "-Wall",
     "-Wno-unused-command-line-argument",
 ]
