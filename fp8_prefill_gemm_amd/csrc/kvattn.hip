@@ -33,12 +33,12 @@
 // goes to the workspace, and a second launch joins it.
 //
 // Measured (4 key heads of 128 columns, 7 queries each; MXFP4 8): 131072
-// positions of one sequence E4M3 34.8 us, 4.0 TB/s of its rows, the loop itself
+// positions of one sequence E4M3 34.7 us, 4.0 TB/s of its rows, the loop itself
 // at 7 TB/s; 64 sequences of 65536 in all 20.7; 24 sequences of 131072 in all
-// MXFP4 26.4, 2.7 TB/s.  E4M3 is bound by memory in the loop and by what comes
+// MXFP4 24.6, 2.9 TB/s.  E4M3 is bound by memory in the loop and by what comes
 // before and after it (lengths, tables, rows and scales are loads that wait for
 // each other, 6 us; the join's launch, 4), MXFP4 by its vector instructions
-// (about 270 a wave and 32 positions, half of them to widen codes).
+// (about 245 a wave and 32 positions, half of them to widen codes).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -420,7 +420,7 @@ struct Kernel {
     struct Chunk {
         u32x4 q[kParts][C][kWave];  // the queries' parts as the matrix cores take them
         // a chunk of positions: rows of the cache (row 0's for what is none), which of a tile's count, their scales
-        uint32_t row[kChunk];
+        uint32_t row[kChunk + kTile];  // behind them the first one's, a tile of it
         uint32_t live[kChunk / kTile];
         float scale[2][kChunk];  // keys, values
         float largest[kWaves], q_largest[kWaves][16];  // scale of the values, |q| of a head
@@ -528,6 +528,7 @@ struct Kernel {
             load_scales(A, row, y.sc[i]);
             const uint64_t on = __ballot(slot >= 0);
             S.row[at] = row;
+            if (i == 0 && threadIdx.x < kTile) S.row[kChunk + threadIdx.x] = scalar(row);
             if (threadIdx.x % kTile == 0) S.live[at / kTile] = (uint32_t)(on >> (threadIdx.x % kWave));
             y.live |= (slot >= 0 ? 1u : 0u) << i;
         }
@@ -617,6 +618,7 @@ struct Kernel {
     static __device__ __forceinline__ void weigh(const Chunk& S, uint32_t at, uint32_t live, float c, float shift, float (&p)[8], State<C>& st) {
         const uint32_t g = threadIdx.x % kWave / 16;
         if (live != 0xFFFFFFFFu) {
+            asm volatile("" : "+s"(live));  // its bits are looked at here alone
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[e] = live >> (16 * (e / 4) + 4 * g + e % 4) & 1 ? p[e] : -INFINITY;
         }
@@ -660,6 +662,7 @@ struct Kernel {
             }
         }
         if (live != 0xFFFFFFFFu) {  // what lies in no row's place must not meet a weight of 0
+            asm volatile("" : "+s"(live));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const bool on = live >> (16 * (e / 4) + 4 * g + e % 4) & 1;
@@ -678,7 +681,7 @@ struct Kernel {
                 for (int t = 0; t < 2; ++t) {
                     const uint32_t four = *reinterpret_cast<const uint32_t*>(by + 16 * t + 4 * g);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[4 * t + i] = cvt_scale(four >> (8 * i) & 255u);
+                    for (int i = 0; i < 4; ++i) sc[4 * t + i] = __uint_as_float(i < 3 ? four << (23 - 8 * i) : four >> 1);  // the exponent field alone counts
                 }
             }
             unrolled<wide / step>([&](auto k_) {
@@ -729,17 +732,21 @@ struct Kernel {
     }
 
     // `blocks` blocks of the chunk, by the workgroup: every wave's own tiles of 32 into `st`, the next one's rows on their way;
-    // x0: the first one's.
+    // x0: the first one's.  A load that may be left out makes the wait for the tile before it one for all loads, as the
+    // compiler counts them.  So behind the last tile of MXFP4 the chunk's first row is loaded instead (24 sequences of 131072
+    // positions in all 28.4 -> 27.3 us, units of one tile 11.5 -> 12.0); E4M3, which waits for memory all the same, gains no
+    // more in long units than it loses in short ones (131072 positions of one 34.1 -> 33.1, 37 positions 5.9 -> 6.3).
+    static constexpr bool kAlways = FMT == kKvMXFP4;
     static __device__ __forceinline__ void chunk(const KvAttend& A, const Chunk& S, uint32_t blocks, float c, float shift, Rows& x0, State<C>& st) {
         Rows x1;
         uint32_t at = scalar(threadIdx.x / kWave) * kTile;
 #pragma unroll 1
         for (uint32_t i = 0; i < blocks; i += 2, at += 2 * kBlock) {
-            if (i + 1 < blocks) load(A, S.row + at + kBlock, x1);
+            if (kAlways || i + 1 < blocks) load(A, S.row + (i + 1 < blocks ? at + kBlock : kChunk), x1);
             const uint32_t on = scalar(S.live[at / kTile]);
             if (on) tile(S, at, on, c, shift, x0, st);
+            if (kAlways || i + 2 < blocks) load(A, S.row + (i + 2 < blocks ? at + 2 * kBlock : kChunk), x0);
             if (i + 1 < blocks) {
-                if (i + 2 < blocks) load(A, S.row + at + 2 * kBlock, x0);
                 const uint32_t then = scalar(S.live[(at + kBlock) / kTile]);
                 if (then) tile(S, at + kBlock, then, c, shift, x1, st);
             }
