@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
     if (few && A.seqs)
         for (uint32_t i = threadIdx.x; i <= A.seqs; i += kThreads) offset_of[i] = A.offsets[i];
     // new pages are written here unless their tokens do that (those that `tokens` leaves out have pages too)
-    const bool fill = A.seqs != 0 && A.offsets[A.seqs] > (int64_t)A.tokens;
+    const bool fill = A.seqs != 0 && (A.offsets[A.seqs] > (int64_t)A.tokens || A.offsets[0] < 0);
     uint32_t before_take = 0, taken = 0;
     if (few) {
         const uint32_t give = step.give();

@@ -607,7 +607,8 @@ int rz_kv_cache_read(int format, const uint8_t* k_codes, const void* k_scales, c
  * [0, lens], where new is negative, where lens or keep + new needs more than
  * max_pages, and, if it lacks pages, from the first sequence on that the stack
  * cannot serve: it gives and takes nothing, lens_out is its lens, and its
- * tokens get -1.  Tokens of no sequence get -1 too.  Entries of page_table
+ * tokens get -1.  Tokens of no sequence get -1 too; new ones outside
+ * [0, tokens) count and have pages, but no slot here.  Entries of page_table
  * behind a sequence's pages are left as they are, and so is the stack above
  * its largest height of the call.  lens_out may be lens or keep, count_out
  * free_count; no other output may overlap an input.  With outputs of its own

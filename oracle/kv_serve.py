@@ -40,7 +40,7 @@ def plan(lens, keep, offsets, tokens, page_len, table, free, count):
         for j in range(held, need):
             table[b, j] = stack.pop()
         lens_out[b] = keep[b] + new
-        for t in range(int(offsets[b]), min(int(offsets[b + 1]), tokens)):
+        for t in range(max(int(offsets[b]), 0), min(int(offsets[b + 1]), tokens)):
             page, at = divmod(int(keep[b]) + t - int(offsets[b]), page_len)
             slots[t] = int(table[b, page]) * page_len + at
     return slots, lens_out, np.array([len(stack)], dtype=np.int32)

@@ -86,6 +86,15 @@ def test_plan_refuses_what_does_not_fit(rz):
     check_plan(rz, 16, i32([2 ** 31 - 2]), i32([2 ** 31 - 2]), i32([0, 9]), 9, np.zeros((1, 3), dtype=np.int32), free, 3)
 
 
+@pytest.mark.parametrize("tokens", [20, 5000])
+def test_plan_tokens_left_out(rz, tokens):
+    """New tokens before the first and behind the last that slots are asked for: they have pages all the same."""
+    lens, table = i32([3, 0, 9]), np.full((3, 2000), -1, dtype=np.int32)
+    table[0, 0], table[2, :3] = 1999, [1990, 1991, 1992]
+    free = np.arange(1980, dtype=np.int32)
+    check_plan(rz, 4, lens, lens, i32([-9, 6, 11, tokens + 30]), tokens, table, free, 1980)
+
+
 def test_plan_tokens_of_no_sequence(rz):
     """Tokens before the first and behind the last sequence, more tokens than the offsets name, no sequence at all."""
     lens, table, free = i32([3, 0]), i32([[2, -1], [-1, -1]]), i32([5, 4, 1])
