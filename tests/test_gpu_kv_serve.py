@@ -240,6 +240,54 @@ def test_select_special(rz):
     assert (host(got) == -1).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_caches_of_nothing(rz, fmt):
+    """A cache without slots, bounds of no pages, steps of no tokens, batches of no sequences."""
+    heads, dim, seqs = 2, 64, 3
+    none = [dev(x) for c in range(2) for x in kv_cache.empty(fmt, 0, heads, dim)]
+    codes, scales = torch.zeros((0, heads, 2, dim), dtype=torch.int8, device="cuda"), torch.zeros((0, heads), device="cuda")
+    q, table, lens = torch.ones((seqs, 4, dim), device="cuda"), torch.zeros((seqs, 700), dtype=torch.int32, device="cuda"), dev(i32([9, 0, 5000]))
+    lse = torch.zeros((seqs, 4), device="cuda")
+    assert not rz.rz_kv_attention(fmt, q, *none, 8, table, lens, 1.0, lse=lse).any() and (lse == -np.inf).all()
+    assert (rz.rz_kv_select(q, codes, scales, 8, table, lens, 5) == -1).all()
+    assert (rz.rz_kv_select(q, codes, scales, 8, table[:, :9].contiguous(), lens, 5) == -1).all()
+    slots = torch.zeros(4, dtype=torch.int64, device="cuda")
+    rz.rz_kv_bounds(fmt, *none[:2], slots, 8, codes, scales)
+    rz.rz_kv_bounds(fmt, *none[:2], slots[:0], 8, codes, scales)
+    assert rz.rz_kv_select(q[:0], codes, scales, 8, table[:0], lens[:0], 5).shape == (0, heads, 5)
+    torch.cuda.synchronize()
+
+
+def test_choices_on_two_streams_and_in_a_graph(rz):
+    """Scores and choices of two batches at once, each with a workspace of its own, and replayed over new queries and lengths."""
+    sets = []
+    for i, (page, lens) in enumerate(((4, [9000, 30]), (8, [700, 6000, 1]))):
+        table, _, slots = paged(page, lens, 80 + i)
+        codes, scales = ranked(slots // page, 2, 64, 82 + i)
+        q = W.act_normal(84 + i, len(lens), 6 * 64).reshape(len(lens), 6, 64)
+        sets.append(((dev(q), dev(codes), dev(scales), page, dev(table), dev(i32(lens)), 40), kv_serve.select(q, codes, scales, page, table, lens, 40)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [rz.rz_kv_select(*sets[i % 2][0], stream=streams[i % 2]) for i in range(20)]
+    torch.cuda.synchronize()
+    assert all(np.array_equal(host(x), sets[i % 2][1]) for i, x in enumerate(got))
+    graphs = []
+    for args, _ in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = rz.rz_kv_select(*args)
+        graphs.append((g, out))
+    for seed in range(3):
+        for (args, _), (g, out) in zip(sets, graphs):
+            args[0].copy_(dev(W.act_normal(90 + seed, args[0].shape[0], 6 * 64).reshape(args[0].shape)))
+            args[5].copy_(args[5] - 1)
+        for g, out in graphs:
+            g.replay()
+        eager = [rz.rz_kv_select(*args) for args, _ in sets]
+        assert all(np.array_equal(host(out), host(e)) for (_, out), e in zip(graphs, eager))
+        assert not np.array_equal(host(eager[0]), sets[0][1])
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("fmt", FORMATS)
