@@ -23,7 +23,9 @@
 // 2^14 <= max |q| < 2^15, a row's scale (MXFP4: its largest block's) multiplies
 // scores and weights in fp32, and weights are taken times 2^14 over the
 // largest scale of the values so far, so that what is lost lies 2^-38 below
-// the largest value times its weight.
+// the largest value times its weight.  A block's scale is a factor of its codes
+// relative to the row's largest one: exact down to 2^-23 of that, and below it
+// fp16's steps are 2^-27 of the row's largest value or less.
 //
 // Workgroups take nearly equal units of the batch's blocks of 128 positions,
 // whatever the sequences' lengths, one key head (and 16 of its queries) each;

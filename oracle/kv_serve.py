@@ -69,7 +69,7 @@ def slots_of(b, h, n, page_len, table, num_slots, pages=None):
     return out
 
 
-def attention(k, v, q, page_len, table, lens, scale, pages=None):
+def attention(k, v, q, page_len, table, lens, scale, pages=None, blocks=False):
     """(out [seqs][q_heads][dim], lse [seqs][q_heads], bound of out, bound of
     lse) in float64, for the caches' values k and v (values()).
 
@@ -89,7 +89,13 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None):
     6 u: e covers them as a weight's relative error.  Weights and their sum
     pass at most 3 additions and 1 rescaling (2 u each) a position and 64 in
     the joins: gamma_{8 n + 64}.  Numerator and denominator each err by
-    (e^e - 1) <= 1.25 e."""
+    (e^e - 1) <= 1.25 e.
+
+    `blocks` (MXFP4): a row is held relative to its largest block's scale X, as
+    fp16 whose least step is 2^-24.  A block 2^-23 X or more is exact, a smaller
+    one's values err by half a step, 2^-25 X.  The row's largest magnitude is at
+    least 4 X (a written block's largest lies in [4, 8) of its scale): 2^-27 of
+    it, for a key times every |scale q|, for a value its weight."""
     seqs, heads_q, dim = q.shape
     heads = k.shape[1]
     group = heads_q // heads
@@ -115,7 +121,10 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None):
                     out[b, g] = w @ vv
                     far = np.max(np.abs(s)[np.isfinite(s)], initial=0.0)
                     e = gamma(8 * dim) * (np.abs(kk) @ np.abs(x)).max() + 2.0 ** -39 * np.abs(x).max() * np.abs(kk).sum(1).max() + (4 * far + 12) * U
-                    tol[b, g] = (2.5 * e + gamma(8 * len(at) + 64)) * (w @ np.abs(vv)) + len(at) * 2.0 ** -38 * np.abs(vv).max() + 1e-37
+                    if blocks:
+                        e += 2.0 ** -27 * np.abs(kk).max() * np.abs(x).sum()
+                        tol[b, g] += 2.0 ** -27 * (w @ np.abs(vv).max(1))
+                    tol[b, g] += (2.5 * e + gamma(8 * len(at) + 64)) * (w @ np.abs(vv)) + len(at) * 2.0 ** -38 * np.abs(vv).max() + 1e-37
                     ltol[b, g] = 1.25 * e + gamma(8 * len(at) + 64) + 4 * U * abs(lse[b, g])
     return out, lse, tol, ltol
 

@@ -325,6 +325,24 @@ def test_values_that_are_none(rz, fmt):
         assert (cols.sum(1) == 1).all() and cols[:, 5].all()
 
 
+@pytest.mark.parametrize("dim", [64, 96, 128, 512])
+def test_blocks_far_apart(rz, dim):
+    """MXFP4 rows whose blocks' scales differ by up to 2^45, against the bound for those; queries that meet small blocks alone."""
+    page, heads, group, lens = 16, 2, 3, [300, 33, 1]
+    table, used, slots = paged(page, lens, 90)
+    cache = raw_cache(1, slots, heads, dim, 90)
+    g = W.rng(91)
+    for c in (0, 2):
+        x = g.standard_normal((len(used), heads, dim // 32, 32)) * np.exp2(-45 * g.random((len(used), heads, dim // 32, 1)))
+        kv_cache.write(1, x.reshape(len(used), heads, dim).astype(np.float32), used, cache[c], cache[c + 1])
+    q = W.act_normal(92, 3, heads * group * dim).reshape(3, heads * group, dim)
+    q[:, 1, 32:] = 0
+    q[:, 2, :32] = 0
+    k, v = (kv_serve.values(1, *c) for c in (cache[:2], cache[2:]))
+    out, lse = run(rz, 1, cache, dev(q), page, table, lens, 0.3)
+    check(out, lse, kv_serve.attention(k, v, q, page, table, lens, 0.3, blocks=True), "f32")
+
+
 def test_small_and_large_rows(rz):
     """E4M3 rows with scales of 2^-90 to 2^90, queries to match."""
     page, heads, dim, lens = 16, 1, 64, [40, 40]
