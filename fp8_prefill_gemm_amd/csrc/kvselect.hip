@@ -32,6 +32,31 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr float kTiny = 0x1p-100f;
 
+// f over the lanes whose numbers differ in the bits from kFrom to below kTo.
+template <int kFrom, int kTo, typename T, typename F>
+__device__ __forceinline__ T across(T v, F&& f) {
+    auto bits = [](T x) { return __builtin_bit_cast(uint32_t, x); };
+    auto value = [](uint32_t x) { return __builtin_bit_cast(T, x); };
+    auto lane = [&](auto c) { return value((uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits(v), decltype(c)::value, 0xF, 0xF, true)); };
+    if constexpr (kFrom <= 1 && kTo > 1) v = f(v, lane(std::integral_constant<int, 0xB1>{}));  // 1 0 3 2
+    if constexpr (kFrom <= 2 && kTo > 2) v = f(v, lane(std::integral_constant<int, 0x4E>{}));  // 2 3 0 1
+    static_assert(kFrom == 1 || kFrom >= 8);
+    if constexpr (kFrom == 1 && kTo > 4) v = f(v, lane(std::integral_constant<int, 0x141>{}));  // 7 - l, alike in fours
+    if constexpr (kFrom <= 8 && kTo > 8) v = f(v, lane(std::integral_constant<int, 0x128>{}));  // l + 8 of 16
+    if constexpr (kFrom <= 16 && kTo > 16) {
+        const auto x = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+        v = f(value(x[0]), value(x[1]));
+    }
+    if constexpr (kFrom <= 32 && kTo > 32) {
+        const auto x = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+        v = f(value(x[0]), value(x[1]));
+    }
+    return v;
+}
+__device__ __forceinline__ uint32_t greater(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+
 // What a largest magnitude a stands for: 1 where there is next to nothing.
 __device__ __forceinline__ float sized(float a) { return a >= kTiny ? a : 1.0f; }
 
@@ -140,28 +165,6 @@ __device__ __forceinline__ uint32_t slot_at(const KvBounds& A, uint64_t t) {
     return s < 0 || (uint64_t)s >= A.num_slots ? kNone : (uint32_t)s;
 }
 
-// f over the lanes whose numbers differ in the bits from kFrom to below kTo.
-template <int kFrom, int kTo, typename F>
-__device__ __forceinline__ float across(float v, F&& f) {
-    auto lane = [&](auto c) { return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), decltype(c)::value, 0xF, 0xF, true)); };
-    if constexpr (kFrom <= 1 && kTo > 1) v = f(v, lane(std::integral_constant<int, 0xB1>{}));  // 1 0 3 2
-    if constexpr (kFrom <= 2 && kTo > 2) v = f(v, lane(std::integral_constant<int, 0x4E>{}));  // 2 3 0 1
-    static_assert(kFrom == 1 || kFrom >= 8);
-    if constexpr (kFrom == 1 && kTo > 4) v = f(v, lane(std::integral_constant<int, 0x141>{}));  // 7 - l, alike in fours
-    if constexpr (kFrom <= 8 && kTo > 8) v = f(v, lane(std::integral_constant<int, 0x128>{}));  // l + 8 of 16
-    if constexpr (kFrom <= 16 && kTo > 16) {
-        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = f(__uint_as_float(x[0]), __uint_as_float(x[1]));
-    }
-    if constexpr (kFrom <= 32 && kTo > 32) {
-        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = f(__uint_as_float(x[0]), __uint_as_float(x[1]));
-    }
-    return v;
-}
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
-
 // How far `page` is filled by token t + l and those that follow it there, the
 // lanes holding the slots of tokens t on: the largest of them counts.
 __device__ __forceinline__ uint32_t filled_from(const KvBounds& A, uint64_t t, uint32_t s, int l, uint32_t page) {
@@ -177,7 +180,7 @@ __device__ __forceinline__ uint32_t filled_from(const KvBounds& A, uint64_t t, u
         l = 0;
         s = slot_at(A, t + lane);
     }
-    return wave_max_u32(top);
+    return across<1, kWave>(top, greater);
 }
 
 // A decoding step: a workgroup a (token, head).  A token whose predecessor lies
@@ -297,11 +300,7 @@ __device__ __forceinline__ void hold_queries(const float* q0, uint32_t rows, uin
             }
         }
     constexpr uint32_t kIn = kLanes < (uint32_t)kWave ? kLanes : kWave;  // of them in a wave
-#pragma unroll
-    for (uint32_t off = 1; off < kIn; off <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)top, (int)off, kWave);
-        top = top > o ? top : o;
-    }
+    top = across<1, (int)kIn>(top, greater);
     const float a = sized(__uint_as_float(top)), inv = 127.0f / a;
     if (part == 0) Q.scale[m] = a / 127.0f;
     for (uint32_t d = part * 4u; d < dim; d += kLanes * 4u) {
@@ -462,8 +461,8 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
         high = k + 0x00800000u > high ? k + 0x00800000u : high;
     });
     some -= forced;
-    high = wave_max_u32(high);
-    low = ~wave_max_u32(~low);
+    high = across<1, kWave>(high, greater);
+    low = ~across<1, kWave>(~low, greater);
     if (lane == 0) {
         if (some) {
             atomicMin(&P.low, low + 1u);
