@@ -11,9 +11,9 @@
 //
 // Few bytes are moved for each launch, so latency counts: the loads that wait for
 // each other (slots, rows; lengths, tables, bounds; keys) and the barriers of
-// the choice.  4 key heads of 128 columns: bounds of 64 pages of 64 rows 6.0 us, of a
-// 32768-token prompt 8.8 (1.2 TB/s); scores of 8192 pages of 32 sequences 7.6
-// and their choice 6.3; of 8192 pages of one 5.8 and 9.2.
+// the choice.  4 key heads of 128 columns: bounds of 64 pages of 64 rows 6.2 us, of a
+// 32768-token prompt 8.7 (1.2 TB/s); scores of 8192 pages of 32 sequences 7.4
+// and their choice 6.4; of 8192 pages of one 5.9 and 9.0.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
