@@ -902,6 +902,8 @@ int rz_kv_select(const float* q, uint32_t q_heads, uint64_t q_stride, const int8
     if (int r = check_kv(fn, RZ_KV_E4M3, heads, dim, num_pages)) return r;
     if (int r = check_kv_query(fn, q_heads, heads, dim, page_len, seqs, q_stride)) return r;
     if (budget == 0) return fail(RZ_ERR_SHAPE, "%s: budget must be positive", fn);
+    // places behind the pages taken are counted in 32 bits, 1024 at a time
+    if (budget > 0x7FFFFFFFu) return fail(RZ_ERR_SHAPE, "%s: budget exceeds 2^31 - 1", fn);
     if (seqs == 0) return RZ_OK;  // nothing to read or write
     if ((uint64_t)seqs * heads * max_pages > RZ_KV_MAX_SCORES || (uint64_t)seqs * heads * budget > RZ_MAX_ELEMS ||
         (uint64_t)seqs * heads > RZ_KV_MAX_SCORES / 64u)

@@ -701,6 +701,7 @@ int rz_kv_bounds(int format, const uint8_t* k_codes, const void* k_scales, uint6
  * (the sum is exact; NaN counts as +inf): to rounding, an upper bound of the
  * page's q . k.  The first and the last of a sequence's pages score +inf.
  * Ties go to the lower page.  A page outside the cache is never taken.
+ * Refused beside the cache's limits: budget 0 or past 2^31 - 1.
  * seqs == 0 is a no-op.
  */
 size_t rz_kv_select_workspace_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages);

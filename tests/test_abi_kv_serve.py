@@ -80,6 +80,14 @@ def test_select(L):
     assert L.rz_kv_select(None, 6, 0, None, None, 20, 2, 64, 16, None, 0, 4, None, 2, None, None, None) == OK
 
 
+def test_select_budget_past_31_bits(L):
+    """A choice is filled up with -1 by 32-bit places a workgroup's width apart, which would wrap for budgets near 2^32."""
+    good = [P, 6, 6 * 64, P, P, 20, 2, 64, 16, P, 1, 4, P, 2, P, P, None]
+    for budget in (0x80000000, 0xFFFFFC01, 0xFFFFFFFF):
+        assert L.rz_kv_select(*changed(good, 13, budget)) == SHAPE, budget
+        assert L.rz_kv_select(None, 6, 0, None, None, 20, 2, 64, 16, None, 0, 4, None, budget, None, None, None) == SHAPE, budget
+
+
 # The binding's checks of a CPU tensor end with the one for a device.
 C = [torch.zeros(32, 2, 64, dtype=U8), f32(32, 2)] * 2
 MX = [torch.zeros(32, 2, 32, dtype=U8), torch.zeros(32, 2, 2, dtype=U8)] * 2
