@@ -21,9 +21,9 @@
 // the parts lie side by side in the 16 columns, one product for both.  What
 // fp16's range does not hold is kept outside it: a head's q is scaled to
 // 2^14 <= max |q| < 2^15, a row's scale (MXFP4: its largest block's) multiplies
-// scores and weights in fp32, and weights are taken times 2^14 over the
-// largest scale of the values so far, so that what is lost lies 2^-38 below
-// the largest value times its weight.  A block's scale is a factor of its codes
+// scores and weights in fp32, and weights are taken times 2^14 over a power of
+// two above the scales of the wave's values so far, so that what is lost lies
+// 2^-38 below the largest value times its weight.  A block's scale is a factor of its codes
 // relative to the row's largest one: exact down to 2^-23 of that, and below it
 // fp16's steps are 2^-27 of the row's largest value or less.
 //
@@ -388,8 +388,8 @@ __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t
 
 // A wave's running state: o[j][i] is column VRuns' product j, row 4 g + i, of
 // head l % 16 (or part l / 8 of head l % 8).  m is the largest score as the
-// products give it, and m c = `base` in powers of two; o and l are sums of
-// 2^(score - base + shift).
+// products give it, and m c = `base` in powers of two; l is the sum of
+// 2^(score - base), o that of these times the values, in their unit.
 template <int C>
 struct State {
     f32x4 o[2 * C];
@@ -421,11 +421,12 @@ struct Kernel {
 
     struct Chunk {
         u32x4 q[kParts][C][kWave];  // the queries' parts as the matrix cores take them
-        // a chunk of positions: rows of the cache (row 0's for what is none), which of a tile's count, their scales
-        uint32_t row[kChunk + kTile];  // behind them the first one's, a tile of it
+        // a chunk of positions, every wave's tiles by itself: rows of the cache (row 0's for what is none), which of a tile's
+        // count, their scales
+        uint32_t row[kChunk + kBlock];  // behind them a wave's first one, a tile of it
         uint32_t live[kChunk / kTile];
         float scale[2][kChunk];  // keys, values
-        float largest[kWaves], q_largest[kWaves][16];  // scale of the values, |q| of a head
+        float q_largest[kWaves][16];  // |q| of a head
         uint8_t byte[FMT == kKvE4M3 ? 1 : 2][FMT == kKvE4M3 ? 1 : C][FMT == kKvE4M3 ? 4 : kChunk];
     };
     union Shared {
@@ -506,14 +507,23 @@ struct Kernel {
         }
     }
 
-    // The workgroup's lanes find a chunk's positions, kTurns each; `blocks` of it are used.
+    // A wave's lanes find the positions of its own tiles of a chunk, kTurns each; `blocks` of it are used.
     static constexpr int kTurns = kChunk / kThreads;
+    static __device__ __forceinline__ uint32_t place(int turn) {
+        const uint32_t lane = threadIdx.x % kWave;
+        return (kWave / kTile * turn + lane / kTile) * kBlock + threadIdx.x / kWave * kTile + lane % kTile;
+    }
     struct Spots {
         Spot s[kTurns];
     };
     static __device__ __forceinline__ void find(const KvAttend& A, const Grid& G, uint32_t b, uint32_t h, uint32_t block, Spots& x) {
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) x.s[i] = spot(A, G, b, h, block * kBlock + i * kThreads + threadIdx.x);
+        for (int i = 0; i < kTurns; ++i) x.s[i] = spot(A, G, b, h, block * kBlock + place(i));
+    }
+    // What a wave has staged, its lanes may read.
+    static __device__ __forceinline__ void staged_by_wave() {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
     // First the rows, whose scales are then on their way, and once those are here the scales.
     struct Staged {
@@ -524,44 +534,44 @@ struct Kernel {
         y.live = 0;
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
-            const uint32_t at = i * kThreads + threadIdx.x;
+            const uint32_t at = place(i), lane = threadIdx.x % kWave;
             const int32_t slot = at < blocks * kBlock ? slot_of(A, x.s[i], len) : -1;
             const uint32_t row = (uint32_t)(slot < 0 ? 0 : slot) * A.heads + h;  // below 2^31
             load_scales(A, row, y.sc[i]);
             const uint64_t on = __ballot(slot >= 0);
             S.row[at] = row;
-            if (i == 0 && threadIdx.x < kTile) S.row[kChunk + threadIdx.x] = scalar(row);
-            if (threadIdx.x % kTile == 0) S.live[at / kTile] = (uint32_t)(on >> (threadIdx.x % kWave));
+            if (i == 0 && lane < kTile) S.row[kChunk + threadIdx.x / kWave * kTile + lane] = scalar(row);
+            if (lane % kTile == 0) S.live[at / kTile] = (uint32_t)(on >> lane);
             y.live |= (slot >= 0 ? 1u : 0u) << i;
         }
     }
-    static __device__ __forceinline__ void stage_scales(Chunk& S, Staged& y) {
+    // The scales of values are staged in a unit of their own, 2^(e - 14) with e the exponent of a power of two over them, at
+    // least the one before, which is returned.  (Times the weights instead, it would be an addend of the exponential's argument,
+    // and its rounding the scores'.)
+    static __device__ __forceinline__ int stage_scales(Chunk& S, Staged& y, int e) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
-            const uint32_t at = i * kThreads + threadIdx.x;
             ready(y.live >> i & 1, y.sc[i]);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                S.scale[c][at] = y.sc[i].row[c];
-                if constexpr (FMT == kKvMXFP4)
-#pragma unroll
-                    for (int k = 0; k < C; ++k) S.byte[c][k][at] = (uint8_t)y.sc[i].byte[c * C + k];
-            }
             const uint32_t key = __float_as_uint(y.sc[i].row[1]) & 0x7FFFFFFFu;
             top = key < 0x7F800000u && key > top ? key : top;
         }
         top = wave_reduce(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-        if (threadIdx.x % kWave == 0) S.largest[threadIdx.x / kWave] = __uint_as_float(top);
-    }
-    // The exponent of a power of two over the chunk's scales of values, within what the weights' range allows, at least e.
-    static __device__ __forceinline__ int exponent(const Chunk& S, int e) {
-        float top = S.largest[0];
+        const int over = (int)(top >> 23) - 126;
+        e = over > e ? over < 127 ? over : 127 : e;
+        const float unit = power(14 - e);
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) top = fmaxf(top, S.largest[i]);
-        int x = (int)(__float_as_uint(top) >> 23) - 126;
-        x = x < 110 ? x : 110;
-        return (int)scalar((uint32_t)(x > e ? x : e));
+        for (int i = 0; i < kTurns; ++i) {
+            const uint32_t at = place(i);
+            S.scale[0][at] = y.sc[i].row[0];
+            S.scale[1][at] = y.sc[i].row[1] * unit;
+            if constexpr (FMT == kKvMXFP4)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < C; ++k) S.byte[c][k][at] = (uint8_t)y.sc[i].byte[c * C + k];
+        }
+        return e;
     }
 
     // kRow as a factor that the compiler does not know: one multiply-add an address, not a shift and two additions.
@@ -616,8 +626,8 @@ struct Kernel {
         }
     }
 
-    // Scores into weights relative to the running maximum times 2^shift and the values' scales, `live` the positions that count.
-    static __device__ __forceinline__ void weigh(const Chunk& S, uint32_t at, uint32_t live, float c, float shift, float (&p)[8], State<C>& st) {
+    // Scores into weights relative to the running maximum times the values' scales, `live` the positions that count.
+    static __device__ __forceinline__ void weigh(const Chunk& S, uint32_t at, uint32_t live, float c, float (&p)[8], State<C>& st) {
         const uint32_t g = threadIdx.x % kWave / 16;
         if (live != 0xFFFFFFFFu) {
             asm volatile("" : "+s"(live));  // its bits are looked at here alone
@@ -636,9 +646,8 @@ struct Kernel {
             st.m = top;
             st.base = base;
         }
-        const float off = shift - st.base;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[e], c, off));
+        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[e], c, -st.base));
         st.l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -726,31 +735,32 @@ struct Kernel {
         load_keys(A, row, x.k);
         load_values(A, row, x.v);
     }
-    static __device__ __forceinline__ void tile(const Chunk& S, uint32_t at, uint32_t live, float c, float shift, Rows& x, State<C>& st) {
+    static __device__ __forceinline__ void tile(const Chunk& S, uint32_t at, uint32_t live, float c, Rows& x, State<C>& st) {
         float p[8];
         scores(S, at, x.k, p);
-        weigh(S, at, live, c, shift, p, st);
+        weigh(S, at, live, c, p, st);
         add_values(S, at, live, p, x.v, st);
     }
 
     // `blocks` blocks of the chunk, by the workgroup: every wave's own tiles of 32 into `st`, the next one's rows on their way;
     // x0: the first one's.  A load that may be left out makes the wait for the tile before it one for all loads, as the
-    // compiler counts them.  So behind the last tile of MXFP4 the chunk's first row is loaded instead (24 sequences of 131072
+    // compiler counts them.  So behind the last tile of MXFP4 the wave's first row is loaded instead (24 sequences of 131072
     // positions in all 28.4 -> 27.3 us, units of one tile 11.5 -> 12.0); E4M3, which waits for memory all the same, gains no
     // more in long units than it loses in short ones (131072 positions of one 34.1 -> 33.1, 37 positions 5.9 -> 6.3).
     static constexpr bool kAlways = FMT == kKvMXFP4;
-    static __device__ __forceinline__ void chunk(const KvAttend& A, const Chunk& S, uint32_t blocks, float c, float shift, Rows& x0, State<C>& st) {
+    static __device__ __forceinline__ void chunk(const KvAttend& A, const Chunk& S, uint32_t blocks, float c, Rows& x0, State<C>& st) {
         Rows x1;
         uint32_t at = scalar(threadIdx.x / kWave) * kTile;
+        const uint32_t spare = kChunk + at;
 #pragma unroll 1
         for (uint32_t i = 0; i < blocks; i += 2, at += 2 * kBlock) {
-            if (kAlways || i + 1 < blocks) load(A, S.row + (i + 1 < blocks ? at + kBlock : kChunk), x1);
+            if (kAlways || i + 1 < blocks) load(A, S.row + (i + 1 < blocks ? at + kBlock : spare), x1);
             const uint32_t on = scalar(S.live[at / kTile]);
-            if (on) tile(S, at, on, c, shift, x0, st);
-            if (kAlways || i + 2 < blocks) load(A, S.row + (i + 2 < blocks ? at + 2 * kBlock : kChunk), x0);
+            if (on) tile(S, at, on, c, x0, st);
+            if (kAlways || i + 2 < blocks) load(A, S.row + (i + 2 < blocks ? at + 2 * kBlock : spare), x0);
             if (i + 1 < blocks) {
                 const uint32_t then = scalar(S.live[(at + kBlock) / kTile]);
-                if (then) tile(S, at + kBlock, then, c, shift, x1, st);
+                if (then) tile(S, at + kBlock, then, c, x1, st);
             }
         }
     }
@@ -814,7 +824,7 @@ struct Kernel {
         __syncthreads();
         Rows x0;
         load(A, S.row + wave * kTile, x0);
-        stage_scales(S, staged);
+        int e = stage_scales(S, staged, -112);
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) top = fmaxf(top, S.q_largest[i][n]);
         // a head's power of two, and what brings its scores back to powers of two
@@ -843,7 +853,6 @@ struct Kernel {
             }
         }
         __syncthreads();
-        int e = exponent(S, -90);
         State<C> st;
 #pragma unroll
         for (int j = 0; j < 2 * C; ++j) st.o[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -851,23 +860,21 @@ struct Kernel {
         st.base = st.l = 0.0f;
         for (uint32_t at = first;;) {
             const uint32_t count = last - at < kChunk / kBlock ? last - at : kChunk / kBlock;
-            chunk(A, S, count, c, (float)(14 - e), x0, st);
+            chunk(A, S, count, c, x0, st);
             at += count;
             if (at >= last) break;
             find(A, G, b, h, at, spots);
-            __syncthreads();  // the chunk is no longer read
+            staged_by_wave();  // and has read: its tiles are done
             stage_rows(A, S, h, last - at, until, spots, staged);
-            __syncthreads();
+            staged_by_wave();
             load(A, S.row + wave * kTile, x0);
-            stage_scales(S, staged);
-            __syncthreads();
-            const int then = exponent(S, e);
-            if (then != e) {  // larger values to come: the sums' unit grows
+            const int then = stage_scales(S, staged, e);
+            if (then != e) {  // larger values to come: the sums' unit grows (past 2^126 what there was is nothing to them)
                 const float f = power(e - then < -126 ? -126 : e - then);
 #pragma unroll
                 for (int j = 0; j < 2 * C; ++j) st.o[j] *= f;
-                st.l *= f;
             }
+            staged_by_wave();
             e = then;
         }
         const float unit = power(e - 14);
@@ -878,7 +885,7 @@ struct Kernel {
 #pragma unroll
             for (int i = 0; i < 4; ++i) W.o[wave][4 * j + i][lane] = st.o[j][i] * unit;
         W.m[wave][lane] = st.m == -INFINITY ? -INFINITY : st.base;  // in powers of two
-        W.l[wave][lane] = head_sum(st.l) * unit;
+        W.l[wave][lane] = head_sum(st.l);
         __syncthreads();
         // wave i joins row i of every product
         float m = W.m[0][lane];

@@ -78,8 +78,9 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None, blocks=False):
     where neither is subnormal.  Subnormal parts err by 2^-25 at most: q is
     scaled so that its largest magnitude is at least 2^14, hence 2^-39 of it;
     a weight w <= 1 is taken times 2^14 times its row's scale over a power of
-    two at most twice the largest scale, hence 2^-38 of the largest value (in a
-    row as it is written the largest code is the format's).  A score is a sum
+    two at most twice the largest scale that it is summed with, hence 2^-38 of
+    the largest value (in a row as it is written the largest code is the
+    format's).  That power stays outside the exponential.  A score is a sum
     of 2 dim exact products and as many additions of 2 u each (truncation),
     with a row's scale (2 u: as read, and as multiplied) and the rounded
     constant (u): it errs by at most gamma_{4 dim + 10}, and so gamma_{8 dim},
@@ -124,7 +125,7 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None, blocks=False):
                     if blocks:
                         e += 2.0 ** -27 * np.abs(kk).max() * np.abs(x).sum()
                         tol[b, g] += 2.0 ** -27 * (w @ np.abs(vv).max(1))
-                    tol[b, g] += (2.5 * e + gamma(8 * len(at) + 64)) * (w @ np.abs(vv)) + len(at) * 2.0 ** -38 * np.abs(vv).max() + 1e-37
+                    tol[b, g] += (2.5 * e + gamma(8 * len(at) + 64)) * (w @ np.abs(vv)) + len(at) * 2.0 ** -38 * np.abs(vv).max()
                     ltol[b, g] = 1.25 * e + gamma(8 * len(at) + 64) + 4 * U * abs(lse[b, g])
     return out, lse, tol, ltol
 
