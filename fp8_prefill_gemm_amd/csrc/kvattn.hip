@@ -545,14 +545,43 @@ struct Kernel {
             y.live |= (slot >= 0 ? 1u : 0u) << i;
         }
     }
+    // Whether the values of a row are zeros: E4M3's have the scale of a row whose largest magnitude is 1, so it is looked at
+    // where that is met, and then staged as 0.
+    static __device__ __forceinline__ bool zeros(const KvAttend& A, uint32_t row) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(A.codes[1] + (uint64_t)row * kRow);
+        uint32_t any = 0;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kRow / 16 && any == 0; ++i) any = (p[i].x | p[i].y | p[i].z | p[i].w) & 0x7F7F7F7Fu;
+        return any == 0;
+    }
     // The scales of values are staged in a unit of their own, 2^(e - 14) with e the exponent of a power of two over them, at
     // least the one before, which is returned.  (Times the weights instead, it would be an addend of the exponential's argument,
     // and its rounding the scores'.)
-    static __device__ __forceinline__ int stage_scales(Chunk& S, Staged& y, int e) {
+    static __device__ __forceinline__ int stage_scales(const KvAttend& A, Chunk& S, Staged& y, int e) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
+            const uint32_t at = place(i);
             ready(y.live >> i & 1, y.sc[i]);
+            S.scale[0][at] = y.sc[i].row[0];
+            if constexpr (FMT == kKvMXFP4)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < C; ++k) S.byte[c][k][at] = (uint8_t)y.sc[i].byte[c * C + k];
+        }
+        if constexpr (FMT == kKvE4M3) {
+            bool one = false;
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) one |= y.sc[i].row[1] == 1.0f / 448.0f;
+            if (__builtin_expect(__any(one), 0)) {  // rare
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i)
+                    if (y.sc[i].row[1] == 1.0f / 448.0f && zeros(A, S.row[place(i)])) y.sc[i].row[1] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
             const uint32_t key = __float_as_uint(y.sc[i].row[1]) & 0x7FFFFFFFu;
             top = key < 0x7F800000u && key > top ? key : top;
         }
@@ -561,16 +590,7 @@ struct Kernel {
         e = over > e ? over < 127 ? over : 127 : e;
         const float unit = power(14 - e);
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const uint32_t at = place(i);
-            S.scale[0][at] = y.sc[i].row[0];
-            S.scale[1][at] = y.sc[i].row[1] * unit;
-            if constexpr (FMT == kKvMXFP4)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int k = 0; k < C; ++k) S.byte[c][k][at] = (uint8_t)y.sc[i].byte[c * C + k];
-        }
+        for (int i = 0; i < kTurns; ++i) S.scale[1][place(i)] = y.sc[i].row[1] * unit;
         return e;
     }
 
@@ -824,7 +844,7 @@ struct Kernel {
         __syncthreads();
         Rows x0;
         load(A, S.row + wave * kTile, x0);
-        int e = stage_scales(S, staged, -112);
+        int e = stage_scales(A, S, staged, -112);
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) top = fmaxf(top, S.q_largest[i][n]);
         // a head's power of two, and what brings its scores back to powers of two
@@ -868,7 +888,7 @@ struct Kernel {
             stage_rows(A, S, h, last - at, until, spots, staged);
             staged_by_wave();
             load(A, S.row + wave * kTile, x0);
-            const int then = stage_scales(S, staged, e);
+            const int then = stage_scales(A, S, staged, e);
             if (then != e) {  // larger values to come: the sums' unit grows (past 2^126 what there was is nothing to them)
                 const float f = power(e - then < -126 ? -126 : e - then);
 #pragma unroll

@@ -80,7 +80,8 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None, blocks=False):
     a weight w <= 1 is taken times 2^14 times its row's scale over a power of
     two at most twice the largest scale that it is summed with, hence 2^-38 of
     the largest value (in a row as it is written the largest code is the
-    format's).  That power stays outside the exponential.  A score is a sum
+    format's; one of zeros has E4M3's scale of 1 or MXFP4's least one, and the
+    first counts as none).  That power stays outside the exponential.  A score is a sum
     of 2 dim exact products and as many additions of 2 u each (truncation),
     with a row's scale (2 u: as read, and as multiplied) and the rounded
     constant (u): it errs by at most gamma_{4 dim + 10}, and so gamma_{8 dim},

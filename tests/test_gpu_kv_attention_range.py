@@ -79,3 +79,49 @@ def test_values_from_end_to_end(rz, fmt, first, then):
     q = W.act_normal(14, 1, group * dim).reshape(1, group, dim)
     # 1076 positions and more make the result: sqrt(8 * 1076 + 64) roundings of 2^-24 are 2^-17.4 if they are independent
     both(rz, fmt, cache, q, page, table, [n], 0.05, 2.0 ** -17.4)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [32, 128, 512])
+@pytest.mark.parametrize("n,at", [(8, 3), (40, 39), (2500, 0), (2500, 1100)])
+@pytest.mark.parametrize("size", [1e-5, 2.0 ** -40])
+def test_value_rows_of_zeros(rz, fmt, dim, n, at, size):
+    """A row of zeros among values of `size`, as an ordinary position and as the one that takes most of the weight: the others
+    count as they do without it."""
+    page, heads, group = 16, 2, 3
+    table, used, slots = paged(page, [n], 1)
+    cache = [x for _ in range(2) for x in kv_cache.empty(fmt, slots, heads, dim, 255)]
+    g = W.rng(2)
+    k, v = (g.standard_normal((n, heads, dim)).astype(np.float32) for _ in range(2))
+    v *= np.float32(size)
+    v[at, 0] = 0
+    for sink in (False, True):
+        if sink:
+            k[at] = 6.0 * np.abs(k).max()
+        kv_cache.write(fmt, k, used, *cache[:2])
+        kv_cache.write(fmt, v, used, *cache[2:])
+        assert not kv_serve.values(fmt, *cache[2:])[used[at], 0].any()
+        q = np.abs(W.act_normal(3, 1, heads * group * dim)).reshape(1, heads * group, dim)
+        both(rz, fmt, cache, q, page, table, [n], 0.5 / dim)
+
+
+@pytest.mark.parametrize("negative", [False, True])
+def test_value_rows_of_the_scale_of_zeros(rz, negative):
+    """E4M3 rows whose largest magnitude is 1 have the scale that rows of zeros have, and count; a zero's sign does not."""
+    page, heads, group, dim, n = 16, 1, 2, 64, 50
+    table, used, slots = paged(page, [n], 4)
+    cache = [x for _ in range(2) for x in kv_cache.empty(0, slots, heads, dim, 255)]
+    g = W.rng(5)
+    v = 1e-6 * g.standard_normal((n, heads, dim))
+    v[7], v[9], v[11] = 0, 0, 0
+    v[7, 0, 63], v[9, 0, 0] = 1, -1
+    kv_cache.write(0, g.standard_normal((n, heads, dim)).astype(np.float32), used, *cache[:2])
+    kv_cache.write(0, v.astype(np.float32), used, *cache[2:])
+    assert (cache[3][used[[7, 9, 11]]] == np.float32(1) / np.float32(448)).all()
+    if negative:
+        cache[2][used[11], 0, ::2] = 0x80
+    q = W.act_normal(6, 1, group * dim).reshape(1, group, dim)
+    both(rz, 0, cache, q, page, table, [n], 0.2)
+    # the rows of 1 out of the way: the row of zeros alone must not set the unit
+    cache[2][used[[7, 9]]], cache[3][used[[7, 9]]] = cache[2][used[8]], cache[3][used[8]]
+    both(rz, 0, cache, q, page, table, [n], 0.2)
