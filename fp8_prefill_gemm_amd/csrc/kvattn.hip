@@ -19,11 +19,13 @@
 // q and the weights count to 22 bits, as two fp16 parts each (the second the
 // first's rounding, rounded: 2^-22 at most).  With up to 8 queries a key head
 // the parts lie side by side in the 16 columns, one product for both.  What
-// fp16's range does not hold is kept outside it: a head's q is scaled to
-// 2^14 <= max |q| < 2^15, a row's scale (MXFP4: its largest block's) multiplies
-// scores and weights in fp32, and weights are taken times 2^14 over a power of
-// two above the scales of the wave's values so far, so that what is lost lies
-// 2^-38 below the largest value times its weight.  A block's scale is a factor of its codes
+// fp16's range does not hold is kept outside it: a head's q, times scale and
+// log2(e), is brought to 2^14 <= max |q| < 2^15 by a power of two, so that a
+// score's way back is exact and the largest one's difference to itself 0 however
+// large it is; a row's scale (MXFP4: its largest block's) multiplies scores and
+// weights in fp32, and weights are taken times 2^14 over a power of two above
+// the scales of the wave's values so far, so that what is lost lies 2^-38 below
+// the largest value times its weight.  A block's scale is a factor of its codes
 // relative to the row's largest one: exact down to 2^-23 of that, and below it
 // fp16's steps are 2^-27 of the row's largest value or less.
 //
@@ -834,11 +836,15 @@ struct Kernel {
         __syncthreads();  // the last piece's results have been read
         Staged staged;
         stage_rows(A, S, h, last - first, until, spots, staged);
+        const float scale = A.scale * 1.44269504088896341f;
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < kSteps; ++i) {
+            q[i][0] *= scale;
+            q[i][1] *= scale;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(q[i][0][e]), fabsf(q[i][1][e])));
+        }
         top = head_max(top);
         if (g == 0) S.q_largest[wave][n] = top;
         __syncthreads();
@@ -847,11 +853,10 @@ struct Kernel {
         int e = stage_scales(A, S, staged, -112);
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) top = fmaxf(top, S.q_largest[i][n]);
-        // a head's power of two, and what brings its scores back to powers of two
+        // a head's power of two, which brings its scores back to powers of two
         int up = 141 - (int)(__float_as_uint(top) >> 23);
         up = up < -112 ? -112 : up > 126 ? 126 : up;
-        const float c = A.scale == 0.0f ? 1.0f : fmaxf(__builtin_ldexpf(fabsf(A.scale) * 1.44269504088896341f, -up), 0x1p-126f);
-        const float by = A.scale == 0.0f ? 0.0f : A.scale < 0.0f ? -power(up) : power(up);
+        const float c = power(-up), by = power(up);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const uint32_t s = i * kWaves + wave;

@@ -644,13 +644,14 @@ int rz_kv_plan(const int32_t* lens, const int32_t* keep, const int32_t* offsets,
  * row without a position, or with all its scores -inf, gives zeros and
  * lse -inf.  Otherwise, for n positions and gamma_t = t eps / (1 - t eps), eps = 2^-24,
  *   |out - exact| <= (2.5 e + gamma_{8 n + 64}) sum_p w_p |v_p| + n 2^-38 max |v| + rounding to dtype,
- *   e = max_p (gamma_{8 dim} scale sum_d |q_d k_pd| + 2^-39 scale max |q| sum_d |k_pd| + (4 |scale q . k_p| + 12) eps)
- * (MXFP4: and 2^-27 scale sum_d |q_d| max_d |k_pd| in e, 2^-27 sum_p w_p max_d
+ *   e = max_p (gamma_{8 dim} s sum_d |q_d k_pd| + 2^-39 s max |q| sum_d |k_pd| + (4 |s q . k_p| + 12) eps)
+ * (MXFP4: and 2^-27 s sum_d |q_d| max_d |k_pd| in e, 2^-27 sum_p w_p max_d
  * |v_pd|, for blocks under 2^-23 of their row's largest scale)
- * where no sum overflows, q and the rows' scales are 0 or between 2^-100 and
- * 2^90 in size, and rows are as rz_kv_cache_write leaves them.  A NaN or an
- * infinity in q or a key gives a NaN or takes no weight, in a value NaN or an
- * infinity in its columns (E4M3: an infinite scale, in its row's).
+ * with s = |scale|, where no sum and no log2(e) scale q_d overflows, q and the
+ * rows' scales are 0 or between 2^-100 and 2^90 in size, and rows are as
+ * rz_kv_cache_write leaves them.  A NaN or an infinity in q or a key gives a NaN
+ * or takes no weight, in a value NaN or an infinity in its columns (E4M3: an
+ * infinite scale, in its row's).
  * Sums have a fixed order for given sizes and workspace.  Refused beside the
  * cache's limits: budget*page_len past 2^31 - 1, pages of all sequences with
  * more than 2^38 positions.  seqs == 0 is a no-op.

@@ -83,11 +83,13 @@ def attention(k, v, q, page_len, table, lens, scale, pages=None, blocks=False):
     format's; one of zeros has E4M3's scale of 1 or MXFP4's least one, and the
     first counts as none).  That power stays outside the exponential.  A score is a sum
     of 2 dim exact products and as many additions of 2 u each (truncation),
-    with a row's scale (2 u: as read, and as multiplied) and the rounded
-    constant (u): it errs by at most gamma_{4 dim + 10}, and so gamma_{8 dim},
-    times sum |scale q k|.  The exponential's argument is rounded (u |s|,
-    twice: the product with the constant and the difference; twice more in a
-    join), the exponential errs by 1 ulp, and a weight's scale and parts by
+    with a row's scale (2 u: as read, and as multiplied) and q's product with
+    the rounded scale log2(e) (3 u): it errs by at most gamma_{4 dim + 10}, and
+    so gamma_{8 dim}, times sum |scale q k|.  Its way back from powers of two is
+    exact; the exponential's argument, its difference to the largest one so
+    far, is rounded, and so is every later difference of maxima up to the last
+    join's, together at most 2 max |s| (u |s|, with log2(e) twice more; 4 |s|
+    bounds it).  The exponential errs by 1 ulp, and a weight's scale and parts by
     6 u: e covers them as a weight's relative error.  Weights and their sum
     pass at most 3 additions and 1 rescaling (2 u each) a position and 64 in
     the joins: gamma_{8 n + 64}.  Numerator and denominator each err by

@@ -1,5 +1,6 @@
 """GPU parity of attention over the paged cache at the ends of what its bound
-holds for (needs an MI355X)."""
+holds for (needs an MI355X): rows of nothing beside small ones, scales and
+queries from one end of the range to the other, scores past 2^24."""
 import ctypes
 
 import numpy as np
@@ -7,7 +8,7 @@ import pytest
 
 import workloads as W
 from oracle import kv_cache, kv_serve
-from test_gpu_kv_attention import FORMATS, check, dev, fill, paged, raw_cache, run
+from test_gpu_kv_attention import FORMATS, check, dev, fill, host, paged, raw_cache, run
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +126,51 @@ def test_value_rows_of_the_scale_of_zeros(rz, negative):
     # the rows of 1 out of the way: the row of zeros alone must not set the unit
     cache[2][used[[7, 9]]], cache[3][used[[7, 9]]] = cache[2][used[8]], cache[3][used[8]]
     both(rz, 0, cache, q, page, table, [n], 0.2)
+
+
+@pytest.mark.parametrize("scale,down,up", [(2.0 ** -16, -100, 88), (2.0 ** -30, -95, 88), (-2.0 ** -14, -99, 85), (1e-30, 0, 88), (2.0 ** 30, -100, 60), (1e-42, 0, 0)])
+def test_small_and_large_scales(rz, scale, down, up):
+    """Queries of 2^down with keys of scales of 2^up: what their products lose to scale they do not get back."""
+    page, heads, group, dim, n = 16, 1, 2, 64, 40
+    table, used, slots = paged(page, [n], 15)
+    cache = raw_cache(0, slots, heads, dim, 15)
+    fill(0, cache, used, 16)
+    cache[1][used] *= np.float32(2.0 ** up * 64)
+    q = (W.act_normal(17, 1, group * dim) * 2.0 ** down).astype(np.float32).reshape(1, group, dim)
+    both(rz, 0, cache, q, page, table, [n], float(np.float32(scale)))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [30, 700, 5000])
+@pytest.mark.parametrize("size", [20, 25, 33, 50, 80])
+@pytest.mark.parametrize("scale", [1.0, -0.37])
+def test_scores_past_2_to_the_24(rz, fmt, n, size, scale):
+    """Queries of one column, so that scores have their keys' order to the last bit: where they are 2^20 and more the largest
+    takes all.  Its weight is 1 and their sum is 1, so what is left, in roundings of 2^-24, are the weight's parts (4), the
+    value's as it is read (1) and four additions of 2 at most: 16 bounds it.  A score has q's product with scale log2(e) (3),
+    its parts (4), two additions (4) and the row's scale (2), and lse 2 for its way back from powers of two: 15."""
+    page, heads, group, dim = 16, 1, 3, 64
+    table, used, slots = paged(page, [n], 18)
+    cache = raw_cache(fmt, slots, heads, dim, 18)
+    g = W.rng(19 + n)
+    kv_cache.write(fmt, g.standard_normal((n, heads, dim)).astype(np.float32), used, *cache[:2])
+    kv_cache.write(fmt, g.standard_normal((n, heads, dim)).astype(np.float32), used, *cache[2:])
+    if fmt == kv_cache.MXFP4:  # few different values: one position ahead of the others
+        cache[0][used] &= 0xBB
+        cache[0][used[n // 2]] = np.where(scale > 0, 0x77, 0xFF)
+        cache[1][used] = 127
+    q = np.zeros((1, group, dim), dtype=np.float32)
+    for i in range(group):
+        q[0, i, 21 * i] = 1.25 * 2.0 ** size * (1 + i)
+    k, v = (kv_serve.values(fmt, *c)[used, 0].astype(np.float64) for c in (cache[:2], cache[2:]))
+    s = q[0].astype(np.float64) @ k.T * np.float32(scale)
+    top = s.argmax(1)
+    gap = np.sort(s, 1)[:, -1] - np.sort(s, 1)[:, -2]
+    assert (gap > 2.0 ** -18 * np.abs(s).max(1)).all() and (gap > 40).all()
+    outs = [whole(rz, fmt, cache, q, page, table, [n], scale)]
+    out, lse = run(rz, fmt, cache, dev(q), page, table, [n], scale)
+    assert (np.abs(host(lse)[0] - s.max(1)) <= 15 * 2.0 ** -24 * s.max(1)).all()
+    for x in (*outs, out):
+        x = host(x)[0].astype(np.float64)
+        assert np.isfinite(x).all()
+        assert (np.abs(x - v[top]) <= 16 * 2.0 ** -24 * np.abs(v[top]) + n * 2.0 ** -38 * np.abs(v).max()).all()
