@@ -632,8 +632,9 @@ def rz_kv_bounds(fmt: int, k_codes, k_scales, slots, page_len: int, bounds, boun
 
 def rz_kv_select(q, bounds, bound_scales, page_len: int, page_table, lens, budget: int, pages=None, stream=None):
     """The `budget` pages of each sequence and key head that may hold the
-    largest q . k by their bounds, the first and the last among them -> pages
-    int32 [seqs][heads][budget]: columns of page_table, ascending, then -1."""
+    largest q . k by their bounds, the first and the last always among them
+    (budget 1: the first) -> pages int32 [seqs][heads][budget]: columns of
+    page_table, ascending, then -1."""
     return _native().kv_select(q, bounds, bound_scales, page_len, page_table, lens, budget, pages, _handle(stream))
 
 

@@ -263,7 +263,8 @@ __device__ __forceinline__ uint32_t order_key(float s) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr uint32_t kForced = 0xFF800000u;  // that of +inf, the largest there is
+constexpr uint32_t kInfinite = 0xFF800000u;  // that of +inf, the largest score
+constexpr uint32_t kEnd = kInfinite + 1;     // a sequence's first and last page
 
 __device__ __forceinline__ uint32_t used_pages(const KvSelect& A, uint32_t b) {
     const int64_t len = A.lens[b] > 0 ? A.lens[b] : 0, n = (len + A.page_len - 1) / A.page_len;
@@ -376,7 +377,7 @@ __device__ __forceinline__ void score_pages(const KvSelect& A, Queries& Q, uint3
             const uint32_t page = p0 + n;
             if (p0 + T / kWave * 16u < last) next.load(A, b, h, page + T / kWave * 16u, last);
             uint32_t key = x.key(Q, rows);
-            if (page == 0 || page == used - 1) key = kForced;
+            if (page == 0 || page == used - 1) key = kEnd;
             if (x.id < 0) key = 0;
             if (lane < 16 && page < last) out[page - first] = q0 && out[page - first] > key ? out[page - first] : key;
             x = next;
@@ -393,7 +394,7 @@ constexpr uint32_t kBins = 2048;
 struct Pick {
     uint32_t count[kBins];
     uint32_t part[2][2][kPickWaves];
-    uint32_t bin, above, in, low, high, some, forced;
+    uint32_t bin, above, in, low, high, some, first;
 };
 
 // Sum of v over the wave's lanes up to and with this one.
@@ -424,8 +425,8 @@ __device__ __forceinline__ void wave_sums(const uint32_t* part, uint32_t& before
 // equal bins between the smallest and the largest key that can be it, then
 // between that bin's ends, and so on: two or three rounds, whose counts fall on
 // many bins (counts by a key's upper bits fall on a few, as scores are alike).
-// Infinite scores, the forced ones, are counted apart: they would stretch the
-// bins.  A wave has a run of 64 HELD places at most in its registers (HELD 0: of
+// A sequence's ends and infinite scores come first, and are counted apart: they
+// would stretch the bins.  A wave has a run of 64 HELD places at most in its registers (HELD 0: of
 // any length, where they lie).
 template <int HELD>
 __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, uint32_t budget, int32_t* out) {
@@ -448,19 +449,19 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
     for (uint32_t i = threadIdx.x; i < kBins; i += kPick) P.count[i] = 0;
     if (threadIdx.x == 0) {
         P.low = 0xFFFFFFFFu;
-        P.high = P.some = P.forced = 0;
+        P.high = P.some = P.first = 0;
     }
     __syncthreads();
-    // key - 1 and key + 2^23 put those that cannot be taken behind the smallest, the forced ones before the largest
-    static_assert((uint32_t)(kForced + 0x00800000u) == 0u);
-    uint32_t low = 0xFFFFFFFFu, high = 0, some = 0, forced = 0;  // the counts are the wave's
+    // key - 1 and key + 2^23 put those that cannot be taken behind the smallest, the first ones before the largest
+    static_assert((uint32_t)(kInfinite + 0x00800000u) == 0u);
+    uint32_t low = 0xFFFFFFFFu, high = 0, some = 0, first_ones = 0;  // the counts are the wave's
     each([&](uint32_t, uint32_t k) {
-        forced += (uint32_t)__popcll(__ballot(k == kForced));
+        first_ones += (uint32_t)__popcll(__ballot(k >= kInfinite));
         some += (uint32_t)__popcll(__ballot(k != 0));
         low = k - 1u < low ? k - 1u : low;
         high = k + 0x00800000u > high ? k + 0x00800000u : high;
     });
-    some -= forced;
+    some -= first_ones;
     high = across<1, kWave>(high, greater);
     low = ~across<1, kWave>(~low, greater);
     if (lane == 0) {
@@ -469,17 +470,18 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
             atomicMax(&P.high, high - 0x00800000u);
             atomicAdd(&P.some, some);
         }
-        if (forced) atomicAdd(&P.forced, forced);
+        if (first_ones) atomicAdd(&P.first, first_ones);
     }
     __syncthreads();
     low = P.low;
     high = P.high;
-    const uint32_t total = P.some, always = P.forced;
+    const uint32_t total = P.some, always = P.first;
     // the threshold: every key above it is taken, and `left` of those equal to it
     uint32_t threshold = 0, left = 0;
     if (always >= budget) {
-        threshold = kForced;
-        left = budget;
+        const uint32_t ends = (keys[0] == kEnd) + (n > 1 && keys[n - 1] == kEnd);  // always > 0: there is a page
+        threshold = ends < budget ? kInfinite : kEnd;
+        left = ends < budget ? budget - ends : budget;
     } else if (total > budget - always) {
         left = budget - always;
         for (uint32_t round = 0;; ++round) {

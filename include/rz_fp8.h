@@ -700,8 +700,9 @@ int rz_kv_bounds(int format, const uint8_t* k_codes, const void* k_scales, uint6
  * score is the largest over the group's queries of
  *   RN(RN(sum_d max(n_d hi_d, n_d lo_d) * bound_scale) * qs)
  * (the sum is exact; NaN counts as +inf): to rounding, an upper bound of the
- * page's q . k.  The first and the last of a sequence's pages score +inf.
- * Ties go to the lower page.  A page outside the cache is never taken.
+ * page's q . k.  The first and the last of a sequence's pages come before all
+ * others, whatever those score (budget 1: the first alone, without the newest
+ * tokens).  Ties go to the lower page.  A page outside the cache is never taken.
  * Refused beside the cache's limits: budget 0 or past 2^31 - 1.
  * seqs == 0 is a no-op.
  */

@@ -185,7 +185,7 @@ def select(q, codes, scales, page_len, table, lens, budget):
         for h in range(heads if len(cols) else 0):
             at = table[b, cols]
             s = scores(q[b, h * group:(h + 1) * group], codes[at, h], scales[at, h])
-            s[(cols == 0) | (cols == n - 1)] = np.inf
-            take = sorted(cols[np.argsort(-s, kind="stable")[:budget]])
+            ends = (cols == 0) | (cols == n - 1)
+            take = sorted(cols[np.lexsort((cols, np.where(ends, 0, -s), ~ends))[:budget]])
             out[b, h, :len(take)] = take
     return out

@@ -240,6 +240,25 @@ def test_select_special(rz):
     assert (host(got) == -1).all()
 
 
+@pytest.mark.parametrize("page,lens", [(4, [64, 61, 4, 5, 0, 33]), (1, [700, 512, 2]), (2, [9000, 1])])
+@pytest.mark.parametrize("budget", [1, 2, 3, 7, 40])
+def test_select_keeps_the_newest_page(rz, page, lens, budget):
+    """A sequence's first and last page among pages whose keys hold a NaN, as many as the budget and more."""
+    heads, group, dim = 2, 3, 64
+    table, _, slots = paged(page, lens, 55)
+    codes, scales = ranked(slots // page, heads, dim, 56)
+    scales[W.rng(57).random(scales.shape) < 0.6] = np.inf
+    q = W.act_normal(58, len(lens), heads * group * dim).reshape(len(lens), heads * group, dim)
+    got = host(rz.rz_kv_select(dev(q), dev(codes), dev(scales), page, dev(table), dev(i32(lens)), budget))
+    assert np.array_equal(got, kv_serve.select(q, codes, scales, page, table, lens, budget))
+    for b, n in enumerate(lens):
+        used = -(-n // page)
+        for row in got[b]:
+            taken = set(row[row >= 0].tolist())
+            assert len(taken) == min(used, budget)
+            assert ({0, used - 1} if budget > 1 else {0}) <= taken if used else not taken
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_caches_of_nothing(rz, fmt):
     """A cache without slots, bounds of no pages, steps of no tokens, batches of no sequences."""

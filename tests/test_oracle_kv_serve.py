@@ -75,6 +75,18 @@ def test_bounds_by_hand():
     assert not codes[0].any() and scales[0, 0] == np.float32(1) / np.float32(127)
 
 
+def test_select_keeps_the_newest_page():
+    """Pages of infinite bounds come behind the first and the last page, whatever their number."""
+    codes, scales = np.ones((6, 1, 2, 32), dtype=np.int8), np.ones((6, 1), dtype=np.float32)
+    scales[1:5] = np.inf
+    q, table = np.ones((1, 1, 32), dtype=np.float32), np.array([[0, 1, 2, 3, 4, 5]], dtype=np.int32)
+    pick = lambda n, budget: kv_serve.select(q, codes, scales, 4, table, [n], budget)[0, 0].tolist()  # noqa: E731
+    assert pick(24, 2) == [0, 5] and pick(24, 3) == [0, 1, 5] and pick(24, 5) == [0, 1, 2, 3, 5] and pick(24, 1) == [0]
+    assert pick(13, 2) == [0, 3]
+    scales[5] = 2.0
+    assert pick(24, 1) == [0]  # of the two the lower, whatever they score
+
+
 def test_bounds_hold():
     """hi * scale and lo * scale enclose the values to the scale's rounding, and a score is at least every n . k."""
     r = np.random.default_rng(2)
