@@ -88,14 +88,15 @@ struct Step {
     int32_t len = 0;
     int64_t first = 0, then = 0;  // tokens kept, and with the new ones
     uint32_t held = 0, need = 0;
-    bool ok = false;
+    bool ok = false, falls = false;  // falls: its offsets decrease
     __device__ __forceinline__ Step(const KvPlan& A, uint32_t b) {
         if (b >= A.seqs) return;
         len = A.lens[b];
         first = A.keep ? A.keep[b] : len;
         const int64_t fresh = (int64_t)A.offsets[b + 1] - A.offsets[b];
         then = first + fresh;
-        ok = first >= 0 && first <= len && fresh >= 0 && then <= INT32_MAX;
+        falls = fresh < 0;
+        ok = first >= 0 && first <= len && !falls && then <= INT32_MAX;
         held = ok ? ((uint32_t)len + (A.page_len - 1ull)) / A.page_len : 0;
         need = ok ? ((uint32_t)then + (A.page_len - 1ull)) / A.page_len : 0;
         ok = ok && held <= A.max_pages && need <= A.max_pages;
@@ -118,13 +119,13 @@ __device__ __forceinline__ uint32_t sequence_of(const int32_t* offsets, uint32_t
 __device__ __forceinline__ int64_t slot_of(const KvPlan& A, const Row& row, uint32_t b, uint32_t t, int32_t offset) {
     if (row.first < 0) return -1;
     const uint64_t pos = (uint64_t)(uint32_t)row.first + (t - (uint32_t)offset), page = pos / A.page_len;
-    if (page >= A.max_pages) return -1;  // offsets that decrease
+    if (page >= A.max_pages) return -1;  // a write stays in the row, and a read in the stack, whatever the lengths say
     const uint32_t at = (uint32_t)(pos - page * A.page_len);
     int32_t* entry = A.page_table + (uint64_t)b * A.max_pages + page;
     int64_t id;
     if (page >= row.held) {
         const uint64_t below = page - row.held;
-        if (below > row.top || row.top - below >= A.num_pages) return -1;  // offsets that decrease
+        if (below > row.top || row.top - below >= A.num_pages) return -1;
         id = A.free_pages[row.top - below];
         if (at == 0) *entry = (int32_t)id;
     } else {
@@ -151,6 +152,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
     __shared__ Row row_of[kThreads];
     __shared__ int32_t offset_of[kThreads + 1];
     __shared__ uint32_t sums[kThreads], need_of[kThreads];
+    __shared__ bool falls_of;
     const int lane = threadIdx.x & (kWave - 1);
     const uint32_t rounds = (A.seqs + kThreads - 1) / kThreads;
     const bool few = rounds <= 1;
@@ -164,19 +166,30 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
     const bool fill = A.seqs != 0 && (A.offsets[A.seqs] > (int64_t)A.tokens || A.offsets[0] < 0);
     uint32_t before_take = 0, taken = 0;
     if (few) {
-        const uint32_t give = step.give();
-        const Scan s = scan(give, step.take(), smem);
+        // offsets that decrease leave no sequence its tokens: a sum at its limit, which no cache's pages reach, says so
+        const Scan s = scan(step.falls ? ~0u : step.give(), step.take(), smem);
+        const uint32_t given = s.all[0] == ~0u ? 0 : s.all[0];
+        step.ok = step.ok && s.all[0] != ~0u;
         before_take = s.before[1];
         sums[threadIdx.x] = s.before[0];
         need_of[threadIdx.x] = step.need;
         __syncthreads();
-        for (uint32_t i = threadIdx.x; i < s.all[0] && add(have, i) < A.num_pages; i += kThreads) {
+        for (uint32_t i = threadIdx.x; i < given && add(have, i) < A.num_pages; i += kThreads) {
             const uint32_t b = row_of_place(sums, A.seqs, i);
             A.free_pages[have + i] = A.page_table[(uint64_t)b * A.max_pages + need_of[b] + (i - sums[b])];
         }
-        have = add(have, s.all[0]);
+        have = add(have, given);
     }
-    for (uint32_t r = 0; r < rounds && !few; ++r) {
+    bool falls = false;
+    if (!few) {
+        if (threadIdx.x == 0) falls_of = false;
+        __syncthreads();
+        for (uint32_t b = threadIdx.x; b < A.seqs; b += kThreads)
+            if (A.offsets[b + 1] < A.offsets[b]) falls_of = true;
+        __syncthreads();
+        falls = falls_of;
+    }
+    for (uint32_t r = 0; r < rounds && !few && !falls; ++r) {
         step = Step(A, r * kThreads + threadIdx.x);
         const uint32_t give = step.give(), wave0 = (r * kThreads + threadIdx.x) & ~(kWave - 1u);
         const Scan s = scan(give, 0, smem);
@@ -194,6 +207,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvPlan A, Row* rows, boo
         const uint32_t b = r * kThreads + threadIdx.x, wave0 = b & ~(kWave - 1u);
         if (!few) {
             step = Step(A, b);
+            step.ok = step.ok && !falls;
             const Scan s = scan(step.take(), 0, smem);
             before_take = add(taken, s.before[0]);
             taken = add(taken, s.all[0]);

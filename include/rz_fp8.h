@@ -604,15 +604,16 @@ int rz_kv_cache_read(int format, const uint8_t* k_codes, const void* k_scales, c
  * First the pages that keep + new tokens no longer need go onto the stack, in
  * order of sequence and page; then the pages that are lacking are taken from
  * its top, in the same order.  A sequence is refused where keep is not in
- * [0, lens], where new is negative, where lens or keep + new needs more than
- * max_pages, and, if it lacks pages, from the first sequence on that the stack
- * cannot serve: it gives and takes nothing, lens_out is its lens, and its
- * tokens get -1.  Tokens of no sequence get -1 too; new ones outside
- * [0, tokens) count and have pages, but no slot here.  Entries of page_table
- * behind a sequence's pages are left as they are, and so is the stack above
- * its largest height of the call.  lens_out may be lens or keep, count_out
- * free_count; no other output may overlap an input.  With outputs of its own
- * the same call gives the same again.  seqs == 0 gives every token -1.
+ * [0, lens], where lens or keep + new needs more than max_pages, where keep +
+ * new passes 2^31 - 1, and, if it lacks pages, from the first sequence on that
+ * the stack cannot serve: it gives and takes nothing, lens_out is its lens, and
+ * its tokens get -1.  Where offsets decrease anywhere, every sequence is.
+ * Tokens of no sequence get -1 too; new ones outside [0, tokens) count and have
+ * pages, but no slot here.  Entries of page_table behind a sequence's pages are
+ * left as they are, and so is the stack above its largest height of the call.
+ * lens_out may be lens or keep, count_out free_count; no other output may
+ * overlap an input.  With outputs of its own the same call gives the same
+ * again.  seqs == 0 gives every token -1.
  */
 size_t rz_kv_plan_workspace_bytes(uint32_t seqs, uint32_t tokens);
 int rz_kv_plan(const int32_t* lens, const int32_t* keep, const int32_t* offsets, uint32_t seqs, uint32_t tokens,

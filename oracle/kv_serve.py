@@ -20,12 +20,12 @@ TINY = np.float32(2.0 ** -100)
 def plan(lens, keep, offsets, tokens, page_len, table, free, count):
     """(slots, lens_out, count_out); table and free are updated in place."""
     seqs, width = table.shape
-    stack = [int(x) for x in free[:count]]
+    stack, falls = [int(x) for x in free[:count]], any(offsets[b + 1] < offsets[b] for b in range(seqs))
     rows = []
     for b in range(seqs):
         new = int(offsets[b + 1]) - int(offsets[b])
         held, need = -(-int(lens[b]) // page_len), -(-(int(keep[b]) + new) // page_len)
-        ok = 0 <= keep[b] <= lens[b] and new >= 0 and held <= width and need <= width
+        ok = 0 <= keep[b] <= lens[b] and not falls and held <= width and need <= width and int(keep[b]) + new < 2 ** 31
         rows.append((ok, held, need, new))
         if ok:
             stack += [int(x) for x in table[b, need:held]]

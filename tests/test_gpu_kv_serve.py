@@ -95,6 +95,19 @@ def test_plan_tokens_left_out(rz, tokens):
     check_plan(rz, 4, lens, lens, i32([-9, 6, 11, tokens + 30]), tokens, table, free, 1980)
 
 
+@pytest.mark.parametrize("seqs,new", [(3, 9), (90, 8), (1024, 40), (1025, 3), (2500, 9)])
+def test_plan_of_decreasing_offsets(rz, seqs, new):
+    """Offsets that decrease once, anywhere, and by as little as one: every sequence stays as it is."""
+    for seed, at in enumerate((0, seqs // 2, seqs - 1)):
+        lens, keep, offsets, tokens, table, free, count = planned(seqs, 4, 30, new, seed)
+        offsets = offsets.copy()
+        offsets[at + 1:] += offsets[at] - 1 - offsets[at + 1]
+        for n in (max(0, int(offsets.max())), tokens):  # all of the tokens, and more than the offsets name
+            check_plan(rz, 4, lens, keep, offsets, n, table, free, count)
+        slots, then, left = rz.rz_kv_plan(dev(lens), dev(offsets), tokens, 4, dev(table), dev(free), dev(i32([count])), keep=dev(keep))
+        assert (host(slots) == -1).all() and np.array_equal(host(then), lens) and host(left).tolist() == [count]
+
+
 def test_plan_tokens_of_no_sequence(rz):
     """Tokens before the first and behind the last sequence, more tokens than the offsets name, no sequence at all."""
     lens, table, free = i32([3, 0]), i32([[2, -1], [-1, -1]]), i32([5, 4, 1])

@@ -31,6 +31,15 @@ def test_plan_refusals_by_hand():
     assert lens.tolist() == [0] and (slots == -1).all()  # five pages, four columns
 
 
+def test_plan_of_decreasing_offsets_by_hand():
+    """Which tokens are whose is not known: no sequence gets any, and no page moves."""
+    table = np.array([[7, 2, -1], [3, -1, -1], [-1, -1, -1]], dtype=np.int32)
+    free, before = np.array([1, 6, 0, 9], dtype=np.int32), table.copy()
+    slots, lens, count = kv_serve.plan([5, 4, 0], [1, 4, 0], [0, 4, 3, 8], 8, 4, table, free, 3)
+    assert (slots == -1).all() and lens.tolist() == [5, 4, 0] and count.tolist() == [3]
+    assert np.array_equal(table, before) and free.tolist() == [1, 6, 0, 9]
+
+
 def test_slots_of_by_hand():
     table = np.array([[2, -1, 9, 0]], dtype=np.int32)
     assert kv_serve.slots_of(0, 0, 7, 2, table, 8) == [4, 5, 0]  # page 1 names nothing, page 2 lies outside
