@@ -48,6 +48,7 @@
 
 #include <type_traits>
 
+#include "kv_steps.h"
 #include "mx_device.h"
 #include "rz_device.h"
 #include "rz_internal.h"
@@ -1064,16 +1065,6 @@ uint32_t part_rows(uint32_t q_heads, uint32_t heads) {
     return group < kHeads ? group : kHeads;
 }
 
-template <typename F>
-void with_steps(uint32_t c, F&& f) {
-    switch (c) {
-#define RZ_C(n) case n: f(std::integral_constant<int, n>{}); break;
-        RZ_C(1) RZ_C(2) RZ_C(3) RZ_C(4) RZ_C(5) RZ_C(6) RZ_C(7) RZ_C(8)
-        RZ_C(9) RZ_C(10) RZ_C(11) RZ_C(12) RZ_C(13) RZ_C(14) RZ_C(15) RZ_C(16)
-#undef RZ_C
-    }
-}
-
 // Workers a key head and 16 queries of it.
 uint32_t split(uint32_t q_heads, uint32_t heads, int cus) {
     const uint32_t lanes = heads * ((q_heads / heads + kHeads - 1) / kHeads);
@@ -1114,7 +1105,7 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
     }
     G.near = G.R >= 8u;
     const uint32_t grid = (G.near ? (G.R + 7u) / 8u * 8u : G.R) * lanes;
-    with_steps(A.dim / 32u, [&](auto c_) {
+    const bool known = with_steps(A.dim / 32u, [&](auto c_) {
         constexpr int C = decltype(c_)::value;
         auto launch = [&](auto pack_) {
             constexpr bool PACK = decltype(pack_)::value;
@@ -1128,6 +1119,7 @@ hipError_t launch_kv_attend(int format, const KvAttend& A, int dtype, int cus, h
         else
             launch(std::false_type{});
     });
+    if (!known) return hipErrorInvalidValue;
     if (!G.whole) {
         const uint32_t jobs = A.seqs * A.q_heads * (A.dim / 32u);
         if (A.seqs < 8u && jobs <= 0x10000u)  // lanes of a launch are counted in 32 bits

@@ -19,6 +19,7 @@
 
 #include <type_traits>
 
+#include "kv_steps.h"
 #include "mx_device.h"
 #include "rz_device.h"
 #include "rz_internal.h"
@@ -586,16 +587,6 @@ __global__ __launch_bounds__(kPick) void pick_kernel(KvSelect A, const uint32_t*
     pick<HELD>(P, keys + (uint64_t)blockIdx.x * A.max_pages, used, A.budget, A.pages + (uint64_t)blockIdx.x * A.budget);
 }
 
-template <typename F>
-void with_steps(uint32_t c, F&& f) {
-    switch (c) {
-#define RZ_C(n) case n: f(std::integral_constant<int, n>{}); break;
-        RZ_C(1) RZ_C(2) RZ_C(3) RZ_C(4) RZ_C(5) RZ_C(6) RZ_C(7) RZ_C(8)
-        RZ_C(9) RZ_C(10) RZ_C(11) RZ_C(12) RZ_C(13) RZ_C(14) RZ_C(15) RZ_C(16)
-#undef RZ_C
-    }
-}
-
 // Scoring workgroups are more only where a tile a wave is not: each holds the queries once (2048 instead: 25.6 and 23.4 us).
 constexpr uint32_t kScorers = 1024;
 
@@ -644,7 +635,7 @@ size_t kv_select_ws_bytes(uint32_t seqs, uint32_t heads, uint32_t max_pages) {
 
 hipError_t launch_kv_select(const KvSelect& A, hipStream_t st) {
     const uint32_t pairs = A.seqs * A.heads;
-    with_steps(A.dim / 32u, [&](auto c_) {
+    const bool known = with_steps(A.dim / 32u, [&](auto c_) {
         constexpr int C = decltype(c_)::value;
         if (one_launch(A.max_pages)) {
             select_kernel<C><<<pairs, kPick, 0, st>>>(A);
@@ -662,6 +653,7 @@ hipError_t launch_kv_select(const KvSelect& A, hipStream_t st) {
         else
             pick_kernel<0><<<pairs, kPick, 0, st>>>(A, keys);
     });
+    if (!known) return hipErrorInvalidValue;
     return hipGetLastError();
 }
 
