@@ -623,8 +623,8 @@ def rz_kv_attention(fmt: int, q, k_codes, k_scales, v_codes, v_scales, page_len:
 
 def rz_kv_bounds(fmt: int, k_codes, k_scales, slots, page_len: int, bounds, bound_scales, stream=None):
     """Bounds of the keys in the pages that `slots` names (int64 [tokens], as
-    just written; tokens of a page together and ascending), a page counting up
-    to its last named slot: bounds int8 [slots // page_len][heads][2][dim]
+    just written; tokens of a page next to each other and ascending), a page
+    counting up to its last named slot: bounds int8 [slots // page_len][heads][2][dim]
     (largest, smallest) times bound_scales fp32 [slots // page_len][heads],
     both updated."""
     _native().kv_bounds(fmt, k_codes, k_scales, slots, page_len, bounds, bound_scales, _handle(stream))

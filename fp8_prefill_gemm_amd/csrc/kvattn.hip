@@ -37,12 +37,18 @@
 // goes to the workspace, and a second launch joins it.
 //
 // Measured (4 key heads of 128 columns, 7 queries each; MXFP4 8): 131072
-// positions of one sequence E4M3 34.7 us, 4.0 TB/s of its rows, the loop itself
-// at 7 TB/s; 64 sequences of 65536 in all 20.7; 24 sequences of 131072 in all
-// MXFP4 24.6, 2.9 TB/s.  E4M3 is bound by memory in the loop and by what comes
+// positions of one sequence E4M3 34.4 us, 4.0 TB/s of its rows, the loop itself
+// at 7 TB/s; 64 sequences of 65536 in all 20.9; 24 sequences of 131072 in all
+// MXFP4 24.3, 2.9 TB/s.  E4M3 is bound by memory in the loop and by what comes
 // before and after it (lengths, tables, rows and scales are loads that wait for
 // each other, 6 us; the join's launch, 4), MXFP4 by its vector instructions
-// (about 245 a wave and 32 positions, half of them to widen codes).
+// (about 245 a wave and 32 positions, half of them to widen codes).  Wider rows
+// are bound by registers: 131072 positions of 128 columns, and fewer of more, of
+// one sequence and with the join take E4M3 at 128, 192, 256, 384 and 512 columns
+// 39, 46, 46, 51 and 89 us (memory: 28), MXFP4 26, 41, 38, 47 and 52 (15).  Beyond
+// 128 columns (MXFP4: 160) a compute unit holds one workgroup of the two that a
+// launch has for it, so the chain before the loop is paid twice, and from 416 on
+// E4M3 keeps 130 to 480 bytes a lane of its two tiles of rows in memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -86,7 +92,8 @@ struct Grid {
     uint64_t info;       // floats before the workspace's record of who holds which sequence
 };
 
-// Positions that sequence b attends (those of a choice may hold gaps).
+// Positions that sequence b attends (those of a choice may hold gaps, and count as many as the budget has: units are cut by
+// these, so a short sequence's choice is shared out, and staged, like a full one).
 __device__ __forceinline__ uint32_t length_of(const KvAttend& A, const Grid& G, uint32_t b) {
     const int32_t len = A.lens[b];
     if (len <= 0 || A.num_slots == 0) return 0;
@@ -131,9 +138,12 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 // first loads, the join of its waves), so a worker should have one, or where
 // there are many sequences two: `per` is the least that makes R units (2 R
 // where more than R / 2 sequences have something), found by halving where one
-// look holds all sequences, and bounded by T / (2 R - S) otherwise.  (A run of
-// equal length for each worker instead, cut where sequences end, took 37 us on
-// 64 sequences of 65536 positions: two or three pieces for the last worker.)
+// look holds all sequences, and bounded by T / (2 R - S) otherwise.  That bound
+// goes to T as S nears 2 R, so just below that many sequences a long one among
+// short ones stays whole (4 key heads, R = 128, one of 131072 positions among
+// ones of 100: 200 sequences 58 us, 250 334, 255 1576, 256 58).  (A run of equal
+// length for each worker instead, cut where sequences end, took 37 us on 64
+// sequences of 65536 positions: two or three pieces for the last worker.)
 struct Batch {
     uint32_t per = 1, units = 0;
     uint32_t b0 = 0;                      // the 64 that the lanes' values are of
@@ -1057,7 +1067,7 @@ __global__ __launch_bounds__(kWays == 1 ? kThreads : kWays* kWave) void join_ker
     if (A.lse && lane == 0 && run == 0) A.lse[head] = lse_of(x.m, x.l);
 }
 
-// Workgroups of a launch: two a compute unit.
+// Workgroups of a launch: two a compute unit, which is what it holds up to 128 columns (MXFP4 160), and one at a time beyond.
 uint32_t workers(int cus) { return 2u * (uint32_t)cus; }
 
 uint32_t part_rows(uint32_t q_heads, uint32_t heads) {

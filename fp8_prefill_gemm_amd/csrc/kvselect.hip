@@ -12,8 +12,9 @@
 // Few bytes are moved for each launch, so latency counts: the loads that wait for
 // each other (slots, rows; lengths, tables, bounds; keys) and the barriers of
 // the choice.  4 key heads of 128 columns: bounds of 64 pages of 64 rows 6.2 us, of a
-// 32768-token prompt 8.7 (1.2 TB/s); scores of 8192 pages of 32 sequences 7.4
-// and their choice 6.4; of 8192 pages of one 5.9 and 9.0.
+// 32768-token prompt 8.6 (1.2 TB/s); scores of 8192 pages of 32 sequences 7.5
+// and their choice 6.0; of 8192 pages of one 5.8 and 8.9, the choice on as many
+// compute units as there are key heads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -555,7 +556,9 @@ __device__ __forceinline__ void pick(Pick& P, const uint32_t* keys, uint32_t n, 
 }
 
 // Few pages a sequence: a workgroup scores all pages of its (sequence, key
-// head) into its LDS and picks from there.
+// head) into its LDS and picks from there.  Its 1024 lanes have 128 registers
+// each: from 288 columns on the next tile's bounds do not fit beside this one's
+// (60 to 428 bytes a lane in memory).
 constexpr uint32_t kOnePages = 512;
 template <int C>
 __global__ __launch_bounds__(kPick) void select_kernel(KvSelect A) {
@@ -600,7 +603,7 @@ bool one_launch(uint32_t max_pages) { return max_pages <= kOnePages; }
 hipError_t launch_kv_bounds(int format, const KvBounds& A, hipStream_t st) {
     const uint32_t lanes = A.dim <= 64 ? 8 : A.dim <= 128 ? 16 : A.dim <= 256 ? 32 : 64;
     // up to 2048 (token, head) pairs a workgroup each; more: as many tokens a workgroup as 1024 of them need, as each costs its
-    // launch (32768 tokens, us: 8 a workgroup 25, 16 16, 32 12.8, 64 14; and 11.7 with 4 rows a lane in flight instead of 8)
+    // launch (32768 tokens, us: 8 a workgroup 15.4, 16 11.5, 32 8.6, 64 10.6; with 8 rows a lane in flight instead of 4 9.3)
     const bool step = (uint64_t)A.tokens * A.heads <= 2048u;
     const uint32_t per = A.tokens / 1024u < 1u ? 1u : A.tokens / 1024u < 64u ? A.tokens / 1024u : 64u;
     const uint32_t grid = step ? A.tokens * A.heads : (A.tokens + per - 1) / per;

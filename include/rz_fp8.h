@@ -668,7 +668,9 @@ int rz_kv_attention(int format, const float* q, uint32_t q_heads, uint64_t q_str
  * Bounds of the keys in the pages that `slots` names, for rz_kv_select; call
  * it after rz_kv_cache_write with the same slots.
  *   slots         device, int64 [tokens]; negative or >= num_slots: no token.
- *                 Tokens of one page stand together, in ascending order
+ *                 Tokens of one page stand next to each other, in
+ *                 ascending order; where something stands between them, even
+ *                 a slot that is none, the page's bounds may be of either part
  *   bounds        device, int8 [num_slots / page_len][heads][2][dim], updated
  *   bound_scales  device, fp32 [num_slots / page_len][heads], updated
  * A page counts as filled up to the last of its slots that is named.  With hi
@@ -704,6 +706,8 @@ int rz_kv_bounds(int format, const uint8_t* k_codes, const void* k_scales, uint6
  * page's q . k.  The first and the last of a sequence's pages come before all
  * others, whatever those score (budget 1: the first alone, without the newest
  * tokens).  Ties go to the lower page.  A page outside the cache is never taken.
+ * For an attention with a negative scale pass -q: its largest scores are the
+ * smallest q . k.
  * Refused beside the cache's limits: budget 0 or past 2^31 - 1.
  * seqs == 0 is a no-op.
  */
